@@ -478,6 +478,191 @@ PKV_API pkv_status pkv_vtoken_plan(const int32_t* token_slots, int MT, const int
                                    int32_t* freed, int64_t max_freed, int64_t* num_freed);
 
 /* ------------------------------------------------------------------------
+ * Sliding window with sinks.
+ *
+ * Source: "LLM推論の「見えないメモリ問題」を解く … vToken", section on token
+ * eviction: keeping the first tokens and a window of recent ones bounds what
+ * a decoding step reads.
+ *
+ * A query at position p sees token t when t <= p and (t < num_sinks or
+ * t > p - window): the first num_sinks tokens of its sequence and the last
+ * `window` tokens, its own among them.  window >= 1, num_sinks >= 0; a
+ * window or sinks beyond a sequence's length hide nothing.  Blocks none of
+ * whose tokens a call's queries see are not read, and neither are their
+ * entries of the block table: they may have been freed or reused.  Tokens of
+ * a read block that no query sees may hold anything, NaN included.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Bytes of workspace for pkv_paged_attention_decode_window, and (window 0:
+ * no window) for pkv_paged_attention_decode_kv4; 0 for invalid arguments.
+ * It is used as pkv_decode_workspace_size describes, and holds partial
+ * results for the tokens a window leaves visible only.
+ */
+PKV_API size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_context_len, int window,
+                                                int num_sinks, int partition_size);
+
+/*
+ * paged_attention_decode_window -- pkv_paged_attention_decode_ex over the
+ * visible tokens only (the sequence's query is at context_lens[s] - 1).
+ * Every dtype, size, kernel choice and status of that call; partitions
+ * divide the visible tokens.
+ */
+PKV_API pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_dtype q_dtype,
+                                                     const void* key_cache, const void* value_cache,
+                                                     pkv_dtype cache_dtype,
+                                                     const int32_t* block_tables, int MB,
+                                                     const int32_t* context_lens, int S, int max_context_len,
+                                                     int Hq, int Hkv, int d, int bs, int NB,
+                                                     float scale, float k_scale, float v_scale,
+                                                     int window, int num_sinks, int partition_size,
+                                                     void* workspace, size_t workspace_bytes,
+                                                     int32_t* err_word, pkv_stream_t stream, int kernel);
+
+/*
+ * paged_attention_prefill_window -- pkv_paged_attention_prefill with each
+ * query of the chunk under its own window.  The workspace is
+ * pkv_prefill_window_workspace_size(...) bytes.  A K or V value that is not
+ * finite, in a token that some query of the chunk sees, may reach other
+ * queries of the same chunk (their weight 0 times it).
+ */
+PKV_API size_t pkv_prefill_window_workspace_size(int S, int num_query_tokens, int max_query_len, int Hq, int Hkv, int d,
+                                                 int bs, int max_context_len, int window, int num_sinks,
+                                                 int partition_size);
+PKV_API pkv_status pkv_paged_attention_prefill_window(void* out, const void* query, pkv_dtype q_dtype,
+                                                      const void* key_cache, const void* value_cache,
+                                                      pkv_dtype cache_dtype,
+                                                      const int32_t* block_tables, int MB,
+                                                      const int32_t* context_lens, const int32_t* query_start,
+                                                      int S, int num_query_tokens, int max_query_len,
+                                                      int max_context_len, int Hq, int Hkv, int d, int bs, int NB,
+                                                      float scale, int window, int num_sinks, int partition_size,
+                                                      void* workspace, size_t workspace_bytes,
+                                                      int32_t* err_word, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A cache held in 4 bits.
+ *
+ * Source: "LLM推論の基礎とvLLMの内部", section 2: the bytes per K/V element
+ * set how many tokens a pool holds; 4-bit codes with a scale and a zero per
+ * 32 values take 5 bits a value (bf16: 16, E4M3: 8).
+ *
+ * key_cache / value_cache are byte arrays [NB, Hkv, bs * (d/2 + d/8)]: each
+ * K/V head of a block holds its tokens' codes, then their fp16 scales, then
+ * their fp16 zeros.  A row of d values x becomes y = x / k_scale (v_scale),
+ * one IEEE fp32 divide, clamped to +-65504, and each group of 32 of them
+ *   zero  = fp16(min y)
+ *   scale = fp16(max(max y - zero, 0) / 15)
+ *   code  = clamp(rint((y - zero) / scale), 0, 15), 0 where scale is 0
+ * in fp32 with rounding to nearest even; the code stands for
+ * (zero + scale * code) * k_scale.  A NaN in a group makes all of it NaN.
+ * The tensor scales bring values into fp16's range; 1 suits values between
+ * about 1e-3 and 1e4.  With G = d / 32, element e of token t of the block
+ * is code c of the 32-bit word w of that head (code c in bits 4c .. 4c + 3):
+ *   K: w = (4 t + e % 32 / 8) G + e / 32,              c = e % 8
+ *   V: w = ((t / 8 * 8 + e % 32 / 4) 4 + t / 2 % 4) G + e / 32,
+ *                                                      c = 4 (t % 2) + e % 4
+ * and its scale (zero) is the half number, past the codes (and the scales),
+ *   K: t G + e / 32          V: (t / 2 G + e / 32) 2 + t % 2
+ * (integer divisions).  d in {64, 128}; bs in {16, 32}.  pkv_copy_blocks
+ * copies such blocks with block_bytes = pkv_kv4_block_bytes(...).
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of one block of a 4-bit K (or V) cache; 0 for unsupported sizes. */
+PKV_API size_t pkv_kv4_block_bytes(int bs, int Hkv, int d);
+
+/*
+ * paged_kv4_write -- pkv_paged_kv_write into a 4-bit cache: key/value
+ * [T, Hkv, d] (F32 or BF16), slot_mapping [T] as there.
+ */
+PKV_API pkv_status pkv_paged_kv4_write(const void* key, const void* value, pkv_dtype in_dtype,
+                                       void* key_cache, void* value_cache, const int64_t* slot_mapping, int T,
+                                       int NB, int bs, int Hkv, int d, float k_scale, float v_scale,
+                                       int32_t* err_word, pkv_stream_t stream);
+
+/*
+ * paged_kv4_read -- the values of the slots: key/value [T, Hkv, d] (F32, or
+ * BF16 rounded to nearest even) of slots[i] (int64 [T]; a negative slot
+ * leaves row i as it was, one outside the pool too and is reported), to move
+ * a sequence to a cache of another dtype or to recompute with.
+ */
+PKV_API pkv_status pkv_paged_kv4_read(void* key, void* value, pkv_dtype out_dtype,
+                                      const void* key_cache, const void* value_cache, const int64_t* slots, int T,
+                                      int NB, int bs, int Hkv, int d, float k_scale, float v_scale,
+                                      int32_t* err_word, pkv_stream_t stream);
+
+/*
+ * paged_attention_decode_kv4 -- pkv_paged_attention_decode over a 4-bit
+ * cache, under a sliding window when window > 0 (0: every token).  bf16
+ * query and output (anything else returns PKV_ERR_UNSUPPORTED).  The query
+ * is rounded to fp16 after a factor of 4 for the products: |query| must stay
+ * below 16376.  Workspace: pkv_decode_window_workspace_size(...) with the
+ * same window and sinks.
+ */
+PKV_API pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtype q_dtype,
+                                                  const void* key_cache, const void* value_cache,
+                                                  const int32_t* block_tables, int MB,
+                                                  const int32_t* context_lens, int S, int max_context_len,
+                                                  int Hq, int Hkv, int d, int bs, int NB,
+                                                  float scale, float k_scale, float v_scale,
+                                                  int window, int num_sinks, int partition_size,
+                                                  void* workspace, size_t workspace_bytes,
+                                                  int32_t* err_word, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight.
+ *
+ * Source: "LLM推論の「見えないメモリ問題」を解く … vToken", section on token
+ * eviction: policies that drop the tokens that received little attention
+ * free slots inside blocks, which the token tables and pkv_repack_tokens
+ * turn into free blocks.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * token_attention_decode_scored -- pkv_token_attention_decode (the same
+ * output, bit for bit) that also adds, to scores[s][t] (fp32 [S, MT],
+ * row length MT as the table's) of every live token t, the attention weights
+ * the sequence's query gives it, summed over the Hq query heads.  The sum
+ * runs in a fixed order, so equal calls give equal bits; entries past
+ * num_tokens[s] are left as they were, and a slot outside the pool gets
+ * weight 0.  `workspace` must hold
+ * pkv_token_attention_scored_workspace_size(...) bytes: the decode's, and
+ * the logits of the step (about 4 bytes per token and query head).  Its
+ * header must be zero before first use, as the decode's.
+ */
+PKV_API size_t pkv_token_attention_scored_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_tokens,
+                                                         int partition_size);
+PKV_API pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_dtype q_dtype,
+                                                     const void* key_cache, const void* value_cache,
+                                                     pkv_dtype cache_dtype,
+                                                     const int32_t* token_slots, int MT,
+                                                     const int32_t* num_tokens, float* scores, int S, int max_tokens,
+                                                     int Hq, int Hkv, int d, int bs, int NB,
+                                                     float scale, float k_scale, float v_scale,
+                                                     int partition_size,
+                                                     void* workspace, size_t workspace_bytes,
+                                                     int32_t* err_word, pkv_stream_t stream);
+
+/*
+ * evict_tokens -- cut every sequence to at most `budget` tokens.  A sequence
+ * of n = num_tokens[s] <= budget tokens keeps them all.  A longer one keeps
+ * its first num_first tokens, its last num_recent, and of those between the
+ * budget - num_first - num_recent with the largest scores (ties: the lowest
+ * index; a NaN score is below every number).  Kept tokens stay in order:
+ * new_slots[s] and new_scores[s] receive their slots and scores, new_num[s]
+ * their count, and evicted[s] (or NULL) the n - new_num[s] dropped tokens'
+ * slots, in order, for the caller's pool.  Arrays are [S, MT] (int32, fp32)
+ * and [S]; entries past the counts are left as they were.  No output may
+ * overlap an input or another output: a loop swaps two tables.
+ * num_first + num_recent <= budget.  A count outside [0, MT] is clamped and
+ * reported (PKV_DEVERR_CONTEXT_LEN).
+ */
+PKV_API pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* scores, const int32_t* num_tokens,
+                                    int S, int MT, int budget, int num_first, int num_recent,
+                                    int32_t* new_slots, float* new_scores, int32_t* new_num, int32_t* evicted,
+                                    int32_t* err_word, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Host block manager: the bookkeeping that produces the block tables, slot
  * mappings and copy-on-write pairs the device calls consume.  Host memory
  * only; nothing here touches the GPU.

@@ -41,7 +41,11 @@ EXPORTED = ("pkv_paged_kv_write", "pkv_decode_workspace_size", "pkv_decode_parti
             "pkv_pool_append_token", "pkv_pool_fork", "pkv_pool_free_sequence", "pkv_pool_block_table",
             "pkv_pool_append_tokens", "pkv_pool_block_tables", "pkv_prefill_workspace_size",
             "pkv_paged_attention_prefill", "pkv_paged_attention_prefill_ex", "pkv_token_attention_decode",
-            "pkv_repack_tokens", "pkv_vtoken_plan", "pkv_paged_kv_write_decode")
+            "pkv_repack_tokens", "pkv_vtoken_plan", "pkv_paged_kv_write_decode",
+            "pkv_decode_window_workspace_size", "pkv_paged_attention_decode_window",
+            "pkv_prefill_window_workspace_size", "pkv_paged_attention_prefill_window", "pkv_kv4_block_bytes",
+            "pkv_paged_kv4_write", "pkv_paged_kv4_read", "pkv_paged_attention_decode_kv4",
+            "pkv_token_attention_scored_workspace_size", "pkv_token_attention_decode_scored", "pkv_evict_tokens")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -121,6 +125,29 @@ def _load() -> ctypes.CDLL:
     lib.pkv_repack_tokens.restype = i32
     lib.pkv_vtoken_plan.argtypes = [pi32, i32, pi32, i32, i32, i32, pi64, i64, pi64, pi32, i64, pi64]
     lib.pkv_vtoken_plan.restype = i32
+    lib.pkv_decode_window_workspace_size.argtypes = [i32] * 9
+    lib.pkv_decode_window_workspace_size.restype = sz
+    lib.pkv_paged_attention_decode_window.argtypes = dec[:19] + [i32, i32] + dec[19:] + [i32]
+    lib.pkv_paged_attention_decode_window.restype = i32
+    lib.pkv_prefill_window_workspace_size.argtypes = [i32] * 11
+    lib.pkv_prefill_window_workspace_size.restype = sz
+    pre = lib.pkv_paged_attention_prefill.argtypes
+    lib.pkv_paged_attention_prefill_window.argtypes = pre[:20] + [i32, i32] + pre[20:]
+    lib.pkv_paged_attention_prefill_window.restype = i32
+    lib.pkv_kv4_block_bytes.argtypes = [i32] * 3
+    lib.pkv_kv4_block_bytes.restype = sz
+    lib.pkv_paged_kv4_write.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, f32, f32, vp, vp]
+    lib.pkv_paged_kv4_write.restype = i32
+    lib.pkv_paged_kv4_read.argtypes = lib.pkv_paged_kv4_write.argtypes
+    lib.pkv_paged_kv4_read.restype = i32
+    lib.pkv_paged_attention_decode_kv4.argtypes = dec[:5] + dec[6:19] + [i32, i32] + dec[19:]
+    lib.pkv_paged_attention_decode_kv4.restype = i32
+    lib.pkv_token_attention_scored_workspace_size.argtypes = [i32] * 7
+    lib.pkv_token_attention_scored_workspace_size.restype = sz
+    lib.pkv_token_attention_decode_scored.argtypes = dec[:9] + [vp] + dec[9:]
+    lib.pkv_token_attention_decode_scored.restype = i32
+    lib.pkv_evict_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.pkv_evict_tokens.restype = i32
     lib.pkv_status_string.argtypes = [i32]
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_version.argtypes = []
@@ -396,6 +423,257 @@ def repack_tokens(key_caches: Sequence[torch.Tensor], value_caches: Sequence[tor
     _check("repack_tokens", lib.pkv_repack_tokens(kp, vp, L, _ptr(token_slots), token_slots.shape[1],
                                                   token_slots.shape[0], _ptr(moves), moves.numel() // 4, NB, bs,
                                                   token_bytes, _ptr(err_word), _stream(stream)))
+
+
+def _on_current_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The launch goes to the current device: tensors of another one are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"pkv calls take tensors of the current CUDA device ({dev}), got one on {t.device}")
+
+
+# ---- sliding window with sinks
+
+def decode_window_workspace_size(S: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, window: int,
+                                 num_sinks: int = 0, partition_size: int = 0) -> int:
+    return int(lib.pkv_decode_window_workspace_size(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks,
+                                                    partition_size))
+
+
+def make_window_workspace(S: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, window: int,
+                          num_sinks: int = 0, partition_size: int = 0, device=None) -> torch.Tensor:
+    """A zero-filled workspace for paged_attention_decode_window and
+    paged_attention_decode_kv4 (window 0: no window)."""
+    n = decode_window_workspace_size(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks, partition_size)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  max_context_len: int, scale: float, window: int, num_sinks: int = 0,
+                                  k_scale: float = 1.0, v_scale: float = 1.0, partition_size: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                                  stream=None, kernel: str = "auto") -> torch.Tensor:
+    """paged_attention_decode over the first num_sinks tokens and the last
+    `window` tokens of every sequence; blocks in between are not read."""
+    S, Hq, d = query.shape
+    NB, bs, Hkv, d2 = key_cache.shape
+    if d2 != d or out.shape != query.shape or out.dtype != query.dtype or value_cache.shape != key_cache.shape or \
+            value_cache.dtype != key_cache.dtype:
+        raise ValueError("shape or dtype mismatch")
+    _check_tables(block_tables, context_lens, S)
+    if workspace is None:
+        workspace = make_window_workspace(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks, partition_size,
+                                          device=query.device)
+    _on_current_device(out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
+    _check("paged_attention_decode_window", lib.pkv_paged_attention_decode_window(
+        _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
+        dtype_code(key_cache.dtype), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S,
+        int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(window),
+        int(num_sinks), int(partition_size), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(err_word), _stream(stream), KERNELS[kernel]))
+    return out
+
+
+def prefill_window_workspace_size(S: int, num_query_tokens: int, max_query_len: int, Hq: int, Hkv: int, d: int,
+                                  bs: int, max_context_len: int, window: int, num_sinks: int = 0,
+                                  partition_size: int = 0) -> int:
+    return int(lib.pkv_prefill_window_workspace_size(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs,
+                                                     max_context_len, window, num_sinks, partition_size))
+
+
+def make_prefill_window_workspace(S: int, num_query_tokens: int, max_query_len: int, Hq: int, Hkv: int, d: int,
+                                  bs: int, max_context_len: int, window: int, num_sinks: int = 0,
+                                  partition_size: int = 0, device=None) -> torch.Tensor:
+    """A zero-filled workspace for paged_attention_prefill_window."""
+    n = prefill_window_workspace_size(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs, max_context_len, window,
+                                      num_sinks, partition_size)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                   value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                   query_start: torch.Tensor, max_query_len: int, max_context_len: int, scale: float,
+                                   window: int, num_sinks: int = 0, partition_size: int = 0,
+                                   workspace: Optional[torch.Tensor] = None,
+                                   err_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_prefill with every query under its own window and sinks."""
+    T, Hq, d = query.shape
+    NB, bs, Hkv, d2 = key_cache.shape
+    S = context_lens.numel()
+    if d2 != d or out.shape != query.shape or out.dtype != query.dtype or value_cache.shape != key_cache.shape or \
+            value_cache.dtype != key_cache.dtype or query_start.numel() != S + 1:
+        raise ValueError("shape or dtype mismatch")
+    _check_tables(block_tables, context_lens, S)
+    if query_start.dtype != torch.int32:
+        raise ValueError("query_start must be int32")
+    if workspace is None:
+        workspace = make_prefill_window_workspace(S, T, max_query_len, Hq, Hkv, d, bs, max_context_len, window,
+                                                  num_sinks, partition_size, device=query.device)
+    _on_current_device(out, query, key_cache, value_cache, block_tables, context_lens, query_start, workspace,
+                       err_word)
+    _check("paged_attention_prefill_window", lib.pkv_paged_attention_prefill_window(
+        _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
+        dtype_code(key_cache.dtype), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+        _ptr(query_start), S, T, int(max_query_len), int(max_context_len), Hq, Hkv, d, bs, NB, float(scale),
+        int(window), int(num_sinks), int(partition_size), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream)))
+    return out
+
+
+# ---- 4-bit cache
+
+def kv4_block_bytes(block_size: int, Hkv: int, d: int) -> int:
+    """Bytes of one block of a 4-bit K (or V) cache; 0 for unsupported sizes."""
+    return int(lib.pkv_kv4_block_bytes(block_size, Hkv, d))
+
+
+def make_kv4_cache(NB: int, block_size: int, Hkv: int, d: int, device=None) -> torch.Tensor:
+    """A 4-bit K (or V) cache, uint8 [NB, Hkv, bytes of a head], of zeros."""
+    n = kv4_block_bytes(block_size, Hkv, d)
+    if n == 0:
+        raise ValueError("4-bit caches take d 64 or 128 and blocks of 16 or 32 tokens")
+    return torch.zeros((NB, Hkv, n // Hkv), dtype=torch.uint8, device=device or "cuda")
+
+
+def _check_kv4(key_cache: torch.Tensor, value_cache: torch.Tensor, block_size: int, Hkv: int, d: int) -> None:
+    n = kv4_block_bytes(block_size, Hkv, d)
+    if key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8 or key_cache.dim() != 3 or \
+            value_cache.shape != key_cache.shape or key_cache.shape[1] != Hkv or \
+            (n != 0 and key_cache.shape[2] * Hkv != n):
+        raise ValueError("4-bit caches are uint8 [NB, Hkv, kv4_block_bytes(block_size, Hkv, d) // Hkv]")
+
+
+def _check_tables(block_tables: torch.Tensor, context_lens: torch.Tensor, S: int) -> None:
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or block_tables.dim() != 2:
+        raise ValueError("tables and lengths must be int32")
+    if block_tables.shape[0] != S or context_lens.numel() != S:
+        raise ValueError("tables and lengths must have a row per sequence")
+
+
+def paged_kv4_write(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, block_size: int, k_scale: float = 1.0, v_scale: float = 1.0,
+                    err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """paged_kv_write into 4-bit caches (make_kv4_cache): key/value
+    [T, Hkv, d] (fp32|bf16), slot_mapping int64 [T] (negative = skip)."""
+    T, Hkv, d = key.shape
+    _check_kv4(key_cache, value_cache, block_size, Hkv, d)
+    if value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("key and value must share shape and dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [T]")
+    _on_current_device(key, value, key_cache, value_cache, slot_mapping, err_word)
+    _check("paged_kv4_write", lib.pkv_paged_kv4_write(
+        _ptr(key), _ptr(value), dtype_code(key.dtype), _ptr(key_cache), _ptr(value_cache), _ptr(slot_mapping), T,
+        key_cache.shape[0], block_size, Hkv, d, float(k_scale), float(v_scale), _ptr(err_word), _stream(stream)))
+
+
+def paged_kv4_read(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                   slots: torch.Tensor, block_size: int, k_scale: float = 1.0, v_scale: float = 1.0,
+                   err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The values of slots (int64 [T]; negative = leave the row) of 4-bit
+    caches, into key/value [T, Hkv, d] (fp32|bf16)."""
+    T, Hkv, d = key.shape
+    _check_kv4(key_cache, value_cache, block_size, Hkv, d)
+    if value.shape != key.shape or value.dtype != key.dtype:
+        raise ValueError("key and value must share shape and dtype")
+    if slots.dtype != torch.int64 or slots.numel() != T:
+        raise ValueError("slots must be int64 [T]")
+    _on_current_device(key, value, key_cache, value_cache, slots, err_word)
+    _check("paged_kv4_read", lib.pkv_paged_kv4_read(
+        _ptr(key), _ptr(value), dtype_code(key.dtype), _ptr(key_cache), _ptr(value_cache), _ptr(slots), T,
+        key_cache.shape[0], block_size, Hkv, d, float(k_scale), float(v_scale), _ptr(err_word), _stream(stream)))
+
+
+def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                               max_context_len: int, scale: float, block_size: int, window: int = 0,
+                               num_sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                               partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                               err_word: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_attention_decode over 4-bit caches, bf16 query/out [S, Hq, d];
+    window 0: every token, else as in paged_attention_decode_window."""
+    S, Hq, d = query.shape
+    Hkv = key_cache.shape[1]
+    _check_kv4(key_cache, value_cache, block_size, Hkv, d)
+    if out.shape != query.shape or out.dtype != query.dtype:
+        raise ValueError("shape or dtype mismatch")
+    _check_tables(block_tables, context_lens, S)
+    if workspace is None:
+        workspace = make_window_workspace(S, Hq, Hkv, d, block_size, max_context_len, window, num_sinks,
+                                          partition_size, device=query.device)
+    _on_current_device(out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
+    _check("paged_attention_decode_kv4", lib.pkv_paged_attention_decode_kv4(
+        _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(context_lens), S, int(max_context_len), Hq, Hkv, d, block_size,
+        key_cache.shape[0], float(scale), float(k_scale), float(v_scale), int(window), int(num_sinks),
+        int(partition_size), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word),
+        _stream(stream)))
+    return out
+
+
+# ---- eviction by accumulated attention weight
+
+def scored_workspace_size(S: int, Hq: int, Hkv: int, d: int, bs: int, max_tokens: int,
+                          partition_size: int = 0) -> int:
+    return int(lib.pkv_token_attention_scored_workspace_size(S, Hq, Hkv, d, bs, max_tokens, partition_size))
+
+
+def make_scored_workspace(S: int, Hq: int, Hkv: int, d: int, bs: int, max_tokens: int, partition_size: int = 0,
+                          device=None) -> torch.Tensor:
+    """A workspace for token_attention_decode_scored, its header zero."""
+    n = scored_workspace_size(S, Hq, Hkv, d, bs, max_tokens, partition_size)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    ws[:256] = 0
+    return ws
+
+
+def token_attention_decode_scored(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, token_slots: torch.Tensor, num_tokens: torch.Tensor,
+                                  scores: torch.Tensor, max_tokens: int, scale: float, k_scale: float = 1.0,
+                                  v_scale: float = 1.0, partition_size: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                                  stream=None) -> torch.Tensor:
+    """token_attention_decode that also adds to scores (fp32 [S, MT]) the
+    attention weight of every live token, summed over the query heads."""
+    S, Hq, d = query.shape
+    NB, bs, Hkv, d2 = key_cache.shape
+    if d2 != d or out.shape != query.shape or out.dtype != query.dtype or value_cache.shape != key_cache.shape or \
+            value_cache.dtype != key_cache.dtype:
+        raise ValueError("shape or dtype mismatch")
+    _check_tables(token_slots, num_tokens, S)
+    if scores.dtype != torch.float32 or scores.shape != token_slots.shape:
+        raise ValueError("scores must be float32 of the token table's shape")
+    if workspace is None:
+        workspace = make_scored_workspace(S, Hq, Hkv, d, bs, max_tokens, partition_size, device=query.device)
+    _on_current_device(out, query, key_cache, value_cache, token_slots, num_tokens, scores, workspace, err_word)
+    _check("token_attention_decode_scored", lib.pkv_token_attention_decode_scored(
+        _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
+        dtype_code(key_cache.dtype), _ptr(token_slots), token_slots.shape[1], _ptr(num_tokens), _ptr(scores), S,
+        int(max_tokens), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(partition_size),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream)))
+    return out
+
+
+def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: torch.Tensor,
+                 new_slots: torch.Tensor, new_scores: torch.Tensor, new_num: torch.Tensor, budget: int,
+                 num_first: int = 0, num_recent: int = 0, evicted: Optional[torch.Tensor] = None,
+                 err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cut every sequence to `budget` tokens: its first num_first, its last
+    num_recent and the highest scores of the rest, in order, into new_slots,
+    new_scores [S, MT] and new_num [S]; the dropped slots go to evicted."""
+    S, MT = token_slots.shape
+    for t, dt, shape in ((token_slots, torch.int32, (S, MT)), (scores, torch.float32, (S, MT)),
+                         (num_tokens, torch.int32, (S,)), (new_slots, torch.int32, (S, MT)),
+                         (new_scores, torch.float32, (S, MT)), (new_num, torch.int32, (S,)),
+                         (evicted, torch.int32, (S, MT))):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
+            raise ValueError("tables are int32 and scores float32, [S, MT]; counts are int32 [S]")
+    _on_current_device(token_slots, scores, num_tokens, new_slots, new_scores, new_num, evicted, err_word)
+    _check("evict_tokens", lib.pkv_evict_tokens(
+        _ptr(token_slots), _ptr(scores), _ptr(num_tokens), S, MT, int(budget), int(num_first), int(num_recent),
+        _ptr(new_slots), _ptr(new_scores), _ptr(new_num), _ptr(evicted), _ptr(err_word), _stream(stream)))
 
 
 def vtoken_plan(token_slots: np.ndarray, num_tokens: np.ndarray, block_size: int, num_blocks: int):

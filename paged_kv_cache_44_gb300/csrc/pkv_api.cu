@@ -9,6 +9,8 @@
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "pkv_kv4.cuh"
+#include "pkv_units.cuh"
 
 namespace pkv {
 namespace {
@@ -135,6 +137,53 @@ void set_partitions(DecodeParams& p, const DecodePlan& pl, int Pl, int no_split_
     p.Q = Pl <= 0 ? p.P : (Pl == pl.P ? pl.Q : tail_chunk(Pl));
     p.hold = hold;
     p.Pmax = hold ? pl.Pmax : pl.Pmax_plain;
+}
+
+// A window or sinks beyond the longest sequence are as good as its length
+// (kept small so that the kernels' sums of them stay in 32 bits).
+void clamp_window(int max_ctx, int& window, int& sinks) {
+    if (window > max_ctx) window = max_ctx > 0 ? max_ctx : 1;
+    if (sinks > max_ctx) sinks = max_ctx;
+}
+
+// Tokens of the longest sequence a decode reads (max_ctx when window is 0).
+int decode_keys(int bs, int max_ctx, int window, int sinks) {
+    return window > 0 ? window_bound(max_ctx, window, sinks, bs, 1) : max_ctx;
+}
+
+// The partial results' place in the workspace and its scheduling counters.
+void set_workspace(DecodeParams& p, const DecodePlan& pl, void* workspace, size_t workspace_bytes) {
+    char* ws = static_cast<char*>(workspace);
+    if (pl.split) {
+        p.sched = reinterpret_cast<unsigned*>(ws);
+        p.part_ml = reinterpret_cast<float*>(ws + pl.ml_offset);
+        p.part_acc = reinterpret_cast<float*>(ws + pl.acc_offset);
+    } else if (workspace && workspace_bytes >= kWorkspaceHeaderBytes && aligned16(workspace)) {
+        p.sched = reinterpret_cast<unsigned*>(workspace);
+    }
+}
+
+// Workspace of a scored decode: its (max, sum) pairs are always there, and
+// the logits of every token behind the partial results.
+struct ScoredPlan {
+    DecodePlan pl;
+    size_t ml_offset, logits_offset, bytes;
+};
+ScoredPlan make_scored_plan(int S, int Hq, int Hkv, int d, int max_tokens, int P) {
+    ScoredPlan sp{};
+    sp.pl = make_plan(S, Hq, d, max_tokens, P);
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const int g = Hq / Hkv;
+    const size_t sets = (size_t)S * Hkv * ((g + kHeadSet - 1) / kHeadSet);
+    sp.ml_offset = sp.pl.split ? sp.pl.ml_offset : kWorkspaceHeaderBytes;
+    sp.logits_offset = sp.pl.split ? sp.pl.bytes : up(sp.ml_offset + (size_t)S * Hq * 2 * sizeof(float));
+    sp.bytes = up(sp.logits_offset + sets * max_tokens * score_width(g) * sizeof(float));
+    return sp;
+}
+
+bool overlap(const void* a, const void* b, size_t na, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
 }
 
 pkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
@@ -431,7 +480,7 @@ pkv_status pkv_token_attention_decode(void* out, const void* query, pkv_dtype q_
         p.sched = reinterpret_cast<unsigned*>(workspace);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, true);
+    cudaError_t e = launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kTokenTable);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     if (pl.split) e = launch_decode_reduce(p, q_dtype, st);
     return from_cuda(e);
@@ -478,7 +527,8 @@ namespace {
 
 // Prefill partition size (0 = no split; -1 = invalid): tiles of 16 (query,
 // head) rows already give parallelism, so split only when there are few.
-int resolve_prefill_partition(int S, int max_q_len, int Hq, int Hkv, int d, int bs, int max_ctx, int req) {
+// keys: the most a tile's queries reach (max_ctx without a window).
+int resolve_prefill_partition(int S, int max_q_len, int Hq, int Hkv, int d, int bs, int max_ctx, int keys, int req) {
     if (!decode_shape_ok(S, Hq, Hkv, d, bs, max_ctx) || max_q_len < 0 || max_q_len > max_ctx) return -1;
     if (req > 0) return req % bs == 0 ? req : -1;
     if (req == -1) return 0;
@@ -486,10 +536,18 @@ int resolve_prefill_partition(int S, int max_q_len, int Hq, int Hkv, int d, int 
     // counted in tiles of 128 rows (the tcgen05 kernel's unit); about four
     // units per SM keep the persistent CTAs busy to the end
     const long long tiles = (long long)S * Hkv * ((max_q_len * (long long)(Hq / Hkv) + 127) / 128);
-    if (tiles == 0 || tiles >= kPrefillTargetUnits || max_ctx <= kMinDefaultPartition) return 0;
+    if (tiles == 0 || tiles >= kPrefillTargetUnits || keys <= kMinDefaultPartition) return 0;
     int P = 1 << 20;
-    while (P > kMinDefaultPartition && tiles * ((max_ctx + P - 1) / P) < kPrefillTargetUnits) P >>= 1;
-    return P >= max_ctx ? 0 : P;
+    while (P > kMinDefaultPartition && tiles * ((keys + P - 1) / P) < kPrefillTargetUnits) P >>= 1;
+    return P >= keys ? 0 : P;
+}
+
+// Keys of the longest tile under a window: a tile of either kernel (up to
+// 256 rows) holds at most 255 / g + 2 queries.
+int prefill_keys(int max_q_len, int Hq, int Hkv, int bs, int max_ctx, int window, int sinks) {
+    if (window <= 0) return max_ctx;
+    const int queries = (2 * kPrefillTileRows - 1) / (Hq / Hkv) + 2;
+    return window_bound(max_ctx, window, sinks, bs, max_q_len < queries ? max_q_len : queries);
 }
 
 struct PrefillPlan {
@@ -516,37 +574,16 @@ PrefillPlan plan_prefill(int T, int Hq, int d, int max_ctx, int P) {
 }  // namespace
 }  // namespace pkv
 
-extern "C" {
+namespace pkv {
+namespace {
 
-size_t pkv_prefill_workspace_size(int S, int num_query_tokens, int max_query_len, int Hq, int Hkv, int d, int bs,
-                                  int max_context_len, int partition_size) {
-    if (num_query_tokens < 0) return 0;
-    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, partition_size);
-    if (P < 0) return 0;
-    return plan_prefill(num_query_tokens, Hq, d, max_context_len, P).bytes;
-}
-
-pkv_status pkv_paged_attention_prefill(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
-                                       const void* value_cache, pkv_dtype cache_dtype, const int32_t* block_tables,
-                                       int MB, const int32_t* context_lens, const int32_t* query_start, int S,
-                                       int num_query_tokens, int max_query_len, int max_context_len, int Hq,
-                                       int Hkv, int d, int bs, int NB, float scale, int partition_size,
-                                       void* workspace, size_t workspace_bytes, int32_t* err_word,
-                                       pkv_stream_t stream) {
-    return pkv_paged_attention_prefill_ex(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,
-                                          context_lens, query_start, S, num_query_tokens, max_query_len,
-                                          max_context_len, Hq, Hkv, d, bs, NB, scale, partition_size, workspace,
-                                          workspace_bytes, err_word, stream, PKV_PREFILL_AUTO);
-}
-
-pkv_status pkv_paged_attention_prefill_ex(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
-                                          const void* value_cache, pkv_dtype cache_dtype,
-                                          const int32_t* block_tables, int MB, const int32_t* context_lens,
-                                          const int32_t* query_start, int S, int num_query_tokens,
-                                          int max_query_len, int max_context_len, int Hq, int Hkv, int d, int bs,
-                                          int NB, float scale, int partition_size, void* workspace,
-                                          size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream,
-                                          int kernel) {
+// Query chunks; window 0: every key up to the query.
+pkv_status prefill_call(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache, const void* value_cache,
+                        pkv_dtype cache_dtype, const int32_t* block_tables, int MB, const int32_t* context_lens,
+                        const int32_t* query_start, int S, int num_query_tokens, int max_query_len,
+                        int max_context_len, int Hq, int Hkv, int d, int bs, int NB, float scale, int partition_size,
+                        void* workspace, size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream, int kernel,
+                        int window, int sinks) {
     if (kernel < PKV_PREFILL_AUTO || kernel > PKV_PREFILL_TCGEN05_2TILE) return PKV_ERR_INVALID_ARG;
     if (S < 0 || MB < 1 || NB < 1 || Hkv < 1 || Hq < 1 || max_context_len < 0 || num_query_tokens < 0 ||
         max_query_len < 0 || max_query_len > max_context_len)
@@ -565,9 +602,11 @@ pkv_status pkv_paged_attention_prefill_ex(void* out, const void* query, pkv_dtyp
         (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(context_lens) & 3u) ||
         (reinterpret_cast<uintptr_t>(query_start) & 3u))
         return PKV_ERR_INVALID_ARG;
-    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, partition_size);
+    clamp_window(max_context_len, window, sinks);
+    const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, sinks);
+    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys, partition_size);
     if (P < 0) return PKV_ERR_INVALID_ARG;
-    const PrefillPlan pl = plan_prefill(num_query_tokens, Hq, d, max_context_len, P);
+    const PrefillPlan pl = plan_prefill(num_query_tokens, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
     if (workspace && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
     DecodeParams p{};
@@ -578,6 +617,8 @@ pkv_status pkv_paged_attention_prefill_ex(void* out, const void* query, pkv_dtyp
     p.Q = p.P;                            // query chunks: whole partitions only
     p.Pmax = pl.Pmax;
     p.max_ctx = max_context_len;
+    p.window = window;
+    p.sinks = sinks;
     p.logit_scale_log2 = scale * kLog2e;
     p.out_scale = 1.f;
     if (workspace && workspace_bytes >= kWorkspaceHeaderBytes) p.sched = reinterpret_cast<unsigned*>(workspace);
@@ -602,6 +643,72 @@ pkv_status pkv_paged_attention_prefill_ex(void* out, const void* query, pkv_dtyp
                                          pl.split, st));
 }
 
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+size_t pkv_prefill_workspace_size(int S, int num_query_tokens, int max_query_len, int Hq, int Hkv, int d, int bs,
+                                  int max_context_len, int partition_size) {
+    if (num_query_tokens < 0) return 0;
+    const int P =
+        resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, max_context_len, partition_size);
+    if (P < 0) return 0;
+    return plan_prefill(num_query_tokens, Hq, d, max_context_len, P).bytes;
+}
+
+size_t pkv_prefill_window_workspace_size(int S, int num_query_tokens, int max_query_len, int Hq, int Hkv, int d, int bs,
+                                         int max_context_len, int window, int num_sinks, int partition_size) {
+    if (num_query_tokens < 0 || window < 1 || num_sinks < 0) return 0;
+    if (!decode_shape_ok(S, Hq, Hkv, d, bs, max_context_len)) return 0;
+    clamp_window(max_context_len, window, num_sinks);
+    const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, num_sinks);
+    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys, partition_size);
+    if (P < 0) return 0;
+    return plan_prefill(num_query_tokens, Hq, d, keys, P).bytes;
+}
+
+pkv_status pkv_paged_attention_prefill_window(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                              const void* value_cache, pkv_dtype cache_dtype,
+                                              const int32_t* block_tables, int MB, const int32_t* context_lens,
+                                              const int32_t* query_start, int S, int num_query_tokens,
+                                              int max_query_len, int max_context_len, int Hq, int Hkv, int d, int bs,
+                                              int NB, float scale, int window, int num_sinks, int partition_size,
+                                              void* workspace, size_t workspace_bytes, int32_t* err_word,
+                                              pkv_stream_t stream) {
+    if (window < 1 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
+    return prefill_call(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB, context_lens,
+                        query_start, S, num_query_tokens, max_query_len, max_context_len, Hq, Hkv, d, bs, NB, scale,
+                        partition_size, workspace, workspace_bytes, err_word, stream, PKV_PREFILL_AUTO, window,
+                        num_sinks);
+}
+
+pkv_status pkv_paged_attention_prefill(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                       const void* value_cache, pkv_dtype cache_dtype, const int32_t* block_tables,
+                                       int MB, const int32_t* context_lens, const int32_t* query_start, int S,
+                                       int num_query_tokens, int max_query_len, int max_context_len, int Hq,
+                                       int Hkv, int d, int bs, int NB, float scale, int partition_size,
+                                       void* workspace, size_t workspace_bytes, int32_t* err_word,
+                                       pkv_stream_t stream) {
+    return pkv_paged_attention_prefill_ex(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,
+                                          context_lens, query_start, S, num_query_tokens, max_query_len,
+                                          max_context_len, Hq, Hkv, d, bs, NB, scale, partition_size, workspace,
+                                          workspace_bytes, err_word, stream, PKV_PREFILL_AUTO);
+}
+
+pkv_status pkv_paged_attention_prefill_ex(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                          const void* value_cache, pkv_dtype cache_dtype,
+                                          const int32_t* block_tables, int MB, const int32_t* context_lens,
+                                          const int32_t* query_start, int S, int num_query_tokens,
+                                          int max_query_len, int max_context_len, int Hq, int Hkv, int d, int bs,
+                                          int NB, float scale, int partition_size, void* workspace,
+                                          size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream,
+                                          int kernel) {
+    return prefill_call(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB, context_lens,
+                        query_start, S, num_query_tokens, max_query_len, max_context_len, Hq, Hkv, d, bs, NB, scale,
+                        partition_size, workspace, workspace_bytes, err_word, stream, kernel, 0, 0);
+}
+
 pkv_status pkv_copy_blocks(void* const* key_caches, void* const* value_caches, int num_layers,
                            const int64_t* block_mapping, int P, int NB, size_t block_bytes, int32_t* err_word,
                            pkv_stream_t stream) {
@@ -620,6 +727,211 @@ pkv_status pkv_copy_blocks(void* const* key_caches, void* const* value_caches, i
     p.mapping = block_mapping; p.err = err_word; p.P = P; p.NB = NB; p.L = num_layers;
     p.block_bytes = block_bytes;
     return from_cuda(launch_copy(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- sliding window with sinks
+
+size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_context_len, int window,
+                                        int num_sinks, int partition_size) {
+    if (window < 0 || num_sinks < 0 || !decode_shape_ok(S, Hq, Hkv, d, bs, max_context_len)) return 0;
+    if (window > 0) clamp_window(max_context_len, window, num_sinks);
+    const int keys = decode_keys(bs, max_context_len, window, num_sinks);
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    return P < 0 ? 0 : make_plan(S, Hq, d, keys, P).bytes;
+}
+
+pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                             const void* value_cache, pkv_dtype cache_dtype,
+                                             const int32_t* block_tables, int MB, const int32_t* context_lens, int S,
+                                             int max_context_len, int Hq, int Hkv, int d, int bs, int NB, float scale,
+                                             float k_scale, float v_scale, int window, int num_sinks,
+                                             int partition_size, void* workspace, size_t workspace_bytes,
+                                             int32_t* err_word, pkv_stream_t stream, int kernel) {
+    if (window < 1 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
+    const pkv_status chk = check_decode_args(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables,
+                                             MB, context_lens, S, max_context_len, Hq, Hkv, d, bs, NB, scale,
+                                             k_scale, v_scale, partition_size, kernel);
+    if (chk != PKV_OK || S == 0) return chk;
+    clamp_window(max_context_len, window, num_sinks);
+    const int keys = decode_keys(bs, max_context_len, window, num_sinks);
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    const bool use_tc = kernel != PKV_DECODE_CUDA_CORES && decode_tc_supports(q_dtype, cache_dtype, d, bs, NB);
+    const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
+    const DecodePlan pl = make_plan(S, Hq, d, keys, P);
+    if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
+    if (pl.split && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    DecodeParams p{};
+    p.out = out; p.q = query; p.kc = key_cache; p.vc = value_cache;
+    p.block_tables = block_tables; p.context_lens = context_lens; p.err = err_word;
+    p.S = S; p.MB = MB; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.d = d; p.bs = bs; p.NB = NB;
+    p.window = window; p.sinks = num_sinks;
+    set_partitions(p, pl, launch_partition(pl, S, Hq, Hkv, keys, partition_size, use_tc && e4m3), MB * bs,
+                   tail_hold(cache_dtype, use_tc));
+    p.max_ctx = max_context_len;
+    p.logit_scale_log2 = scale * (e4m3 ? k_scale : 1.f) * kLog2e;
+    p.out_scale = e4m3 ? v_scale : 1.f;
+    set_workspace(p, pl, workspace, workspace_bytes);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = use_tc ? launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kWindow)
+                           : launch_decode_simt(p, q_dtype, cache_dtype, st);
+    if (e == cudaSuccess && pl.split) e = launch_decode_reduce(p, q_dtype, st);
+    return from_cuda(e);
+}
+
+// ---- 4-bit cache
+
+size_t pkv_kv4_block_bytes(int bs, int Hkv, int d) {
+    if (!(d == 64 || d == 128) || !(bs == 16 || bs == 32) || Hkv < 1) return 0;
+    return (size_t)Hkv * kv4_head_bytes(bs, d);
+}
+
+static pkv_status kv4_rows(const void* key, const void* value, void* key_out, void* value_out, pkv_dtype dt,
+                           const void* key_cache, const void* value_cache, const int64_t* slots, int T, int NB, int bs,
+                           int Hkv, int d, float k_scale, float v_scale, int32_t* err_word, pkv_stream_t stream,
+                           bool read) {
+    if (T < 0 || NB < 1 || bs < 1 || Hkv < 1 || d < 1) return PKV_ERR_INVALID_ARG;
+    if (dt != PKV_F32 && dt != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (pkv_kv4_block_bytes(bs, Hkv, d) == 0) return PKV_ERR_UNSUPPORTED;
+    if (!finite_pos(k_scale) || !finite_pos(v_scale)) return PKV_ERR_INVALID_ARG;
+    if (T == 0) return PKV_OK;
+    const void* a = read ? key_out : key;
+    const void* b = read ? value_out : value;
+    if (!a || !b || !key_cache || !value_cache || !slots) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return PKV_ERR_INVALID_ARG;
+    Kv4Params p{};
+    p.key = key; p.value = value; p.key_out = key_out; p.value_out = value_out;
+    p.key_cache = const_cast<void*>(key_cache); p.value_cache = const_cast<void*>(value_cache);
+    p.slots = slots; p.err = err_word;
+    p.T = T; p.NB = NB; p.bs = bs; p.Hkv = Hkv; p.d = d; p.k_scale = k_scale; p.v_scale = v_scale;
+    return from_cuda(launch_kv4(p, dt, read, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_paged_kv4_write(const void* key, const void* value, pkv_dtype in_dtype, void* key_cache,
+                               void* value_cache, const int64_t* slot_mapping, int T, int NB, int bs, int Hkv, int d,
+                               float k_scale, float v_scale, int32_t* err_word, pkv_stream_t stream) {
+    return kv4_rows(key, value, nullptr, nullptr, in_dtype, key_cache, value_cache, slot_mapping, T, NB, bs, Hkv, d,
+                    k_scale, v_scale, err_word, stream, false);
+}
+
+pkv_status pkv_paged_kv4_read(void* key, void* value, pkv_dtype out_dtype, const void* key_cache,
+                              const void* value_cache, const int64_t* slots, int T, int NB, int bs, int Hkv, int d,
+                              float k_scale, float v_scale, int32_t* err_word, pkv_stream_t stream) {
+    return kv4_rows(nullptr, nullptr, key, value, out_dtype, key_cache, value_cache, slots, T, NB, bs, Hkv, d, k_scale,
+                    v_scale, err_word, stream, true);
+}
+
+pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                          const void* value_cache, const int32_t* block_tables, int MB,
+                                          const int32_t* context_lens, int S, int max_context_len, int Hq, int Hkv,
+                                          int d, int bs, int NB, float scale, float k_scale, float v_scale, int window,
+                                          int num_sinks, int partition_size, void* workspace, size_t workspace_bytes,
+                                          int32_t* err_word, pkv_stream_t stream) {
+    if (window < 0 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
+    if (q_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    // the checks of a decode over a cache with tensor scales
+    const pkv_status chk = check_decode_args(out, query, q_dtype, key_cache, value_cache, PKV_FP8_E4M3, block_tables,
+                                             MB, context_lens, S, max_context_len, Hq, Hkv, d, bs, NB, scale,
+                                             k_scale, v_scale, partition_size, PKV_DECODE_AUTO);
+    if (chk != PKV_OK || S == 0) return chk;
+    if (window > 0) clamp_window(max_context_len, window, num_sinks);
+    const int keys = decode_keys(bs, max_context_len, window, num_sinks);
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    const DecodePlan pl = make_plan(S, Hq, d, keys, P);
+    if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
+    if (pl.split && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    DecodeParams p{};
+    p.out = out; p.q = query; p.kc = key_cache; p.vc = value_cache;
+    p.block_tables = block_tables; p.context_lens = context_lens; p.err = err_word;
+    p.S = S; p.MB = MB; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.d = d; p.bs = bs; p.NB = NB;
+    p.window = window; p.sinks = window > 0 ? num_sinks : 0;
+    set_partitions(p, pl, pl.P, MB * bs, 0);
+    p.max_ctx = max_context_len;
+    p.logit_scale_log2 = scale * k_scale * kLog2e;
+    p.out_scale = v_scale;
+    set_workspace(p, pl, workspace, workspace_bytes);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_decode_kv4(p, num_sms_current(), st);
+    if (e == cudaSuccess && pl.split) e = launch_decode_reduce(p, q_dtype, st);
+    return from_cuda(e);
+}
+
+// ---- eviction by accumulated attention weight
+
+size_t pkv_token_attention_scored_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_tokens,
+                                                 int partition_size) {
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, max_tokens, partition_size);
+    return P < 0 ? 0 : make_scored_plan(S, Hq, Hkv, d, max_tokens, P).bytes;
+}
+
+pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                             const void* value_cache, pkv_dtype cache_dtype,
+                                             const int32_t* token_slots, int MT, const int32_t* num_tokens,
+                                             float* scores, int S, int max_tokens, int Hq, int Hkv, int d, int bs,
+                                             int NB, float scale, float k_scale, float v_scale, int partition_size,
+                                             void* workspace, size_t workspace_bytes, int32_t* err_word,
+                                             pkv_stream_t stream) {
+    if (max_tokens < 0 || max_tokens > MT) return PKV_ERR_INVALID_ARG;
+    // the checks of a decode whose table holds every token: one table entry per token, none per block
+    const pkv_status chk = check_decode_args(out, query, q_dtype, key_cache, value_cache, cache_dtype, token_slots,
+                                             MT, num_tokens, S, max_tokens, Hq, Hkv, d, bs, NB, scale, k_scale,
+                                             v_scale, partition_size, PKV_DECODE_TENSOR_CORES);
+    if (chk != PKV_OK || S == 0) return chk;
+    if (!scores || (reinterpret_cast<uintptr_t>(scores) & 3u)) return PKV_ERR_INVALID_ARG;
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, max_tokens, partition_size);
+    const ScoredPlan sp = make_scored_plan(S, Hq, Hkv, d, max_tokens, P);
+    if (!workspace || workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
+    DecodeParams p{};
+    p.out = out; p.q = query; p.kc = key_cache; p.vc = value_cache;
+    p.token_slots = token_slots; p.MT = MT; p.context_lens = num_tokens; p.err = err_word;
+    p.S = S; p.MB = 1; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.d = d; p.bs = bs; p.NB = NB;
+    set_partitions(p, sp.pl, launch_partition(sp.pl, S, Hq, Hkv, max_tokens, partition_size, e4m3),
+                   max_tokens > 0 ? max_tokens : 1, tail_hold(cache_dtype, true));
+    p.max_ctx = max_tokens;
+    p.logit_scale_log2 = scale * (e4m3 ? k_scale : 1.f) * kLog2e;
+    p.out_scale = e4m3 ? v_scale : 1.f;
+    set_workspace(p, sp.pl, workspace, workspace_bytes);
+    char* ws = static_cast<char*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(ws + sp.ml_offset);
+    p.logits = reinterpret_cast<float*>(ws + sp.logits_offset);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kScored);
+    if (e == cudaSuccess && sp.pl.split) e = launch_decode_reduce(p, q_dtype, st);
+    if (e == cudaSuccess) e = launch_score(p, scores, MT, st);
+    return from_cuda(e);
+}
+
+pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* scores, const int32_t* num_tokens, int S, int MT,
+                            int budget, int num_first, int num_recent, int32_t* new_slots, float* new_scores,
+                            int32_t* new_num, int32_t* evicted, int32_t* err_word, pkv_stream_t stream) {
+    if (S < 0 || MT < 1 || budget < 0 || num_first < 0 || num_recent < 0) return PKV_ERR_INVALID_ARG;
+    if ((long long)num_first + num_recent > budget) return PKV_ERR_INVALID_ARG;
+    if (S > 65535) return PKV_ERR_UNSUPPORTED;
+    if (S == 0) return PKV_OK;
+    if (!token_slots || !scores || !num_tokens || !new_slots || !new_scores || !new_num) return PKV_ERR_INVALID_ARG;
+    const size_t rows = (size_t)S * MT * 4, nums = (size_t)S * 4;
+    const void* in[3] = {token_slots, scores, num_tokens};
+    const size_t in_bytes[3] = {rows, rows, nums};
+    const void* to[4] = {new_slots, new_scores, new_num, evicted};
+    const size_t to_bytes[4] = {rows, rows, nums, rows};
+    for (int i = 0; i < 4; ++i) {
+        if (to[i] == nullptr) continue;
+        if (reinterpret_cast<uintptr_t>(to[i]) & 3u) return PKV_ERR_INVALID_ARG;
+        for (int j = 0; j < 3; ++j)
+            if (overlap(to[i], in[j], to_bytes[i], in_bytes[j])) return PKV_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[i], to[j], to_bytes[i], to_bytes[j])) return PKV_ERR_INVALID_ARG;
+    }
+    for (const void* q : in)
+        if (reinterpret_cast<uintptr_t>(q) & 3u) return PKV_ERR_INVALID_ARG;
+    EvictParams p{};
+    p.token_slots = token_slots; p.scores = scores; p.num_tokens = num_tokens;
+    p.new_slots = new_slots; p.new_scores = new_scores; p.new_num = new_num; p.evicted = evicted; p.err = err_word;
+    p.S = S; p.MT = MT; p.budget = budget; p.first = num_first; p.recent = num_recent;
+    return from_cuda(launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

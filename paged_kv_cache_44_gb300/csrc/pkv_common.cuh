@@ -80,6 +80,35 @@ __host__ __device__ __forceinline__ void partition_range(int n, int P, int Q, in
     }
 }
 
+// Sliding window with sinks: a query at position p sees token t <= p when
+// t < sinks or t > p - window.  Whole blocks that no query of a unit sees
+// are left out: the unit's tokens are numbered without the gap between the
+// block that holds the last sink and the first block of the window.  Token v
+// of this numbering is token v + (v >= cut ? gap : 0) of the sequence; cut
+// and gap are multiples of the block size, so block boundaries agree.
+struct WindowSpan {
+    int cut, gap;
+};
+// start: the first token the window of the unit's first query holds (it may be negative)
+__host__ __device__ __forceinline__ WindowSpan window_span(int start, int sinks, int bs) {
+    WindowSpan w;
+    w.cut = (sinks + bs - 1) / bs * bs;
+    const int first = start > 0 ? start / bs * bs : 0;
+    w.gap = first > w.cut ? first - w.cut : 0;
+    return w;
+}
+__host__ __device__ __forceinline__ int span_token(const WindowSpan& w, int v) {
+    return v >= w.cut ? v + w.gap : v;
+}
+// Upper bound of a unit's tokens in that numbering, for lengths up to
+// max_ctx and units whose queries' positions span `queries` tokens: the gap
+// leaves at most the sinks' blocks, the window, the queries and the rest of
+// the window's first block.
+__host__ __device__ __forceinline__ int window_bound(int max_ctx, int window, int sinks, int bs, int queries) {
+    const long long b = (long long)(sinks + bs - 1) / bs * bs + window + queries - 1 + bs - 1;
+    return b < max_ctx ? (int)b : max_ctx;
+}
+
 // ---- scalar element -> float (fp8: the code's value, scale applied by caller)
 
 __device__ __forceinline__ float to_float(float x) { return x; }

@@ -45,6 +45,17 @@
 // counts one arrival per lane when its copies land; the math is unchanged.
 // (A tensor copy that gathers rows could write only whole 1024-byte swizzle
 // atoms, which four 128-byte rows do not fill.)
+//
+// With a sliding window and sinks (WIN) a unit's tokens are numbered without
+// the blocks no query sees (window_span): the copies, the masks and the
+// partitions of the visible tokens are those of a shorter sequence, so the
+// bytes read are the visible blocks' and the rate is the decode's.
+//
+// Scored (SCORED): also stores the logits of a token table's tokens, 4 bytes
+// per token and query head, and every unit's (max, sum).  A weight
+// 2^(x - M) / L needs the whole row's M and L, known only after the last
+// unit; storing the logits costs 8 * g / (2 * row bytes) of the K/V traffic
+// (an eighth, for bf16 rows of 128 values and g = 8), reading K again a half.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -55,6 +66,7 @@
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc_common.cuh"
+#include "pkv_units.cuh"
 
 namespace pkv {
 namespace {
@@ -85,7 +97,6 @@ using namespace tc;
 #define PKV_TC_TOK_FP8 32
 #endif
 
-constexpr int kHeadsPerUnit = 8;
 constexpr long long kWaitLimitCycles = 4000000000LL;   // ~2 s: a stage that never lands
 
 template <int D, bool FP8, int QB>
@@ -122,68 +133,6 @@ struct Cfg {
     static_assert(kCtlOff % 1024 == 0 && kCtlBytes % 16 == 0, "trailer alignment");
 };
 
-// ------------------------------------------------------------------- units
-
-// Region B ids per (sequence, head set): the full-size chunks of the longest
-// remainder (hold * P + P - 1 tokens), then one for the partial chunk.
-__host__ __device__ __forceinline__ int chunk_slots(int P, int Q, int hold) {
-    const int held = Q < P ? hold : 0;
-    return (held * P + P - 1) / Q + 1;
-}
-
-struct __align__(16) Unit {
-    int s, kvh, h0, nh, part, t0, t1, np;
-};
-
-// Unit id -> coordinates.  The ids run over two regions:
-//   A: every full partition (P tokens) not held back, partition-major -- the same
-//      partition of every sequence is claimed close together in time, so
-//      shared prefix blocks are read while still in L2;
-//   B: the chunks of each sequence's last, partial partition (and, with
-//      p.hold, of the full partitions held back before it): first every
-//      full-size chunk (Q tokens), chunk-major, then each sequence's
-//      shorter last chunk (and the empty unit of a sequence with no tokens).
-// Claimed in id order, the long units go first and the short ones last, so
-// the tail of the launch is short.  Returns false for ids that name no
-// work (a partition past the sequence's full ones, a chunk past its
-// remainder, or a last chunk that does not exist).
-__device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long long u, int nsets,
-                                        unsigned long long region_a, Unit& x) {
-    const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
-    const bool in_a = u < region_a;
-    const unsigned long long v = in_a ? u : u - region_a;
-    const int idx = (int)(v / per_part);                  // partition (A) or chunk (B) index
-    const unsigned long long rem = v - (unsigned long long)idx * per_part;
-    x.s = (int)(rem / (unsigned)(p.Hkv * nsets));
-    const int r2 = (int)(rem - (unsigned long long)x.s * (p.Hkv * nsets));
-    x.kvh = r2 / nsets;
-    const int set = r2 - x.kvh * nsets;
-    x.h0 = x.kvh * p.g + set * kHeadsPerUnit;
-    x.nh = min(kHeadsPerUnit, p.g - set * kHeadsPerUnit);
-    int n = __ldg(p.context_lens + x.s);
-    if (n < 0 || n > p.max_ctx) {
-        if (!in_a && idx == 0 && r2 == 0) report(p.err, PKV_DEVERR_CONTEXT_LEN);
-        n = n < 0 ? 0 : p.max_ctx;
-    }
-    x.np = num_partitions(n, p.P, p.Q, p.hold);
-    const int full = whole_partitions(n, p.P, p.Q, p.hold);
-    const int tail = n - full * p.P;
-    const int cfull = chunk_slots(p.P, p.Q, p.hold) - 1;   // full-size chunks of the longest remainder
-    if (in_a) {
-        if (idx >= full) return false;
-        x.part = idx;
-    } else if (idx < cfull) {
-        if ((idx + 1) * p.Q > tail) return false;          // full-size chunks first
-        x.part = full + idx;
-    } else {
-        if (idx > cfull) return false;
-        if (n > 0 && tail % p.Q == 0) return false;        // then the remainder's partial chunk
-        x.part = full + tail / p.Q;
-    }
-    partition_range(n, p.P, p.Q, p.hold, x.part, x.t0, x.t1);
-    return true;
-}
-
 template <typename QF>
 __device__ __forceinline__ void store_out(const DecodeParams& p, size_t idx, float v) {
     store_elem<QF>(p.out, idx, v);
@@ -191,12 +140,15 @@ __device__ __forceinline__ void store_out(const DecodeParams& p, size_t idx, flo
 
 // ------------------------------------------------------------------ kernel
 
-template <int D, bool FP8, typename QF, bool TT>
+template <int D, bool FP8, typename QF, DecodeMode MODE>
 __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, unsigned long long total_units,
                      unsigned long long region_a, int nsets) {
     using C = Cfg<D, FP8, QF::bytes>;
+    constexpr bool TT = MODE == DecodeMode::kTokenTable || MODE == DecodeMode::kScored;
+    constexpr bool WIN = MODE == DecodeMode::kWindow;
+    constexpr bool SCORED = MODE == DecodeMode::kScored;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;     // fragment row / column-pair of this lane
@@ -300,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             static_next += total_warps;
             if (v >= total_units) return false;
             Unit x;
-            if (!unit_of(p, v, nsets, region_a, x)) continue;
+            if (!unit_of<WIN>(p, v, nsets, region_a, x)) continue;
             if (x.t1 <= x.t0) {
                 // a sequence with no tokens: its output is zero
                 for (int i = lane; i < x.nh * D; i += 32)
@@ -315,9 +267,14 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     // block-table entries of the issuing unit, 32 per chunk, one per lane;
     // the next chunk is loaded while the current one is in use
     int tab = 0, tab_next = 0, tab_chunk = 0, tab_blocks = 0;
+    int i_n = 0;                          // with a window: the sequence's length and the tokens left out
+    WindowSpan i_span{};
     auto load_chunk = [&](int chunk) -> int {
         const int rb = 32 * chunk + lane;
-        return rb < tab_blocks ? __ldg(p.block_tables + (size_t)iu.s * p.MB + iu.t0 / p.bs + rb) : 0;
+        if (rb >= tab_blocks) return 0;
+        int lb = iu.t0 / p.bs + rb;
+        if constexpr (WIN) lb = span_token(i_span, lb * p.bs) / p.bs;
+        return __ldg(p.block_tables + (size_t)iu.s * p.MB + lb);
     };
 
     auto issue_one = [&]() -> bool {
@@ -328,7 +285,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
                 claiming = false;
                 return false;
             }
-            unit_of(p, u, nsets, region_a, iu);
+            unit_of<WIN>(p, u, nsets, region_a, iu);
+            if constexpr (WIN) {
+                i_n = min(max(__ldg(p.context_lens + iu.s), 0), p.max_ctx);
+                i_span = window_span(i_n - p.window, p.sinks, p.bs);
+            }
             if (lane == 0) {
                 int4* e = reinterpret_cast<int4*>(queue + q_tail % C::kQueue);
                 e[0] = make_int4(iu.s, iu.kvh, iu.h0, iu.nh);
@@ -401,6 +362,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             report(p.err, PKV_DEVERR_BLOCK_ID);
             ok = false;
         }
+        if constexpr (WIN) {                                   // tokens of the loaded blocks the query does not see
+            const int t = span_token(i_span, ts + lane);
+            ok = ok && (t < p.sinks || t >= i_n - p.window);
+        }
         const uint32_t m = __ballot_sync(0xffffffffu, ok);
         // one box per (box_rows tokens of the stage, K or V, 128-byte half): lane i issues box i
         const int nbox = boxes_per_stage * 2 * C::kHalves;
@@ -435,6 +400,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     float o[C::KS][4];                    // O^T accumulators, m-tile t of d
     float m_run[2], l_run[2];             // heads 2c, 2c+1
     const float scl = p.logit_scale_log2;
+    const int s_width = score_width(p.g);
+    float* c_logits = nullptr;            // scored: the unit's sequence and head set
     bool bail = false;
 
     // Fused write + decode: when this stage holds the sequence's last token,
@@ -497,6 +464,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             c_nst = (cu.t1 - cu.t0 + kTok - 1) / kTok;
             have_unit = true;
             need_q = true;
+            if constexpr (SCORED) {
+                const size_t row = ((size_t)cu.s * p.Hkv + cu.kvh) * nsets + (cu.h0 - cu.kvh * p.g) / kHeadsPerUnit;
+                c_logits = p.logits + row * p.max_ctx * s_width;
+            }
 #pragma unroll
             for (int t = 0; t < C::KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
             m_run[0] = m_run[1] = -CUDART_INF_F;
@@ -558,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
         }
         const uint32_t vmask = masks[slot];
         const uint32_t kb = stage_k(slot), vb = stage_v(slot);
-        if constexpr (!TT) {
+        if constexpr (MODE == DecodeMode::kBlockTable) {
             if (p.new_k != nullptr) patch_new_token(kb, vb);
         }
 
@@ -623,6 +594,19 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             x[mt][3] = vb2 ? sacc[mt][3] * scl : -CUDART_INF_F;
             cmax0 = fmaxf(cmax0, fmaxf(x[mt][0], x[mt][2]));
             cmax1 = fmaxf(cmax1, fmaxf(x[mt][1], x[mt][3]));
+            if constexpr (SCORED) {
+                // this lane's two heads of tokens ta and tb, a row of s_width heads per token:
+                // eight rows of a warp's store are consecutive (fp32: a weight is their exponential)
+                const int t = cu.t0 + c_stage * kTok;
+                if (2 * c < s_width) {
+                    if (t + ta < cu.t1)
+                        *reinterpret_cast<float2*>(c_logits + (size_t)(t + ta) * s_width + 2 * c) =
+                            make_float2(x[mt][0], x[mt][1]);
+                    if (t + tb < cu.t1)
+                        *reinterpret_cast<float2*>(c_logits + (size_t)(t + tb) * s_width + 2 * c) =
+                            make_float2(x[mt][2], x[mt][3]);
+                }
+            }
         }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -738,6 +722,11 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
                     if (wA) { store_out<QF>(p, oA + d0, o[t][0] * fA); store_out<QF>(p, oA + d1, o[t][2] * fA); }
                     if (wB) { store_out<QF>(p, oB + d0, o[t][1] * fB); store_out<QF>(p, oB + d1, o[t][3] * fB); }
                 }
+                if constexpr (SCORED) {
+                    const size_t uA = ((size_t)cu.s * p.Hq + cu.h0 + hA) * p.Pmax;
+                    if (r == 0 && wA) *reinterpret_cast<float2*>(p.part_ml + 2 * uA) = make_float2(m_run[0], l0);
+                    if (r == 0 && wB) *reinterpret_cast<float2*>(p.part_ml + 2 * (uA + p.Pmax)) = make_float2(m_run[1], l1);
+                }
             } else {
                 const uint64_t keep = l2_policy_evict_last();   // held in L2 until the merge reads it
                 const size_t uA = ((size_t)cu.s * p.Hq + cu.h0 + hA) * p.Pmax + cu.part;
@@ -810,10 +799,10 @@ bool encode_cache_map(CUtensorMap* map, const void* base, const DecodeParams& p)
     return rc == CUDA_SUCCESS;
 }
 
-template <int D, bool FP8, typename QF, bool TT>
+template <int D, bool FP8, typename QF, DecodeMode MODE>
 cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
     using C = Cfg<D, FP8, QF::bytes>;
-    auto kern = decode_tc_kernel<D, FP8, QF, TT>;
+    auto kern = decode_tc_kernel<D, FP8, QF, MODE>;
     static SmemOptIn optin;
     cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), C::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -822,7 +811,7 @@ cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit;
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
-    const unsigned long long region_a = (unsigned long long)(p.max_ctx / p.P) * per_part;   // full partitions
+    const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
     unsigned long long want = (units + C::kWarps - 1) / C::kWarps;
     int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
@@ -840,20 +829,26 @@ bool decode_tc_supports(pkv_dtype q_dt, pkv_dtype c_dt, int d, int bs, int NB) {
     return c_dt == PKV_FP8_E4M3 && (q_dt == PKV_BF16 || q_dt == PKV_F32);
 }
 
-template <bool TT>
+template <DecodeMode MODE>
 cudaError_t launch_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st) {
     if (c_dt == PKV_BF16)
-        return p.d == 64 ? launch_one<64, false, BF16, TT>(p, num_sms, st)
-                         : launch_one<128, false, BF16, TT>(p, num_sms, st);
+        return p.d == 64 ? launch_one<64, false, BF16, MODE>(p, num_sms, st)
+                         : launch_one<128, false, BF16, MODE>(p, num_sms, st);
     if (q_dt == PKV_BF16)
-        return p.d == 64 ? launch_one<64, true, BF16, TT>(p, num_sms, st) : launch_one<128, true, BF16, TT>(p, num_sms, st);
-    return p.d == 64 ? launch_one<64, true, F32, TT>(p, num_sms, st) : launch_one<128, true, F32, TT>(p, num_sms, st);
+        return p.d == 64 ? launch_one<64, true, BF16, MODE>(p, num_sms, st) : launch_one<128, true, BF16, MODE>(p, num_sms, st);
+    return p.d == 64 ? launch_one<64, true, F32, MODE>(p, num_sms, st) : launch_one<128, true, F32, MODE>(p, num_sms, st);
 }
 
 cudaError_t launch_decode_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st,
-                             bool token_table) {
+                             DecodeMode mode) {
     if (p.S == 0) return cudaSuccess;
-    return token_table ? launch_tc<true>(p, q_dt, c_dt, num_sms, st) : launch_tc<false>(p, q_dt, c_dt, num_sms, st);
+    switch (mode) {
+        case DecodeMode::kBlockTable: return launch_tc<DecodeMode::kBlockTable>(p, q_dt, c_dt, num_sms, st);
+        case DecodeMode::kTokenTable: return launch_tc<DecodeMode::kTokenTable>(p, q_dt, c_dt, num_sms, st);
+        case DecodeMode::kWindow: return launch_tc<DecodeMode::kWindow>(p, q_dt, c_dt, num_sms, st);
+        case DecodeMode::kScored: return launch_tc<DecodeMode::kScored>(p, q_dt, c_dt, num_sms, st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace pkv

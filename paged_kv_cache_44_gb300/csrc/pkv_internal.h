@@ -81,6 +81,21 @@ struct WriteParams {
 };
 cudaError_t launch_write(const WriteParams& p, pkv_dtype in_dt, pkv_dtype cache_dt, cudaStream_t st);
 
+struct Kv4Params {
+    const void* key;          // write: [T][Hkv][d]
+    const void* value;
+    void* key_cache;          // [NB][Hkv][kv4_head_bytes(bs, d)]
+    void* value_cache;
+    void* key_out;            // read: [T][Hkv][d]
+    void* value_out;
+    const int64_t* slots;     // [T]
+    int32_t* err;
+    int T, NB, bs, Hkv, d;
+    float k_scale, v_scale;
+};
+// the write, or the read of the same slots (dt: the dtype of the tokens outside the cache)
+cudaError_t launch_kv4(const Kv4Params& p, pkv_dtype dt, bool read, cudaStream_t st);
+
 struct CopyParams {
     const int64_t* mapping;
     int32_t* err;
@@ -131,7 +146,26 @@ struct DecodeParams {
     const int64_t* slot_mapping;
     pkv_dtype new_dt;
     float k_scale, v_scale;   // E4M3 write scales
+    // sliding window (0: none, every token up to the query) and the first
+    // tokens that stay visible; both at most max_ctx
+    int window, sinks;
+    // scored token-table decode: the logits (log2 units) of each unit's
+    // tokens, rows of score_width(g) heads, [S][Hkv * head sets][max_ctx]
+    float* logits;
 };
+
+struct EvictParams {
+    const int32_t* token_slots;   // [S][MT]
+    const float* scores;          // [S][MT]
+    const int32_t* num_tokens;    // [S]
+    int32_t* new_slots;           // [S][MT]
+    float* new_scores;            // [S][MT]
+    int32_t* new_num;             // [S]
+    int32_t* evicted;             // [S][MT], or null
+    int32_t* err;
+    int S, MT, budget, first, recent;
+};
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 
 // Resolved layout of the decode workspace.
 struct DecodePlan {
@@ -153,10 +187,21 @@ pkv_status check_decode_args(const void* out, const void* query, pkv_dtype q_dty
                              int bs, int NB, float scale, float k_scale, float v_scale, int partition_size,
                              int kernel);
 
+// What a tensor-core decode reads K/V through, and what else it does.
+enum class DecodeMode {
+    kBlockTable,
+    kTokenTable,
+    kWindow,     // block table, sliding window with sinks
+    kScored      // token table; also writes the logits and every row's (max, sum)
+};
+
 cudaError_t launch_decode_simt(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, cudaStream_t st);
 cudaError_t launch_decode_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms,
-                             cudaStream_t st, bool token_table = false);
+                             cudaStream_t st, DecodeMode mode = DecodeMode::kBlockTable);
+cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
+// scores[s][t] += the attention weights of a scored decode, rows of MT scores
+cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStream_t st);
 bool decode_tc_supports(pkv_dtype q_dt, pkv_dtype c_dt, int d, int bs, int NB);
 cudaError_t launch_prefill_tc(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                               bool merge, cudaStream_t st);

@@ -433,7 +433,9 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(DecodeParams p, cons
     const int kvh = h / p.g, row = (tq - q0) * p.g + (h - kvh * p.g);
     const int rows = ql * p.g, rt = row / tile_rows;
     const int last_row = min(rt * tile_rows + tile_rows - 1, rows - 1);
-    const int key_end = n - ql + last_row / p.g + 1;
+    int first;
+    WindowSpan span;
+    const int key_end = qtile_keys(p, n, ql, rt * tile_rows, last_row, first, span);
     const int np = (key_end + p.P - 1) / p.P;
     if (np <= 1) return;
     const size_t u0 = ((size_t)tq * p.Hq + h) * p.Pmax;

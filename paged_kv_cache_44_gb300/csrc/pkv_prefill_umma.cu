@@ -103,7 +103,7 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_umma_kernel(const __grid_constant__ DecodeParams p, const int32_t* __restrict__ query_start, int T,
                         int max_q, const __grid_constant__ CUtensorMap kmap,
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v = __shfl_sync(0xffffffffu, v, 0);
                 static_next += gridDim.x;
                 if (v >= total_units) break;
-                if (qtile_of<kURows>(p, query_start, T, max_q, v, rt_max, x)) {
+                if (qtile_of<kURows, WIN>(p, query_start, T, max_q, v, rt_max, x)) {
                     have = true;
                     break;
                 }
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     e[0] = make_int4(x.s, x.kvh, x.rt, x.part);
                     e[1] = make_int4(x.k0, x.k1, x.n, x.ql);
                     e[2] = make_int4(x.q0, x.np, x.rows, 1);
+                    if constexpr (WIN) e[3] = make_int4(x.span.cut, x.span.gap, 0, 0);
                 } else {
                     e[2] = make_int4(0, 0, 0, 0);
                 }
@@ -225,14 +226,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nst = (x.k1 - x.k0 + kTok - 1) / kTok;
             const int bps = kTok / p.bs;                      // blocks per stage: 8 or 4
             const int unit_blocks = (x.k1 - x.k0 + p.bs - 1) / p.bs;
-            const int32_t* trow = p.block_tables + (size_t)x.s * p.MB + x.k0 / p.bs;
+            const int32_t* trow = p.block_tables + (size_t)x.s * p.MB + (WIN ? 0 : x.k0 / p.bs);
             auto load_chunk = [&](int c) -> int {
-                const int rb = 32 * c + lane;
-                return rb < unit_blocks ? __ldg(trow + rb) : 0;
+                int rb = 32 * c + lane;
+                if (rb >= unit_blocks) return 0;
+                if constexpr (WIN) rb = span_token(x.span, x.k0 + rb * p.bs) / p.bs;
+                return __ldg(trow + rb);
             };
             int tab = load_chunk(0), tab_next = load_chunk(1), tab_chunk = 0;
             // one tile into its ring: K_j also publishes the token masks of stage j
-            auto issue = [&](bool isv, uint32_t gs, int pbv, uint32_t bmv, int nbv, int tnv) -> bool {
+            auto issue = [&](bool isv, uint32_t gs, int pbv, uint32_t bmv, int nbv, int tsv, int tnv) -> bool {
                 const uint32_t n_ring = isv ? NV : NK;
                 const uint32_t slot = gs % n_ring, ph = gs / n_ring;
                 if (ph >= 1) ok = wait(bar(isv ? kBarVEmpty : kBarKEmpty, slot), (ph - 1) & 1, true);
@@ -249,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int lo = 32 * lane;
                     const uint32_t tm = tnv >= lo + 32 ? 0xffffffffu : (tnv <= lo ? 0u : ((1u << (tnv - lo)) - 1u));
+                    // with a window, tokens no query of the tile sees are not present either
+                    if constexpr (WIN) w &= ~bits_between(tsv + lo, p.sinks, x.first - x.span.gap);
                     masks[4 * (gs & 3) + lane] = w & tm;
                 }
                 __syncwarp();
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool bok = lane < nb && pb >= 0 && pb < p.NB;
                 if (lane < nb && !bok) report(p.err, PKV_DEVERR_BLOCK_ID);
                 const uint32_t bm = __ballot_sync(0xffffffffu, bok);
-                if (!issue(false, g + j, pb, bm, nb, tn)) {
+                if (!issue(false, g + j, pb, bm, nb, ts, tn)) {
                     bad = true;
                     break;
                 }
@@ -312,6 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            WindowSpan span{};
+            if constexpr (WIN) span = WindowSpan{ring[4 * slot + 3].x, ring[4 * slot + 3].y};
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kBarUEmpty, slot));
             if (e2.w == 0) break;
@@ -319,10 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nst = (k1 - k0 + kTok - 1) / kTok;
             const int bps = kTok / p.bs;
             const int unit_blocks = (k1 - k0 + p.bs - 1) / p.bs;
-            const int32_t* trow = p.block_tables + (size_t)us * p.MB + k0 / p.bs;
+            const int32_t* trow = p.block_tables + (size_t)us * p.MB + (WIN ? 0 : k0 / p.bs);
             auto load_chunk = [&](int c) -> int {
-                const int rb = 32 * c + lane;
-                return rb < unit_blocks ? __ldg(trow + rb) : 0;
+                int rb = 32 * c + lane;
+                if (rb >= unit_blocks) return 0;
+                if constexpr (WIN) rb = span_token(span, k0 + rb * p.bs) / p.bs;
+                return __ldg(trow + rb);
             };
             int tab = load_chunk(0), tab_next = load_chunk(1), tab_chunk = 0;
             for (int j = 0; j < nst; ++j, ++g) {
@@ -486,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            const int gap = WIN ? ring[4 * slot + 3].y : 0;
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kBarUEmpty, slot));
             if (e2.w == 0) break;
@@ -495,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool rv = row < rows;
             const int qi = rv ? row / p.g : 0;
             const int hh = rv ? row - qi * p.g : 0;
-            const int pos = rv ? n - ql + qi : -1;
+            const int pos = rv ? n - ql + qi - gap : -1;      // in the tile's numbering of the keys
             float m_ref = -CUDART_INF_F, l = 0.f;
             const int nst = (k1 - k0 + kTok - 1) / kTok;
             for (int j = 0; j < nst; ++j, ++g) {
@@ -521,7 +531,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) umma::mbar_arrive(bar(kBarMaskEmpty, g & 3));
                 const bool all_present = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
                 // rows past the tile's last take the same path: their output is never stored
-                const bool whole = ((lim >= kTok - 1 && all_present) || !rv) && scl > 0.f;
+                bool seen_all = lim >= kTok - 1 && all_present;
+                uint32_t rw[4];                                  // this row's visible tokens, with a window
+                if constexpr (WIN) {
+                    const int v0 = k0 + j * kTok;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        rw[w] = mw[w] & bits_below(lim + 1 - 32 * w) &
+                                ~bits_between(v0 + 32 * w, p.sinks, pos - p.window + 1);
+                    seen_all = (rw[0] & rw[1] & rw[2] & rw[3]) == 0xffffffffu;
+                }
+                const bool whole = (seen_all || !rv) && scl > 0.f;
                 float mx8[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mx8[k] = -CUDART_INF_F;
@@ -537,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int bb = 0; bb < 32; ++bb) {
-                            const bool live = ((mw[q] >> bb) & 1u) && (32 * q + bb) <= lim;
+                            const bool live = WIN ? ((rw[q] >> bb) & 1u) : ((mw[q] >> bb) & 1u) && (32 * q + bb) <= lim;
                             const float xv = live ? __uint_as_float(sr[q][bb]) * scl : -CUDART_INF_F;
                             sr[q][bb] = __float_as_uint(xv);
                             mx8[bb & 7] = fmaxf(mx8[bb & 7], xv);
@@ -672,11 +692,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_umma_d(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                           bool merge, cudaStream_t st) {
     using C = UCfg<D>;
-    auto kern = prefill_umma_kernel<D>;
+    auto kern = prefill_umma_kernel<D, WIN>;
     static SmemOptIn optin;
     cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), C::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -698,8 +718,11 @@ cudaError_t launch_umma_d(const DecodeParams& p, const int32_t* query_start, int
 cudaError_t launch_prefill_umma(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                                 bool merge, cudaStream_t st) {
     if (p.S == 0 || T == 0) return cudaSuccess;
-    return p.d == 64 ? launch_umma_d<64>(p, query_start, T, max_q_len, num_sms, merge, st)
-                     : launch_umma_d<128>(p, query_start, T, max_q_len, num_sms, merge, st);
+    if (p.window > 0)
+        return p.d == 64 ? launch_umma_d<64, true>(p, query_start, T, max_q_len, num_sms, merge, st)
+                         : launch_umma_d<128, true>(p, query_start, T, max_q_len, num_sms, merge, st);
+    return p.d == 64 ? launch_umma_d<64, false>(p, query_start, T, max_q_len, num_sms, merge, st)
+                     : launch_umma_d<128, false>(p, query_start, T, max_q_len, num_sms, merge, st);
 }
 
 }  // namespace pkv

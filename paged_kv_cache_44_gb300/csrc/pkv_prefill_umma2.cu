@@ -119,7 +119,7 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_umma2_kernel(const __grid_constant__ DecodeParams p, const int32_t* __restrict__ query_start, int T,
                          int max_q, const __grid_constant__ CUtensorMap kmap,
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v = __shfl_sync(0xffffffffu, v, 0);
                 static_next += gridDim.x;
                 if (v >= total_units) break;
-                if (qtile_of<kURows>(p, query_start, T, max_q, v, rt_max, x)) {
+                if (qtile_of<kURows, WIN>(p, query_start, T, max_q, v, rt_max, x)) {
                     have = true;
                     break;
                 }
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     e[0] = make_int4(x.s, x.kvh, x.rt, x.part);
                     e[1] = make_int4(x.k0, x.k1, x.n, x.ql);
                     e[2] = make_int4(x.q0, x.np, x.rows, 1);
+                    if constexpr (WIN) e[3] = make_int4(x.span.cut, x.span.gap, 0, 0);
                 } else {
                     e[2] = make_int4(0, 0, 0, 0);
                 }
@@ -239,10 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nst = (x.k1 - x.k0 + kTok - 1) / kTok;
             const int bps = kTok / p.bs;                      // blocks per stage: 8 or 4
             const int unit_blocks = (x.k1 - x.k0 + p.bs - 1) / p.bs;
-            const int32_t* trow = p.block_tables + (size_t)x.s * p.MB + x.k0 / p.bs;
+            const int32_t* trow = p.block_tables + (size_t)x.s * p.MB + (WIN ? 0 : x.k0 / p.bs);
             auto load_chunk = [&](int c) -> int {
-                const int rb = 32 * c + lane;
-                return rb < unit_blocks ? __ldg(trow + rb) : 0;
+                int rb = 32 * c + lane;
+                if (rb >= unit_blocks) return 0;
+                if constexpr (WIN) rb = span_token(x.span, x.k0 + rb * p.bs) / p.bs;
+                return __ldg(trow + rb);
             };
             int tab = load_chunk(0), tab_next = load_chunk(1), tab_chunk = 0;
             for (int j = 0; j < nst; ++j) {
@@ -278,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int lo = 32 * lane;
                     const uint32_t tm = tn >= lo + 32 ? 0xffffffffu : (tn <= lo ? 0u : ((1u << (tn - lo)) - 1u));
+                    // with a window, tokens no query of the tile sees are not present either
+                    if constexpr (WIN) w &= ~bits_between(ts + lo, p.sinks, x.first - x.span.gap);
                     masks[4 * (gs & 3) + lane] = w & tm;
                 }
                 __syncwarp();
@@ -322,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            WindowSpan span{};
+            if constexpr (WIN) span = WindowSpan{ring[4 * slot + 3].x, ring[4 * slot + 3].y};
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kBarUEmpty, slot));
             if (e2.w == 0) break;
@@ -329,10 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nst = (k1 - k0 + kTok - 1) / kTok;
             const int bps = kTok / p.bs;
             const int unit_blocks = (k1 - k0 + p.bs - 1) / p.bs;
-            const int32_t* trow = p.block_tables + (size_t)us * p.MB + k0 / p.bs;
+            const int32_t* trow = p.block_tables + (size_t)us * p.MB + (WIN ? 0 : k0 / p.bs);
             auto load_chunk = [&](int c) -> int {
-                const int rb = 32 * c + lane;
-                return rb < unit_blocks ? __ldg(trow + rb) : 0;
+                int rb = 32 * c + lane;
+                if (rb >= unit_blocks) return 0;
+                if constexpr (WIN) rb = span_token(span, k0 + rb * p.bs) / p.bs;
+                return __ldg(trow + rb);
             };
             int tab = load_chunk(0), tab_next = load_chunk(1), tab_chunk = 0;
             for (int j = 0; j < nst; ++j, ++g) {
@@ -523,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            const int gap = WIN ? ring[4 * slot + 3].y : 0;
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kBarUEmpty, slot));
             if (e2.w == 0) break;
@@ -549,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool rv = row < rows;
             const int qi = rv ? row / p.g : 0;
             const int hh = rv ? row - qi * p.g : 0;
-            const int pos = rv ? n - ql + qi : -1;
+            const int pos = rv ? n - ql + qi - gap : -1;      // in the tile's numbering of the keys
             float m_ref = -CUDART_INF_F, l = 0.f;
             for (int j = 0; j < nst; ++j, ++g, ++gt) {
                 // S of this stage done (so the previous P . V is done too), and the token masks published
@@ -567,7 +577,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) umma::mbar_arrive(bar(kBarMaskEmpty, g & 3));
                 const bool all_present = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
                 // rows past the tile's last take the same path: their output is never stored
-                const bool whole = ((lim >= kTok - 1 && all_present) || !rv) && scl > 0.f;
+                bool seen_all = lim >= kTok - 1 && all_present;
+                uint32_t rw[4];                                  // this row's visible tokens, with a window
+                if constexpr (WIN) {
+                    const int v0 = k0 + j * kTok;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        rw[w] = mw[w] & bits_below(lim + 1 - 32 * w) &
+                                ~bits_between(v0 + 32 * w, p.sinks, pos - p.window + 1);
+                    seen_all = (rw[0] & rw[1] & rw[2] & rw[3]) == 0xffffffffu;
+                }
+                const bool whole = (seen_all || !rv) && scl > 0.f;
                 uint32_t sr[4][32];
 #pragma unroll
                 for (int qq = 0; qq < 4; ++qq) umma::tmem_ld32(tmem + lane_base + s_col + 32 * qq, sr[qq]);
@@ -587,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int qq = 0; qq < 4; ++qq)
 #pragma unroll
                         for (int bb = 0; bb < 32; ++bb) {
-                            const bool live = ((mw[qq] >> bb) & 1u) && (32 * qq + bb) <= lim;
+                            const bool live = WIN ? ((rw[qq] >> bb) & 1u) : ((mw[qq] >> bb) & 1u) && (32 * qq + bb) <= lim;
                             const float xv = live ? __uint_as_float(sr[qq][bb]) * scl : -CUDART_INF_F;
                             sr[qq][bb] = __float_as_uint(xv);
                             mx8[bb & 7] = fmaxf(mx8[bb & 7], xv);
@@ -717,11 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_umma2_d(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                            bool merge, cudaStream_t st) {
     using C = UCfg<D>;
-    auto kern = prefill_umma2_kernel<D>;
+    auto kern = prefill_umma2_kernel<D, WIN>;
     // the warpgroups' register shares must fit in what the block is launched
     // with (setmaxnreg waits forever otherwise): checked once, on the binary
     static std::once_flag checked;
@@ -755,8 +775,11 @@ cudaError_t launch_umma2_d(const DecodeParams& p, const int32_t* query_start, in
 cudaError_t launch_prefill_umma2(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len,
                                  int num_sms, bool merge, cudaStream_t st) {
     if (p.S == 0 || T == 0) return cudaSuccess;
-    return p.d == 64 ? launch_umma2_d<64>(p, query_start, T, max_q_len, num_sms, merge, st)
-                     : launch_umma2_d<128>(p, query_start, T, max_q_len, num_sms, merge, st);
+    if (p.window > 0)
+        return p.d == 64 ? launch_umma2_d<64, true>(p, query_start, T, max_q_len, num_sms, merge, st)
+                         : launch_umma2_d<128, true>(p, query_start, T, max_q_len, num_sms, merge, st);
+    return p.d == 64 ? launch_umma2_d<64, false>(p, query_start, T, max_q_len, num_sms, merge, st)
+                     : launch_umma2_d<128, false>(p, query_start, T, max_q_len, num_sms, merge, st);
 }
 
 }  // namespace pkv

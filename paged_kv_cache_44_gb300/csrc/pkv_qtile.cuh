@@ -8,7 +8,11 @@
 // its last query's position n - q_len + i_last, cut into partitions of P
 // tokens.  Unit ids run partition-major, then sequence, K/V head, row tile,
 // so the tiles of one key range are claimed together and share the K/V
-// reads in L2.
+// reads in L2.  With a sliding window (WIN) the keys of a tile are numbered
+// without the blocks none of its queries sees (window_span, from the window
+// of its first query): key_end, the partitions and k0, k1 are of that
+// numbering, in which the keys a query at position pos does not see are
+// those from `sinks` to pos - window - gap and those past pos - gap.
 #pragma once
 
 #include "pkv_common.cuh"
@@ -20,15 +24,36 @@ struct __align__(16) QTile {
     int s, kvh, rt, part;      // sequence, K/V head, row tile, key partition
     int k0, k1;                // key tokens [k0, k1)
     int n, ql;                 // sequence length, queries in the chunk
-    int q0, np, rows, pad;     // first query token, partitions of the tile, rows of the sequence
+    int q0, np, rows;          // first query token, partitions of the tile, rows of the sequence
+    int first;                 // WIN: the first token of the window of the tile's first query
+    WindowSpan span;           // WIN: the tokens left out
 };
+
+// The low x bits of a word, none for x <= 0, all for x >= 32.
+__device__ __forceinline__ uint32_t bits_below(int x) {
+    return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
+}
+// Bit b set: key v0 + b lies in [lo, hi).
+__device__ __forceinline__ uint32_t bits_between(int v0, int lo, int hi) {
+    return bits_below(hi - v0) & ~bits_below(lo - v0);
+}
+
+// Keys of a row tile: how many its queries reach, in window_span's numbering with a window.
+__device__ __forceinline__ int qtile_keys(const DecodeParams& p, int n, int ql, int first_row, int last_row,
+                                          int& first, WindowSpan& span) {
+    const int key_end = n - ql + last_row / p.g + 1;
+    if (p.window <= 0) return key_end;
+    first = n - ql + first_row / p.g - p.window + 1;
+    span = window_span(first, p.sinks, p.bs);
+    return key_end - span.gap;
+}
 
 // Unit id -> coordinates; false for ids that name no work.  A sequence whose
 // length exceeds the host bound, whose query count is outside [0, n] or
 // above the host's max_q, or whose queries leave [0, T) is skipped and
 // reported once.  rt_max = ceil(max_q * g / ROWS) tiles per (sequence, K/V
 // head).
-template <int ROWS>
+template <int ROWS, bool WIN = false>
 __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* query_start, int T, int max_q,
                                          unsigned long long u, int rt_max, QTile& x) {
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * rt_max;
@@ -49,7 +74,9 @@ __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* q
     x.rows = x.ql * p.g;
     if (x.rt * ROWS >= x.rows) return false;
     const int last_row = min(x.rt * ROWS + ROWS - 1, x.rows - 1);
-    const int key_end = n - x.ql + last_row / p.g + 1;
+    int key_end;
+    if constexpr (WIN) key_end = qtile_keys(p, n, x.ql, x.rt * ROWS, last_row, x.first, x.span);
+    else key_end = n - x.ql + last_row / p.g + 1;
     x.np = (key_end + p.P - 1) / p.P;
     if (x.part >= x.np) return false;
     x.k0 = x.part * p.P;
