@@ -595,8 +595,8 @@ PKV_API pkv_status pkv_paged_kv4_read(void* key, void* value, pkv_dtype out_dtyp
  * paged_attention_decode_kv4 -- pkv_paged_attention_decode over a 4-bit
  * cache, under a sliding window when window > 0 (0: every token).  bf16
  * query and output (anything else returns PKV_ERR_UNSUPPORTED).  The query
- * is rounded to fp16 after a factor of 4 for the products: |query| must stay
- * below 16376.  Workspace: pkv_decode_window_workspace_size(...) with the
+ * and its sums over 32 values go through fp16 for the products: |query| must
+ * stay below 2047.  Workspace: pkv_decode_window_workspace_size(...) with the
  * same window and sinks.
  */
 PKV_API pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtype q_dtype,

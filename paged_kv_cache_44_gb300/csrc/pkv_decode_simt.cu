@@ -14,14 +14,10 @@
 // (3) thread e accumulates sum_t p_t * V[t][e] for every head.  A sequence
 // that fits one partition writes `out` directly; otherwise the partition's
 // (m, l, acc) goes to the workspace and the merge kernel combines them.
-#include <cuda_fp16.h>
 #include <math_constants.h>
-
-#include <type_traits>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
-#include "pkv_kv4.cuh"
 #include "pkv_merge.cuh"
 
 namespace pkv {
@@ -30,27 +26,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kChunk = 64;
 constexpr int kHeads = 8;       // query heads per CTA
-
-struct KV4 {};                  // the 4-bit cache
-
-// element e of K/V head kvh of the token in pool row `row`; V: of the value cache
-template <int D, typename CF, bool V>
-__device__ __forceinline__ float kv_elem(const DecodeParams& p, int row, int kvh, int e) {
-    const void* base = V ? p.vc : p.kc;
-    if constexpr (std::is_same_v<CF, KV4>) {
-        using F = Kv4<D>;
-        const int t = row % p.bs;
-        const unsigned char* blk = static_cast<const unsigned char*>(base) +
-                                   ((size_t)(row / p.bs) * p.Hkv + kvh) * kv4_head_bytes(p.bs, D);
-        const __half* par = reinterpret_cast<const __half*>(blk + F::codes(p.bs));
-        const int a = V ? F::v_par(t, e / 32) : F::k_par(t, e / 32);
-        const uint32_t w = reinterpret_cast<const uint32_t*>(blk)[V ? F::v_word(t, e) : F::k_word(t, e)];
-        const int sh = V ? 16 * (t % 2) + 4 * (e % 4) : 4 * (e % 8);
-        return fmaf(__half2float(par[a]), (float)((w >> sh) & 15u), __half2float(par[p.bs * F::G + a]));
-    } else {
-        return load_elem<CF>(base, ((size_t)row * p.Hkv + kvh) * D + e);
-    }
-}
 
 template <int D, typename QF, typename CF>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
@@ -100,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
     for (int h = 0; h < kHeads; ++h) acc[h] = 0.f;
     __syncthreads();
 
+    const size_t row_stride = (size_t)p.Hkv * D;   // elements between tokens of one block
     for (int c0 = t0; c0 < t1; c0 += kChunk) {
         const int cn = min(kChunk, t1 - c0);
         // physical row of each token of the chunk (-1 when its block id is bad or the query does not see it)
@@ -124,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
             float kv[D / 32];
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-                kv[i] = row >= 0 ? kv_elem<D, CF, false>(p, row, kvh, lane + 32 * i) : 0.f;
+                kv[i] = row >= 0 ? load_elem<CF>(p.kc, (size_t)row * row_stride + (size_t)kvh * D + lane + 32 * i) : 0.f;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 if (h >= nh) break;
@@ -170,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
             for (int tt = 0; tt < cn; ++tt) {
                 const int row = pb_s[tt];
                 if (row < 0) continue;
-                const float v = kv_elem<D, CF, true>(p, row, kvh, e);
+                const float v = load_elem<CF>(p.vc, (size_t)row * row_stride + (size_t)kvh * D + e);
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) acc[h] = fmaf(x_s[h][tt], v, acc[h]);
             }
@@ -262,13 +238,6 @@ cudaError_t launch_decode_simt(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype 
     if (p.d == 64)
         return q_dt == PKV_F32 ? launch_simt_q<64, F32>(p, c_dt, grid, st) : launch_simt_q<64, BF16>(p, c_dt, grid, st);
     return q_dt == PKV_F32 ? launch_simt_q<128, F32>(p, c_dt, grid, st) : launch_simt_q<128, BF16>(p, c_dt, grid, st);
-}
-
-cudaError_t launch_decode_kv4(const DecodeParams& p, int, cudaStream_t st) {
-    if (p.S == 0) return cudaSuccess;
-    const dim3 grid(p.Pmax, p.Hkv * ((p.g + kHeads - 1) / kHeads), p.S), block(kThreads);
-    return p.d == 64 ? launch_pdl(decode_simt_kernel<64, BF16, KV4>, grid, block, 0, st, p)
-                     : launch_pdl(decode_simt_kernel<128, BF16, KV4>, grid, block, 0, st, p);
 }
 
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st) {
