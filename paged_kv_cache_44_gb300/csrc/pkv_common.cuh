@@ -109,6 +109,15 @@ __host__ __device__ __forceinline__ int window_bound(int max_ctx, int window, in
     return b < max_ctx ? (int)b : max_ctx;
 }
 
+// The low x bits of a word, none for x <= 0, all for x >= 32.
+__device__ __forceinline__ uint32_t bits_below(int x) {
+    return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
+}
+// Bit b set: key v0 + b lies in [lo, hi).
+__device__ __forceinline__ uint32_t bits_between(int v0, int lo, int hi) {
+    return bits_below(hi - v0) & ~bits_below(lo - v0);
+}
+
 // ---- scalar element -> float (fp8: the code's value, scale applied by caller)
 
 __device__ __forceinline__ float to_float(float x) { return x; }

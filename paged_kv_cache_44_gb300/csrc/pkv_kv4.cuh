@@ -26,7 +26,7 @@ namespace pkv {
 constexpr int kKv4Group = 32;
 constexpr float kKv4Max = 65504.f;       // largest magnitude of a scaled value: fp16's
 
-__host__ __device__ __forceinline__ int kv4_head_bytes(int bs, int d) { return bs * (d / 2 + d / 8); }
+__host__ __device__ constexpr int kv4_head_bytes(int bs, int d) { return bs * (d / 2 + d / 8); }
 
 template <int D>
 struct Kv4 {

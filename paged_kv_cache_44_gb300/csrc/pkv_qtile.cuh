@@ -29,15 +29,6 @@ struct __align__(16) QTile {
     WindowSpan span;           // WIN: the tokens left out
 };
 
-// The low x bits of a word, none for x <= 0, all for x >= 32.
-__device__ __forceinline__ uint32_t bits_below(int x) {
-    return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
-}
-// Bit b set: key v0 + b lies in [lo, hi).
-__device__ __forceinline__ uint32_t bits_between(int v0, int lo, int hi) {
-    return bits_below(hi - v0) & ~bits_below(lo - v0);
-}
-
 // Keys of a row tile: how many its queries reach, in window_span's numbering with a window.
 __device__ __forceinline__ int qtile_keys(const DecodeParams& p, int n, int ql, int first_row, int last_row,
                                           int& first, WindowSpan& span) {
