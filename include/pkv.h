@@ -654,7 +654,7 @@ PKV_API pkv_status pkv_token_attention_decode_scored(void* out, const void* quer
  * slots, in order, for the caller's pool.  Arrays are [S, MT] (int32, fp32)
  * and [S]; entries past the counts are left as they were.  No output may
  * overlap an input or another output: a loop swaps two tables.
- * num_first + num_recent <= budget.  A count outside [0, MT] is clamped and
+ * num_first + num_recent <= budget; MT <= 2^30.  A count outside [0, MT] is clamped and
  * reported (PKV_DEVERR_CONTEXT_LEN).
  */
 PKV_API pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* scores, const int32_t* num_tokens,

@@ -62,6 +62,30 @@ int resolve_partition(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int re
     return P;
 }
 
+// The same for the windowed and the 4-bit decode (keys: the most tokens a
+// sequence reads).  A launch too small to fill the GPU is split further, down
+// to 64 tokens: one warp's pace (a 4-bit stage of 64 tokens alone takes about
+// 2 us), not bandwidth, is then the launch's length.  In 64- / 128- /
+// 256-token partitions and in one: a 4-bit sequence of 500 tokens 12.4 / 14.4
+// / 16.5 / 20.7 us; a window of 1,000 bf16 tokens over 8 sequences of 4 K/V
+// heads 14.6 / 17.0 / 20.6 / 55.5.  Beyond 48 partitions a row's merge costs
+// what that saves (one 4-bit sequence of 32,768 tokens: 69 us in 64, 45 in
+// 128, 28.7 in 256; a window of 4,100 bf16 tokens: 18.5 and 18.7).
+constexpr int kMinSplit = 64, kMaxSmallSplits = 48;
+int resolve_split(int S, int Hq, int Hkv, int d, int bs, int keys, int req) {
+    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, req);
+    if (P < 0 || req != 0 || keys <= kMinSplit) return P;
+    const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);
+    int p = P > 0 ? P : keys;
+    while (p > kMinSplit) {
+        const int half = max(kMinSplit, (p / 2 + 31) / 32 * 32);
+        const int n = (keys + half - 1) / half;
+        if (half >= p || sets * n > kSmallLaunchUnits || n > kMaxSmallSplits) break;
+        p = half;
+    }
+    return p < keys ? p : 0;
+}
+
 // The last, partial partition of a sequence is cut into chunks of Q tokens
 // (a quarter partition, a multiple of 32 tokens and so of the block size):
 // those chunks are the last units a launch hands out, so the launch ends on
@@ -77,6 +101,16 @@ int tail_chunk(int P) { return P >= 128 ? (P / 4) / 32 * 32 : P; }
 constexpr int kTailHold = 1;
 int tail_hold(pkv_dtype cache_dtype, bool tensor_cores) {
     return cache_dtype == PKV_FP8_E4M3 && tensor_cores ? kTailHold : 0;
+}
+
+// The 4-bit decode: partitions held back where the launch has fewer than
+// three units per worker (152 SMs x 11), so that its last round is made of
+// chunks.  128 sequences under a window of 2,048: 53.3 us held, 56.6 not; 64
+// of 512..4,096 tokens: 26.8 and 27.9; with five rounds (256 sequences of
+// 1..4,096) the small units cost more than they even out: 86.5 and 81.9.
+int kv4_hold(int S, int Hq, int Hkv, int keys, int P) {
+    const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);
+    return P > 0 && sets * ((keys + P - 1) / P) < 3LL * 152 * 11 ? kTailHold : 0;
 }
 
 // Partial results per row for lengths up to max_ctx with `hold` held-back
@@ -736,7 +770,7 @@ size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, i
     if (window < 0 || num_sinks < 0 || !decode_shape_ok(S, Hq, Hkv, d, bs, max_context_len)) return 0;
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
     return P < 0 ? 0 : make_plan(S, Hq, d, keys, P).bytes;
 }
 
@@ -754,7 +788,7 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     if (chk != PKV_OK || S == 0) return chk;
     clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
     const bool use_tc = kernel != PKV_DECODE_CUDA_CORES && decode_tc_supports(q_dtype, cache_dtype, d, bs, NB);
     const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
@@ -837,7 +871,7 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
     if (chk != PKV_OK || S == 0) return chk;
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
     if (pl.split && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
@@ -846,7 +880,7 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
     p.block_tables = block_tables; p.context_lens = context_lens; p.err = err_word;
     p.S = S; p.MB = MB; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.d = d; p.bs = bs; p.NB = NB;
     p.window = window; p.sinks = window > 0 ? num_sinks : 0;
-    set_partitions(p, pl, pl.P, MB * bs, 0);
+    set_partitions(p, pl, pl.P, MB * bs, kv4_hold(S, Hq, Hkv, keys, pl.P));
     p.max_ctx = max_context_len;
     p.logit_scale_log2 = scale * k_scale * kLog2e;
     p.out_scale = v_scale;
@@ -909,7 +943,7 @@ pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* scores, con
                             int32_t* new_num, int32_t* evicted, int32_t* err_word, pkv_stream_t stream) {
     if (S < 0 || MT < 1 || budget < 0 || num_first < 0 || num_recent < 0) return PKV_ERR_INVALID_ARG;
     if ((long long)num_first + num_recent > budget) return PKV_ERR_INVALID_ARG;
-    if (S > 65535) return PKV_ERR_UNSUPPORTED;
+    if (S > 65535 || MT > (1 << 30)) return PKV_ERR_UNSUPPORTED;
     if (S == 0) return PKV_OK;
     if (!token_slots || !scores || !num_tokens || !new_slots || !new_scores || !new_num) return PKV_ERR_INVALID_ARG;
     const size_t rows = (size_t)S * MT * 4, nums = (size_t)S * 4;

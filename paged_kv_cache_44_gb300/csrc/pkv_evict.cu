@@ -4,6 +4,7 @@
 // "LLM推論の「見えないメモリ問題」を解く … vToken", section on token eviction:
 // policies such as heavy hitters and sinks with a recent window pick the
 // tokens a sequence drops; the token table then lists the survivors.
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include "pkv_common.cuh"
@@ -90,12 +91,23 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, fl
 // rest, the `need` = budget - F - R with the largest scores, ties to the
 // lowest index.  Scores are compared as 32-bit keys that order as the floats
 // do (NaN lowest, -0 = +0).  The need-th largest key T is found digit by
-// digit (four 8-bit histograms); then one pass in token order keeps a token
-// when its key is above T, or equals T and fewer than need - #(above T)
-// equal ones came before it.  A kept token's place is the number kept before
-// it, a dropped one's the number dropped before it: the order is preserved.
+// digit (histograms of 11, 11 and 10 bits); then a token is kept when its key
+// is above T, or equals T and fewer than need - #(above T) equal ones come
+// before it.  A kept token's place is the number kept before it, a dropped
+// one's the number dropped before it: the order is preserved.
+//
+// The floor is 8 bytes in and 8 (kept) or 4 (dropped) out per token, a few
+// us even for 64 sequences of 32,768; what costs is the chain of dependent
+// steps.  So a sequence is spread over a cluster of CTAs that keep their
+// share of the keys in registers (one read of the scores), add up their
+// histograms and counts through distributed shared memory, and each find T
+// for themselves: four cluster barriers in all.  The cluster grows while the
+// grid still fits the GPU in one wave; a share that does not fit the
+// registers (more than 8,192 tokens) is read again in every step instead.
 
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictKeys = 16;                       // per thread, in registers
+constexpr int kBins = 2048, kBinsPerThread = kBins / kEvictThreads;
 
 __device__ __forceinline__ uint32_t score_key(float f) {
     if (f != f) return 0u;
@@ -103,90 +115,159 @@ __device__ __forceinline__ uint32_t score_key(float f) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t pick[2];          // digit of T, tokens still to find at or below it
-    __shared__ uint32_t warp_sum[32];
-    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// REG: every CTA's share fits its registers.
+template <bool REG>
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    __shared__ __align__(16) uint32_t hist[3][kBins];
+    __shared__ uint32_t warp_a[kEvictWarps], warp_b[kEvictWarps], pick[2], counts[2];
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int s = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
+    for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
     pdl_wait();
     int n = p.num_tokens[s];
     if (n < 0 || n > p.MT) {
-        if (tid == 0) report(p.err, PKV_DEVERR_CONTEXT_LEN);
+        if (rank == 0 && tid == 0) report(p.err, PKV_DEVERR_CONTEXT_LEN);
         n = n < 0 ? 0 : p.MT;
     }
     const size_t row = (size_t)s * p.MT;
     const bool all = n <= p.budget;
-    if (tid == 0) p.new_num[s] = all ? n : p.budget;
+    if (rank == 0 && tid == 0) p.new_num[s] = all ? n : p.budget;
     const int lo = p.first, hi = n - p.recent;       // tokens [lo, hi) compete
     const uint32_t need = all ? 0u : (uint32_t)(p.budget - p.first - p.recent);
-    uint32_t T = 0xffffffffu, left = 0;              // left: tokens of key T to keep
+
+    // rank r's tokens are [r * 32 * W * turns, ...), warp w's 32 * turns of them in order
+    const int turns = (n + ranks * kEvictThreads - 1) / (ranks * kEvictThreads);
+    const int base = (rank * kEvictWarps + warp) * 32 * turns + lane;
+    uint32_t keys[REG ? kEvictKeys : 1];
+    if constexpr (REG) {
+#pragma unroll
+        for (int i = 0; i < kEvictKeys; ++i)
+            if (i < turns && base + 32 * i < n) keys[i] = score_key(__ldg(p.scores + row + base + 32 * i));
+    }
+    // f(i, token, key) for this thread's tokens in order; every lane of a warp takes part in each turn
+    auto each = [&](auto f) {
+        if constexpr (REG) {
+#pragma unroll
+            for (int i = 0; i < kEvictKeys; ++i)
+                if (i < turns) f(base + 32 * i, keys[i]);
+        } else {
+            for (int i = 0; i < turns; ++i) {
+                const int t = base + 32 * i;
+                f(t, t < n ? score_key(__ldg(p.scores + row + t)) : 0u);
+            }
+        }
+    };
+
+    uint32_t T = 0xffffffffu, left = 0;              // keep keys above T, and `left` of key T
     if (need > 0) {
         T = 0;
         left = need;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-            __syncthreads();
-            for (int t = lo + tid; t < hi; t += kEvictThreads) {
-                const uint32_t k = score_key(p.scores[row + t]);
-                if (shift == 24 || (k >> (shift + 8)) == (T >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        __syncthreads();
+#pragma unroll
+        for (int step = 0; step < 3; ++step) {
+            const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
+            const uint32_t mask = step == 2 ? 1023u : 2047u;
+            each([&](int t, uint32_t k) {
+                const bool mine = step == 0 || (k >> (shift + (step == 1 ? 11 : 10))) == (T >> (shift + (step == 1 ? 11 : 10)));
+                if (t >= lo && t < hi && mine) atomicAdd(&hist[step][(k >> shift) & mask], 1u);
+            });
+            cluster.sync();
+            // bins 4 tid .. 4 tid + 3 over the cluster, then how many keys lie in higher bins
+            uint32_t h[kBinsPerThread] = {0u, 0u, 0u, 0u};
+            for (int r = 0; r < ranks; ++r) {
+                const uint4 v = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[step][0], r))[tid];
+                h[0] += v.x; h[1] += v.y; h[2] += v.z; h[3] += v.w;
             }
+            const uint32_t own = h[0] + h[1] + h[2] + h[3];
+            uint32_t up = own;                       // of this thread and the lanes above it
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_down_sync(0xffffffffu, up, o);
+                if (lane + o < 32) up += u;
+            }
+            if (lane == 0) warp_a[warp] = up;
             __syncthreads();
-            if (tid == 0) {
-                int dg = 255;
-                uint32_t want = left;
-                while (dg > 0 && hist[dg] < want) want -= hist[dg--];
-                pick[0] = (uint32_t)dg;
-                pick[1] = want;
+            for (int w = warp + 1; w < kEvictWarps; ++w) up += warp_a[w];
+            uint32_t above = up - own;
+            if (above < left && up >= left) {        // T's digit is one of this thread's four
+                int j = kBinsPerThread - 1;
+                while (above + h[j] < left) above += h[j--];
+                pick[0] = (uint32_t)(kBinsPerThread * tid + j);
+                pick[1] = left - above;
             }
             __syncthreads();
             T |= pick[0] << shift;
             left = pick[1];
         }
     }
-    uint32_t above = 0, equal = 0;                   // kept above T, and of key T, before this pass
-    for (int c0 = 0; c0 < n; c0 += kEvictThreads) {
-        const int t = c0 + tid;
-        const bool fixed = t < lo || t >= hi || all;
-        float sc = 0.f;
-        int slot = 0;
-        uint32_t v = 0;                              // (equal to T) << 16 | above T or fixed
+    // what a token is to the sequence: kept for certain, a candidate of key T, or dropped
+    auto kept = [&](int t, uint32_t k) { return t < n && (all || t < lo || t >= hi || (need > 0 && k > T)); };
+    auto tied = [&](int t, uint32_t k) { return need > 0 && t >= lo && t < hi && k == T; };
+    uint32_t a = 0, b = 0;                           // of this warp
+    each([&](int t, uint32_t k) {
+        a += __popc(__ballot_sync(0xffffffffu, kept(t, k)));
+        b += __popc(__ballot_sync(0xffffffffu, tied(t, k)));
+    });
+    __syncthreads();
+    if (lane == 0) {
+        warp_a[warp] = a;
+        warp_b[warp] = b;
+    }
+    __syncthreads();
+    uint32_t ta = 0, tb = 0;                         // before this warp, first in the CTA
+    a = b = 0;
+    for (int w = 0; w < kEvictWarps; ++w) {
+        if (w == warp) {
+            a = ta;
+            b = tb;
+        }
+        ta += warp_a[w];
+        tb += warp_b[w];
+    }
+    if (ranks > 1) {
+        if (tid == 0) {
+            counts[0] = ta;
+            counts[1] = tb;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t* c = cluster.map_shared_rank(&counts[0], r);
+            a += c[0];
+            b += c[1];
+        }
+        // no CTA leaves while another may still read its counts
+        cluster.barrier_arrive();
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    each([&](int t, uint32_t k) {
+        const bool in = kept(t, k), tie = tied(t, k);
+        const uint32_t ba = __ballot_sync(0xffffffffu, in), bb = __ballot_sync(0xffffffffu, tie);
+        const uint32_t eq = b + __popc(bb & below);  // of key T before this token
+        const uint32_t place = a + __popc(ba & below) + min(eq, left);
         if (t < n) {
-            sc = p.scores[row + t];
-            slot = p.token_slots[row + t];
-            const uint32_t k = score_key(sc);
-            v = fixed ? 1u : (need == 0 ? 0u : (k > T ? 1u : (k == T ? 0x10000u : 0u)));
-        }
-        uint32_t inc = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) warp_sum[warp] = inc;
-        __syncthreads();
-        uint32_t before = 0, total = 0;
-        for (int w = 0; w < kEvictThreads / 32; ++w) {
-            const uint32_t x = warp_sum[w];
-            before += w < warp ? x : 0u;
-            total += x;
-        }
-        __syncthreads();
-        const uint32_t ex = before + inc - v;
-        const uint32_t eq0 = equal + (ex >> 16);
-        const uint32_t place = above + (ex & 0xffffu) + min(eq0, left);
-        if (t < n) {
-            const bool keep = (v & 0xffffu) || (v != 0 && eq0 < left);
-            if (keep) {
+            const int slot = __ldg(p.token_slots + row + t);
+            if (in || (tie && eq < left)) {
                 p.new_slots[row + place] = slot;
-                p.new_scores[row + place] = sc;
+                p.new_scores[row + place] = __ldg(p.scores + row + t);
             } else if (p.evicted != nullptr) {
                 p.evicted[row + t - place] = slot;
             }
         }
-        above += total & 0xffffu;
-        equal += total >> 16;
-    }
+        a += __popc(ba);
+        b += __popc(bb);
+    });
+    if (ranks > 1) cluster.barrier_wait();
+}
+
+// CTAs per sequence: a cluster of up to 16, doubled while a share is above
+// 1,024 tokens and the grid still fits the GPU's two CTAs per SM.
+int evict_cluster(int S, int MT) {
+    int c = 1;
+    while (c < 16 && (MT + c - 1) / c > 1024 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
+    return c;
 }
 
 }  // namespace
@@ -199,7 +280,27 @@ cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStrea
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
-    return launch_pdl(evict_kernel, dim3((unsigned)p.S), dim3(kEvictThreads), 0, st, p);
+    const int c = evict_cluster(p.S, p.MT);
+    const bool reg = (p.MT + c - 1) / c <= kEvictThreads * kEvictKeys;
+    auto kern = reg ? evict_kernel<true> : evict_kernel<false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.S * c));
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)c;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (c > 8) {       // more than the portable cluster size, allowed per kernel and context
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace pkv

@@ -76,7 +76,7 @@ def test_scored_decode(kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(S=-1), 1), (dict(S=0), 0), (dict(S=65536), 2), (dict(MT=0), 1), (dict(budget=-1), 1), (dict(first=-1), 1),
+    (dict(S=-1), 1), (dict(S=0), 0), (dict(S=65536), 2), (dict(MT=0), 1), (dict(MT=(1 << 30) + 1), 2), (dict(budget=-1), 1), (dict(first=-1), 1),
     (dict(recent=-1), 1), (dict(first=50, recent=51), 1), (dict(first=2 ** 31 - 1, recent=2 ** 31 - 1, budget=2 ** 31 - 1), 1),
     (dict(slots=None), 1), (dict(new_num=None), 1), (dict(new_slots=A), 1), (dict(new_slots=A + 2396), 1),
     (dict(new_scores=4 * A), 1), (dict(evicted=5 * A), 1), (dict(evicted=2 * A + 1200), 1), (dict(new_num=3 * A), 1),
