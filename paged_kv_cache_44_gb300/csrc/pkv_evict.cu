@@ -106,8 +106,20 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, fl
 // registers (more than 8,192 tokens) is read again in every step instead.
 
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictKeys = 16;                       // per thread, in registers
-constexpr int kBins = 2048, kBinsPerThread = kBins / kEvictThreads;
+constexpr int kEvictHeld = 16384;                    // keys per CTA, in shared memory
+constexpr int kBins = 2048, kMaxRanks = 16;
+static_assert(kBins == 4 * kEvictThreads && kBins == 64 * 32, "four bins per thread, 64 sums of 32 bins");
+
+// Sum of the values of the lanes above this one.
+__device__ __forceinline__ uint32_t lanes_above(uint32_t v, int lane) {
+    uint32_t up = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_down_sync(0xffffffffu, up, o);
+        if (lane + o < 32) up += u;
+    }
+    return up - v;
+}
 
 __device__ __forceinline__ uint32_t score_key(float f) {
     if (f != f) return 0u;
@@ -115,17 +127,20 @@ __device__ __forceinline__ uint32_t score_key(float f) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// REG: every CTA's share fits its registers.
-template <bool REG>
+// HELD: every CTA's share fits its shared memory.
+template <bool HELD>
 __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ uint32_t keys[];               // HELD: of this CTA's tokens, in order
     __shared__ __align__(16) uint32_t hist[3][kBins];
+    __shared__ __align__(16) uint32_t coarse[3][kBins / 32];
     __shared__ uint32_t warp_a[kEvictWarps], warp_b[kEvictWarps], pick[2], counts[2];
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int s = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
-    for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kBins / 4; i += kEvictThreads)
+        reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     int n = p.num_tokens[s];
     if (n < 0 || n > p.MT) {
@@ -138,26 +153,25 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     const int lo = p.first, hi = n - p.recent;       // tokens [lo, hi) compete
     const uint32_t need = all ? 0u : (uint32_t)(p.budget - p.first - p.recent);
 
-    // rank r's tokens are [r * 32 * W * turns, ...), warp w's 32 * turns of them in order
+    // rank r's tokens are [r * 512 * turns, ...), warp w's 32 * turns of them in order
     const int turns = (n + ranks * kEvictThreads - 1) / (ranks * kEvictThreads);
     const int base = (rank * kEvictWarps + warp) * 32 * turns + lane;
-    uint32_t keys[REG ? kEvictKeys : 1];
-    if constexpr (REG) {
-#pragma unroll
-        for (int i = 0; i < kEvictKeys; ++i)
-            if (i < turns && base + 32 * i < n) keys[i] = score_key(__ldg(p.scores + row + base + 32 * i));
-    }
-    // f(i, token, key) for this thread's tokens in order; every lane of a warp takes part in each turn
+    uint32_t* own = keys + warp * 32 * turns + lane;
+    if (HELD && need > 0)
+#pragma unroll 4
+        for (int i = 0; i < turns; ++i)
+            own[32 * i] = base + 32 * i < n ? score_key(__ldg(p.scores + row + base + 32 * i)) : 0u;
+    // f(token, key) for this thread's tokens in order; every lane of a warp takes part in each turn
     auto each = [&](auto f) {
-        if constexpr (REG) {
-#pragma unroll
-            for (int i = 0; i < kEvictKeys; ++i)
-                if (i < turns) f(base + 32 * i, keys[i]);
-        } else {
-            for (int i = 0; i < turns; ++i) {
-                const int t = base + 32 * i;
-                f(t, t < n ? score_key(__ldg(p.scores + row + t)) : 0u);
+#pragma unroll 4
+        for (int i = 0; i < turns; ++i) {
+            const int t = base + 32 * i;
+            uint32_t k = 0u;
+            if (need > 0) {
+                if constexpr (HELD) k = own[32 * i];
+                else k = t < n ? score_key(__ldg(p.scores + row + t)) : 0u;
             }
+            f(t, k);
         }
     };
 
@@ -166,37 +180,50 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         T = 0;
         left = need;
         __syncthreads();
-#pragma unroll
+        // one copy of the code for the three digits: a launch runs it once, and fetching it is part of the time
+#pragma unroll 1
         for (int step = 0; step < 3; ++step) {
             const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
-            const uint32_t mask = step == 2 ? 1023u : 2047u;
+            const int width = step == 2 ? 10 : 11;
+            const uint32_t mask = (1u << width) - 1u;
+            uint32_t* bins = hist[step];
             each([&](int t, uint32_t k) {
-                const bool mine = step == 0 || (k >> (shift + (step == 1 ? 11 : 10))) == (T >> (shift + (step == 1 ? 11 : 10)));
-                if (t >= lo && t < hi && mine) atomicAdd(&hist[step][(k >> shift) & mask], 1u);
+                const bool mine = step == 0 || ((k ^ T) >> (shift + width)) == 0;
+                if (t >= lo && t < hi && mine) atomicAdd(&bins[(k >> shift) & mask], 1u);
             });
-            cluster.sync();
-            // bins 4 tid .. 4 tid + 3 over the cluster, then how many keys lie in higher bins
-            uint32_t h[kBinsPerThread] = {0u, 0u, 0u, 0u};
-            for (int r = 0; r < ranks; ++r) {
-                const uint4 v = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[step][0], r))[tid];
-                h[0] += v.x; h[1] += v.y; h[2] += v.z; h[3] += v.w;
-            }
-            const uint32_t own = h[0] + h[1] + h[2] + h[3];
-            uint32_t up = own;                       // of this thread and the lanes above it
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_down_sync(0xffffffffu, up, o);
-                if (lane + o < 32) up += u;
-            }
-            if (lane == 0) warp_a[warp] = up;
             __syncthreads();
-            for (int w = warp + 1; w < kEvictWarps; ++w) up += warp_a[w];
-            uint32_t above = up - own;
-            if (above < left && up >= left) {        // T's digit is one of this thread's four
-                int j = kBinsPerThread - 1;
-                while (above + h[j] < left) above += h[j--];
-                pick[0] = (uint32_t)(kBinsPerThread * tid + j);
-                pick[1] = left - above;
+            // sums of 32 bins: eight threads of four bins each
+            const uint4 v = reinterpret_cast<const uint4*>(bins)[tid];
+            uint32_t sum = v.x + v.y + v.z + v.w;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane % 8 == 0) coarse[step][tid / 8] = sum;
+            if (ranks > 1) cluster.sync();
+            else __syncthreads();
+            // one warp reads the cluster's 64 sums, then the 32 bins of the sum that T's digit is in
+            if (warp == 0) {
+                uint32_t h0 = 0, h1 = 0;                 // sums 2 lane, 2 lane + 1
+#pragma unroll 8
+                for (int r = 0; r < ranks; ++r) {
+                    const uint2 u = reinterpret_cast<const uint2*>(cluster.map_shared_rank(&coarse[step][0], r))[lane];
+                    h0 += u.x;
+                    h1 += u.y;
+                }
+                uint32_t above = lanes_above(h0 + h1, lane);
+                const bool here = above < left && above + h0 + h1 >= left;
+                const bool upper = above + h1 >= left;   // of the two sums, the higher one
+                if (!upper) above += h1;
+                const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+                const int group = __shfl_sync(0xffffffffu, 2 * lane + (upper ? 1 : 0), src);
+                const uint32_t want = left - __shfl_sync(0xffffffffu, above, src);
+                uint32_t h = 0;                          // bin 32 group + lane
+#pragma unroll 8
+                for (int r = 0; r < ranks; ++r) h += cluster.map_shared_rank(bins, r)[32 * group + lane];
+                above = lanes_above(h, lane);
+                if (above < want && above + h >= want) {
+                    pick[0] = (uint32_t)(32 * group + lane);
+                    pick[1] = want - above;
+                }
             }
             __syncthreads();
             T |= pick[0] << shift;
@@ -266,7 +293,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
 // 1,024 tokens and the grid still fits the GPU's two CTAs per SM.
 int evict_cluster(int S, int MT) {
     int c = 1;
-    while (c < 16 && (MT + c - 1) / c > 1024 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
+    while (c < kMaxRanks && (MT + c - 1) / c > 1024 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
     return c;
 }
 
@@ -281,11 +308,18 @@ cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStrea
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
     const int c = evict_cluster(p.S, p.MT);
-    const bool reg = (p.MT + c - 1) / c <= kEvictThreads * kEvictKeys;
-    auto kern = reg ? evict_kernel<true> : evict_kernel<false>;
+    const int share = ((p.MT + c - 1) / c + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
+    const bool held = share <= kEvictHeld;
+    auto kern = held ? evict_kernel<true> : evict_kernel<false>;
+    static SmemOptIn optin;
+    if (held) {
+        const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kEvictHeld * sizeof(uint32_t));
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.S * c));
     cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = held ? share * sizeof(uint32_t) : 0;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
