@@ -197,10 +197,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_reduce_kernel(DecodeP
     n = n < 0 ? 0 : min(n, p.max_ctx);     // same clamp as the decode kernel: np <= Pmax
     if (p.window > 0) n -= window_span(n - p.window, p.sinks, p.bs).gap;
     const int np = num_partitions(n, p.P, p.Q, p.hold);
-    if (np <= 1) return;
     const size_t u0 = ((size_t)s * p.Hq + h) * p.Pmax;
-    float o[E];
-    const float L = merge_partitions<D>(p.part_ml + 2 * u0, p.part_acc + u0 * D, np, lane, o);
+    if (np <= 1) {
+        // a scored decode wants every row's (max, sum) in one place; without tokens there is none
+        if (p.row_ml != nullptr && lane < 2) p.row_ml[2 * gw + lane] = n > 0 ? p.part_ml[2 * u0 + lane] : 0.f;
+        return;
+    }
+    float o[E], M;
+    const float L = merge_partitions<D>(p.part_ml + 2 * u0, p.part_acc + u0 * D, np, lane, o, &M);
+    if (p.row_ml != nullptr && lane == 0) reinterpret_cast<float2*>(p.row_ml)[gw] = make_float2(M, L);
     const float f = L > 0.f ? p.out_scale / L : 0.f;
     const size_t ob = ((size_t)s * p.Hq + h) * D + lane * E;
 #pragma unroll

@@ -5,7 +5,6 @@
 // policies such as heavy hitters and sinks with a recent window pick the
 // tokens a sequence drops; the token table then lists the survivors.
 #include <cooperative_groups.h>
-#include <math_constants.h>
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
@@ -18,71 +17,71 @@ namespace {
 // ------------------------------------------------------------------- scores
 //
 // score[s][t] += sum over the query heads h of 2^(x[s][h][t] - M) / L, with
-// the logits x the scored decode stored and the (M, L) of row (s, h) merged
-// from its partitions.  One thread owns a token and adds its heads in order,
-// so the sum is the same in every launch (no atomics).
+// the logits x the scored decode stored and each row's (M, L), merged from
+// its partitions.  One thread owns a token and adds its heads in order, so
+// the sum is the same in every launch (no atomics).  The bound is the read
+// of the logits, 4 bytes per token and head: a head set's row of a token is
+// 32 consecutive bytes, a thread keeps kSets of them (two 16-byte loads
+// each) in flight.
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreTokens = 1024;       // per CTA
 constexpr int kScoreRows = 512;          // (set, head) rows whose (M, 1 / L) are staged at a time
+constexpr int kSets = 4;                 // head sets a thread loads at once
 
+template <int W>                         // heads per row of logits
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, float* __restrict__ scores, int MT) {
-    __shared__ float2 ml[kScoreRows];    // (M, 1 / L); (0, 0) for a row without tokens or past the set's heads
-    const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float2 ml[kScoreRows];    // (M, 1 / L); 1 / L = 0 for a row without weight or past the set's heads
+    const int s = blockIdx.y, tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
     int n = p.context_lens[s];
     n = n < 0 ? 0 : min(n, p.max_ctx);   // the decode's clamp
-    const int t0 = blockIdx.x * kScoreTokens;
-    if (t0 >= n) return;
-    const int np = num_partitions(n, p.P, p.Q, p.hold);
-    const int W = score_width(p.g), nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit;
-    const int sets = p.Hkv * nsets, tile = kScoreRows / W;
-    constexpr int K = kScoreTokens / kScoreThreads;
-    float sum[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) sum[k] = 0.f;
-    for (int b0 = 0; b0 < sets; b0 += tile) {
-        const int bn = min(tile, sets - b0);
+    if ((int)(blockIdx.x * kScoreThreads) >= n) return;
+    const int t = blockIdx.x * kScoreThreads + tid;
+    const int nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit, sets = p.Hkv * nsets;
+    constexpr int kTile = kScoreRows / W;
+    float sum = 0.f;
+    for (int b0 = 0; b0 < sets; b0 += kTile) {
+        const int bn = min(kTile, sets - b0);
         __syncthreads();
-        for (int i = warp; i < bn * W; i += kScoreThreads / 32) {
-            const int set = b0 + i / W, j = i % W;
-            const int kvh = set / nsets, hg = (set - kvh * nsets) * kHeadsPerUnit + j;
-            float M = -CUDART_INF_F, L = 0.f;
-            if (hg < p.g) {
-                const float2* src = reinterpret_cast<const float2*>(p.part_ml) + ((size_t)s * p.Hq + kvh * p.g + hg) * p.Pmax;
-                for (int q = lane; q < np; q += 32) M = fmaxf(M, src[q].x);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                if (M != -CUDART_INF_F)
-                    for (int q = lane; q < np; q += 32) L += src[q].y * exp2f(src[q].x - M);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            }
-            if (lane == 0) ml[i] = L > 0.f ? make_float2(M, 1.f / L) : make_float2(0.f, 0.f);
+        for (int i = tid; i < bn * W; i += kScoreThreads) {
+            const int set = b0 + i / W, kvh = set / nsets, hg = (set - kvh * nsets) * kHeadsPerUnit + i % W;
+            float2 v = make_float2(0.f, 0.f);
+            if (hg < p.g) v = __ldg(reinterpret_cast<const float2*>(p.row_ml) + (size_t)s * p.Hq + kvh * p.g + hg);
+            ml[i] = v.y > 0.f ? make_float2(v.x, 1.f / v.y) : make_float2(0.f, 0.f);
         }
         __syncthreads();
-        for (int b = 0; b < bn; ++b) {
-            const float* x = p.logits + ((size_t)s * sets + b0 + b) * p.max_ctx * W;
+        const float* x = p.logits + (((size_t)s * sets + b0) * p.max_ctx + t) * W;
+        const size_t set_stride = (size_t)p.max_ctx * W;
+        for (int b = 0; b < bn && t < n; b += kSets) {
+            float v[kSets][W];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int t = t0 + tid + k * kScoreThreads;
-                if (t >= n) continue;
-                for (int j = 0; j < W; j += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(x + (size_t)t * W + j);
-                    const float2 a = ml[b * W + j], c = ml[b * W + j + 1];
-                    // a row without weight (L = 0) adds nothing, whatever its logits are
-                    if (a.y > 0.f) sum[k] = fmaf(tc::fast_exp2(v.x - a.x), a.y, sum[k]);
-                    if (c.y > 0.f) sum[k] = fmaf(tc::fast_exp2(v.y - c.x), c.y, sum[k]);
+            for (int k = 0; k < kSets; ++k) {
+                const float* src = x + (b + k) * set_stride;
+#pragma unroll
+                for (int j = 0; j < W; j += (W % 4 ? 2 : 4)) {
+                    if (b + k >= bn) continue;
+                    if constexpr (W % 4 == 0) {
+                        const float4 q = __ldcs(reinterpret_cast<const float4*>(src + j));
+                        v[k][j] = q.x; v[k][j + 1] = q.y; v[k][j + 2] = q.z; v[k][j + 3] = q.w;
+                    } else {
+                        const float2 q = __ldcs(reinterpret_cast<const float2*>(src + j));
+                        v[k][j] = q.x; v[k][j + 1] = q.y;
+                    }
                 }
             }
+#pragma unroll
+            for (int k = 0; k < kSets; ++k)
+                if (b + k < bn)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        const float2 a = ml[(b + k) * W + j];
+                        // a row without weight adds nothing, whatever its logits are
+                        if (a.y > 0.f) sum = fmaf(tc::fast_exp2(v[k][j] - a.x), a.y, sum);
+                    }
         }
     }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int t = t0 + tid + k * kScoreThreads;
-        if (t < n) scores[(size_t)s * MT + t] += sum[k];
-    }
+    if (t < n) scores[(size_t)s * MT + t] += sum;
 }
 
 // ----------------------------------------------------------------- eviction
@@ -157,10 +156,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     const int turns = (n + ranks * kEvictThreads - 1) / (ranks * kEvictThreads);
     const int base = (rank * kEvictWarps + warp) * 32 * turns + lane;
     uint32_t* own = keys + warp * 32 * turns + lane;
-    if (HELD && need > 0)
-#pragma unroll 4
-        for (int i = 0; i < turns; ++i)
-            own[32 * i] = base + 32 * i < n ? score_key(__ldg(p.scores + row + base + 32 * i)) : 0u;
+    constexpr int kBatch = 8;                        // loads in flight per thread
+    if (HELD && need > 0) {
+        for (int i0 = 0; i0 < turns; i0 += kBatch) {
+            float v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int t = base + 32 * (i0 + j);
+                v[j] = i0 + j < turns && t < n ? __ldg(p.scores + row + t) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (i0 + j < turns) own[32 * (i0 + j)] = score_key(v[j]);
+        }
+    }
     // f(token, key) for this thread's tokens in order; every lane of a warp takes part in each turn
     auto each = [&](auto f) {
 #pragma unroll 4
@@ -269,23 +278,35 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         cluster.barrier_arrive();
     }
     const uint32_t below = (1u << lane) - 1u;
-    each([&](int t, uint32_t k) {
-        const bool in = kept(t, k), tie = tied(t, k);
-        const uint32_t ba = __ballot_sync(0xffffffffu, in), bb = __ballot_sync(0xffffffffu, tie);
-        const uint32_t eq = b + __popc(bb & below);  // of key T before this token
-        const uint32_t place = a + __popc(ba & below) + min(eq, left);
-        if (t < n) {
-            const int slot = __ldg(p.token_slots + row + t);
-            if (in || (tie && eq < left)) {
-                p.new_slots[row + place] = slot;
-                p.new_scores[row + place] = __ldg(p.scores + row + t);
-            } else if (p.evicted != nullptr) {
-                p.evicted[row + t - place] = slot;
-            }
+    for (int i0 = 0; i0 < turns; i0 += kBatch) {
+        int slot[kBatch];
+        float sc[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int t = base + 32 * (i0 + j);
+            const bool on = i0 + j < turns && t < n;
+            slot[j] = on ? __ldg(p.token_slots + row + t) : 0;
+            sc[j] = on ? __ldg(p.scores + row + t) : 0.f;
         }
-        a += __popc(ba);
-        b += __popc(bb);
-    });
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i0 + j >= turns) break;
+            const int t = base + 32 * (i0 + j);
+            const uint32_t k = score_key(sc[j]);
+            const bool in = kept(t, k), tie = tied(t, k);
+            const uint32_t ba = __ballot_sync(0xffffffffu, in), bb = __ballot_sync(0xffffffffu, tie);
+            const uint32_t eq = b + __popc(bb & below);  // of key T before this token
+            const uint32_t place = a + __popc(ba & below) + min(eq, left);
+            if (in || (tie && eq < left)) {
+                p.new_slots[row + place] = slot[j];
+                p.new_scores[row + place] = sc[j];
+            } else if (t < n && p.evicted != nullptr) {
+                p.evicted[row + t - place] = slot[j];
+            }
+            a += __popc(ba);
+            b += __popc(bb);
+        }
+    }
     if (ranks > 1) cluster.barrier_wait();
 }
 
@@ -301,8 +322,13 @@ int evict_cluster(int S, int MT) {
 
 cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStream_t st) {
     if (p.S == 0 || p.max_ctx == 0) return cudaSuccess;
-    const dim3 grid((unsigned)((p.max_ctx + kScoreTokens - 1) / kScoreTokens), (unsigned)p.S);
-    return launch_pdl(score_kernel, grid, dim3(kScoreThreads), 0, st, p, scores, MT);
+    const dim3 grid((unsigned)((p.max_ctx + kScoreThreads - 1) / kScoreThreads), (unsigned)p.S), block(kScoreThreads);
+    switch (score_width(p.g)) {
+        case 2: return launch_pdl(score_kernel<2>, grid, block, 0, st, p, scores, MT);
+        case 4: return launch_pdl(score_kernel<4>, grid, block, 0, st, p, scores, MT);
+        case 6: return launch_pdl(score_kernel<6>, grid, block, 0, st, p, scores, MT);
+        default: return launch_pdl(score_kernel<8>, grid, block, 0, st, p, scores, MT);
+    }
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {

@@ -152,6 +152,7 @@ struct DecodeParams {
     // scored token-table decode: the logits (log2 units) of each unit's
     // tokens, rows of score_width(g) heads, [S][Hkv * head sets][max_ctx]
     float* logits;
+    float* row_ml;            // scored: the merged (max, sum) of every row, [S][Hq][2] (part_ml when not split)
 };
 
 struct EvictParams {

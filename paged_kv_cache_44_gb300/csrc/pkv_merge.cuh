@@ -39,11 +39,12 @@ __device__ __forceinline__ void merge_load_row(const float* src, float (&a)[E], 
 
 // ml: the (m, l) pairs of the row's partitions [np][2]; acc: their rows
 // [np][D].  Lane i ends with o = elements [i*E, i*E+E) of sum 2^(m_p - M)
-// acc_p; returns L (the same on every lane).  The data were written by
+// acc_p; returns L (the same on every lane) and, in *Mout, M.  The data were written by
 // another kernel: loads go through L2 (ld.global.cg).
 template <int D>
 __device__ __forceinline__ float merge_partitions(const float* __restrict__ ml, const float* __restrict__ acc,
-                                                  int np, int lane, float (&o)[D / 32]) {
+                                                  int np, int lane, float (&o)[D / 32],
+                                                  float* Mout = nullptr) {
     constexpr int E = D / 32, B = kMergeChunk;
     const uint64_t once = l2_policy_evict_first();
     float M = -CUDART_INF_F, lpart = 0.f;
@@ -87,6 +88,7 @@ __device__ __forceinline__ float merge_partitions(const float* __restrict__ ml, 
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lpart += __shfl_xor_sync(0xffffffffu, lpart, off);
+    if (Mout != nullptr) *Mout = M;
     return lpart;
 }
 
