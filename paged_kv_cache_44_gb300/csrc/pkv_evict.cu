@@ -120,8 +120,13 @@ __device__ __forceinline__ uint32_t lanes_above(uint32_t v, int lane) {
     return up - v;
 }
 
+// Order of the floats as 32-bit keys: 2 for a NaN, then -inf = 0x007fffff up
+// to +inf = 0xff800000.  The values outside are free for what has no score in
+// the choice: kFixed is above every T and alone in the last bin, kNone (past
+// the sequence's end) below every T.
+constexpr uint32_t kFixed = 0xffffffffu, kNone = 0u;
 __device__ __forceinline__ uint32_t score_key(float f) {
-    if (f != f) return 0u;
+    if (f != f) return 2u;
     const uint32_t u = f == 0.f ? 0u : __float_as_uint(f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -131,7 +136,7 @@ template <bool HELD>
 __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ uint32_t keys[];               // HELD: of this CTA's tokens, in order
+    extern __shared__ __align__(16) uint32_t keys[];   // HELD: of this CTA's tokens, in order
     __shared__ __align__(16) uint32_t hist[3][kBins];
     __shared__ __align__(16) uint32_t coarse[3][kBins / 32];
     __shared__ uint32_t warp_a[kEvictWarps], warp_b[kEvictWarps], pick[2], counts[2];
@@ -155,7 +160,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     // rank r's tokens are [r * 512 * turns, ...), warp w's 32 * turns of them in order
     const int turns = (n + ranks * kEvictThreads - 1) / (ranks * kEvictThreads);
     const int base = (rank * kEvictWarps + warp) * 32 * turns + lane;
-    uint32_t* own = keys + warp * 32 * turns + lane;
+    uint32_t* own = keys + warp * 32 * turns;        // this warp's
+    // without a choice to make: every token is fixed (all), or only the first and the recent ones (need 0)
+    auto key_of = [&](int t, float sc) {
+        if (t >= n) return kNone;
+        if (t < lo || t >= hi || all) return kFixed;
+        return need > 0 ? score_key(sc) : 1u;
+    };
     constexpr int kBatch = 8;                        // loads in flight per thread
     if (HELD && need > 0) {
         for (int i0 = 0; i0 < turns; i0 += kBatch) {
@@ -167,24 +178,32 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                if (i0 + j < turns) own[32 * (i0 + j)] = score_key(v[j]);
+                if (i0 + j < turns) own[32 * (i0 + j) + lane] = key_of(base + 32 * (i0 + j), v[j]);
         }
+        __syncwarp();
     }
-    // f(token, key) for this thread's tokens in order; every lane of a warp takes part in each turn
+    // f(key) for the keys of this warp's tokens, in no order
     auto each = [&](auto f) {
-#pragma unroll 4
-        for (int i = 0; i < turns; ++i) {
-            const int t = base + 32 * i;
-            uint32_t k = 0u;
-            if (need > 0) {
-                if constexpr (HELD) k = own[32 * i];
-                else k = t < n ? score_key(__ldg(p.scores + row + t)) : 0u;
+        if constexpr (HELD) {
+            const uint4* k4 = reinterpret_cast<const uint4*>(own);
+#pragma unroll 2
+            for (int i = lane; i < 8 * turns; i += 32) {
+                const uint4 k = k4[i];
+                f(k.x);
+                f(k.y);
+                f(k.z);
+                f(k.w);
             }
-            f(t, k);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < turns; ++i) {
+                const int t = base + 32 * i;
+                f(key_of(t, t < n ? __ldg(p.scores + row + t) : 0.f));
+            }
         }
     };
 
-    uint32_t T = 0xffffffffu, left = 0;              // keep keys above T, and `left` of key T
+    uint32_t T = kFixed - 1u, left = 0;              // keep keys above T, and `left` of key T
     if (need > 0) {
         T = 0;
         left = need;
@@ -196,11 +215,19 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             const int width = step == 2 ? 10 : 11;
             const uint32_t mask = (1u << width) - 1u;
             uint32_t* bins = hist[step];
-            each([&](int t, uint32_t k) {
-                const bool mine = step == 0 || ((k ^ T) >> (shift + width)) == 0;
-                if (t >= lo && t < hi && mine) atomicAdd(&bins[(k >> shift) & mask], 1u);
-            });
+            if (step == 0) {
+                each([&](uint32_t k) { atomicAdd(&bins[k >> 21], 1u); });
+            } else {
+                const uint32_t prefix = T >> (shift + width);
+                each([&](uint32_t k) {
+                    if (k >> (shift + width) == prefix) atomicAdd(&bins[(k >> shift) & mask], 1u);
+                });
+            }
             __syncthreads();
+            if (step == 0) {                             // the fixed tokens do not compete
+                if (tid == 0) bins[kBins - 1] = 0;
+                __syncthreads();
+            }
             // sums of 32 bins: eight threads of four bins each
             const uint4 v = reinterpret_cast<const uint4*>(bins)[tid];
             uint32_t sum = v.x + v.y + v.z + v.w;
@@ -239,14 +266,18 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             left = pick[1];
         }
     }
-    // what a token is to the sequence: kept for certain, a candidate of key T, or dropped
-    auto kept = [&](int t, uint32_t k) { return t < n && (all || t < lo || t >= hi || (need > 0 && k > T)); };
-    auto tied = [&](int t, uint32_t k) { return need > 0 && t >= lo && t < hi && k == T; };
-    uint32_t a = 0, b = 0;                           // of this warp
-    each([&](int t, uint32_t k) {
-        a += __popc(__ballot_sync(0xffffffffu, kept(t, k)));
-        b += __popc(__ballot_sync(0xffffffffu, tied(t, k)));
-    });
+    uint32_t a = 0, b = 0;                           // this warp's tokens kept for certain, and of key T
+    if (need > 0) {
+        each([&](uint32_t k) {
+            a += k > T;
+            b += k == T;
+        });
+    } else {
+        for (int i = 0; i < turns; ++i) a += key_of(base + 32 * i, 0.f) == kFixed;
+    }
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    const uint32_t ties = b;
     __syncthreads();
     if (lane == 0) {
         warp_a[warp] = a;
@@ -292,9 +323,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         for (int j = 0; j < kBatch; ++j) {
             if (i0 + j >= turns) break;
             const int t = base + 32 * (i0 + j);
-            const uint32_t k = score_key(sc[j]);
-            const bool in = kept(t, k), tie = tied(t, k);
-            const uint32_t ba = __ballot_sync(0xffffffffu, in), bb = __ballot_sync(0xffffffffu, tie);
+            uint32_t k;
+            if (HELD && need > 0) k = own[32 * (i0 + j) + lane];
+            else k = key_of(t, sc[j]);
+            const bool in = k > T, tie = k == T;
+            const uint32_t ba = __ballot_sync(0xffffffffu, in);
+            const uint32_t bb = ties ? __ballot_sync(0xffffffffu, tie) : 0u;
             const uint32_t eq = b + __popc(bb & below);  // of key T before this token
             const uint32_t place = a + __popc(ba & below) + min(eq, left);
             if (in || (tie && eq < left)) {
@@ -311,10 +345,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
 }
 
 // CTAs per sequence: a cluster of up to 16, doubled while a share is above
-// 1,024 tokens and the grid still fits the GPU's two CTAs per SM.
+// 2,048 tokens and the grid still fits the GPU's two CTAs per SM.  Shares of
+// 1,024 / 2,048 / 4,096: one sequence of 16,384 tokens 10.5 / 9.0 / 11.6 us,
+// of 4,096 9.7 / 8.4 / 7.7, eight of 8,192 8.7 / 10.1 / 10.1.
 int evict_cluster(int S, int MT) {
     int c = 1;
-    while (c < kMaxRanks && (MT + c - 1) / c > 1024 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
+    while (c < kMaxRanks && (MT + c - 1) / c > 2048 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
     return c;
 }
 

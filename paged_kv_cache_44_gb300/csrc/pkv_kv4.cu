@@ -15,8 +15,11 @@
 // each), of V a pair of tokens' word of every group (four values each), so
 // its codes leave in one 16-byte store and a warp's in 512 consecutive
 // bytes.  Two tokens of V that are not neighbours in a block (a decoding
-// step's) take 2-byte stores instead.  The bound is the bytes (read and
-// written once) and, as close, about 16 instructions per value.
+// step's) take 2-byte stores instead.  The smallest and largest values of
+// the groups a warp's lanes share are reduced together, each lane ending with
+// one group (14 shuffles for 16 reductions over 8 lanes), whose scale and
+// zero it alone computes and hands out.  The bound is the bytes, read and
+// written once, and, as close, the instructions per value.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
@@ -34,40 +37,96 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     return r;
 }
 
-// A group's scale and zero from its smallest and largest value (NaN if the group holds one).
-__device__ __forceinline__ void kv4_params(float mn, float mx, __half& hs, __half& hz) {
+// A group's scale and zero, and what its codes are computed with: a value x
+// has the quotient q = (x / by - zero) / scale = 15 (x A + B) up to rounding.
+struct GroupScale {
+    __half hs, hz;
+    float A, B, slack;
+};
+
+// mn, mx: the smallest and largest x of the group (NaN if it holds one);
+// rby = 1 / by.  x / by is monotonic in x, so the two divisions give the
+// smallest and largest y.  In fp32 A is off by three roundings (2^-24
+// relative each), B by two, their sum by one; y, y - zero and its division
+// in the definition by one each: together at most 2^-24 (6 max|y| / scale +
+// 45) of q, which `slack` bounds.
+__device__ __forceinline__ GroupScale group_scale(float mn, float mx, float by, float rby) {
+    GroupScale s;
+    s.A = s.B = 0.f;
+    s.slack = 0.f;
     if (mn != mn) {
-        hz = __ushort_as_half(0x7e00);
-        hs = __ushort_as_half(0);
-        return;
+        s.hz = __ushort_as_half(0x7e00);
+        s.hs = __ushort_as_half(0);
+        return s;
     }
-    hz = __float2half_rn(fminf(fmaxf(mn, -kKv4Max), kKv4Max));
-    const float top = fminf(fmaxf(mx, -kKv4Max), kKv4Max);
-    hs = __float2half_rn(__fdiv_rn(fmaxf(__fsub_rn(top, __half2float(hz)), 0.f), 15.f));
+    if (by != 1.f) {
+        mn = __fdiv_rn(mn, by);
+        mx = __fdiv_rn(mx, by);
+    }
+    mn = fminf(fmaxf(mn, -kKv4Max), kKv4Max);
+    mx = fminf(fmaxf(mx, -kKv4Max), kKv4Max);
+    s.hz = __float2half_rn(mn);
+    const float z = __half2float(s.hz);
+    s.hs = __float2half_rn(__fdiv_rn(fmaxf(__fsub_rn(mx, z), 0.f), 15.f));
+    const float sc = __half2float(s.hs);
+    if (sc > 0.f) {
+        const float inv = __fdiv_rn(1.f, 15.f * sc);
+        s.A = __fmul_rn(inv, rby);
+        s.B = -__fmul_rn(z, inv);
+        s.slack = 4.76837158203125e-7f * (fmaxf(fabsf(mn), fabsf(mx)) * inv * 15.f + 6.f);   // 2^-21
+        if (!(s.A > 1e-30f && s.A < 1e30f)) s.slack = 1.f;                                    // extreme tensor scales
+    }
+    return s;
 }
 
-// N codes of one group, code k in bits 4 k.  The quotient is taken as a
-// product with the scale's reciprocal, which is within 2^-18 of the IEEE
-// quotient where that is between 0 and 15 (two roundings of 2^-24 relative,
-// against one), so both round to the same whole number unless the product
-// is that near a half; there the division is done.  Values clamped to fp16's
-// range need no clamp here: they end at code 0 or 15 either way.
-template <int N>
-__device__ __forceinline__ uint32_t kv4_codes(const float (&y)[N], float sc, float z) {
+// Four codes of one group by the definition, code k in bits 4 k; par: the group's scale and zero.
+__device__ __noinline__ uint32_t kv4_codes_exact(float x0, float x1, float x2, float x3, float by, uint32_t par) {
+    const float sc = __half2float(__ushort_as_half((unsigned short)par));
+    const float z = __half2float(__ushort_as_half((unsigned short)(par >> 16)));
     if (!(sc > 0.f)) return 0u;
-    const float inv = __fdiv_rn(1.f, sc);
+    const float x[4] = {x0, x1, x2, x3};
     uint32_t w = 0;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float d = __fsub_rn(y[k], z);
-        float q = fminf(fmaxf(__fmul_rn(d, inv), 0.f), 15.f);
-        const float near = __fadd_rn(q, 12582912.f);            // 1.5 * 2^23: the nearest whole number in the low bits
-        uint32_t code = __float_as_uint(near) & 15u;
-        if (fabsf(__fsub_rn(q, __fsub_rn(near, 12582912.f))) > 0.5f - 3.814697265625e-6f)
-            code = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(d, sc)), 0.f), 15.f);
-        w |= code << (4 * k);
+    for (int k = 0; k < 4; ++k) {
+        const float y = fminf(fmaxf(__fdiv_rn(x[k], by), -kKv4Max), kKv4Max);
+        w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(y, z), sc)), 0.f), 15.f) << (4 * k);
     }
     return w;
+}
+
+// The same: q saturated to 0 .. 15 and rounded by one fused multiply-add
+// (1.5 * 2^23 + 15 q / 15); values past fp16's range end at code 0 or 15
+// without a clamp.  Where a quotient is within the slack of a half, so that it
+// may round either way, this lane takes the definition's: of bf16 values about
+// one in 2,500 is an exact half.
+__device__ __forceinline__ uint32_t kv4_codes(const float* x, float A, float B, float thr, float by, uint32_t par) {
+    constexpr float kWhole = 12582912.f;
+    float packed = 0.f;                                   // below 2^16: exact
+    bool close = false;
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+        const float q = __saturatef(__fmaf_rn(x[k], A, B));
+        const float f = __fsub_rn(__fmaf_rn(q, 15.f, kWhole), kWhole);
+        close = close || !(fabsf(__fmaf_rn(q, 15.f, -f)) <= thr);
+        packed = __fmaf_rn(packed, 16.f, f);
+    }
+    if (close) return kv4_codes_exact(x[0], x[1], x[2], x[3], by, par);
+    return __float2uint_rn(packed);
+}
+
+// One step of a reduction that halves what a lane holds: of v[0 .. 2 N) it keeps the upper
+// half (in v[0 .. N)) where `upper`, its partner in the lane distance `mask` the lower one.
+template <int N, bool MIN>
+__device__ __forceinline__ void halve(float* v, int mask, bool upper) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float send = upper ? v[i] : v[i + N], keep = upper ? v[i + N] : v[i];
+        const float got = __shfl_xor_sync(0xffffffffu, send, mask);
+        v[i] = MIN ? min_nan(keep, got) : fmaxf(keep, got);
+    }
+}
+__device__ __forceinline__ float warp_max(float v) {      // v >= 0
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
 // What a warp works on: head h of K (v false) or V, tokens i0 .. i0 + 7, whose
@@ -149,105 +208,122 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Params p) {
     if (!octet_of(p, o)) return;
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, sh = p.bs == 16 ? 4 : 5;
     const int head_bytes = kv4_head_bytes(p.bs, D), zeros = p.bs * G;
-    const float by = o.v ? p.v_scale : p.k_scale;
-    const bool scaled = by != 1.f;
+    const float by = o.v ? p.v_scale : p.k_scale, rby = __fdiv_rn(1.f, by);
     if (!o.v) {
         const long long s = __shfl_sync(0xffffffffu, o.slot, r);
         const size_t src = ((size_t)(o.i0 + r) * p.Hkv + o.h) * D + 8 * c;
-        float y[G][8], mn[G], mx[G];
+        float x[G][8], mn[G], mx[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             if (s >= 0) {
-                load8<In>(p.key, src + 32 * g, y[g]);
+                load8<In>(p.key, src + 32 * g, x[g]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[g][k] = 0.f;
+                for (int k = 0; k < 8; ++k) x[g][k] = 0.f;
             }
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (scaled)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[g][k] = __fdiv_rn(y[g][k], by);
-            mn[g] = mx[g] = y[g][0];
+            mn[g] = mx[g] = x[g][0];
 #pragma unroll
             for (int k = 1; k < 8; ++k) {
-                mn[g] = min_nan(mn[g], y[g][k]);
-                mx[g] = fmaxf(mx[g], y[g][k]);
+                mn[g] = min_nan(mn[g], x[g][k]);
+                mx[g] = fmaxf(mx[g], x[g][k]);
             }
+        }
+        // over the token's four lanes: lane c ends with group c (d 64: lanes 2 g, 2 g + 1 with group g)
+        halve<G / 2, true>(mn, 2, c & 2);
+        halve<G / 2, false>(mx, 2, c & 2);
+        if constexpr (G == 4) {
+            halve<1, true>(mn, 1, c & 1);
+            halve<1, false>(mx, 1, c & 1);
+        } else {
+            mn[0] = min_nan(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], 1));
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 1));
+        }
+        const GroupScale gs = group_scale(mn[0], mx[0], by, rby);
+        const float thr = 0.5f - warp_max(gs.slack);
+        auto holder = [&](int g) { return (lane & ~3) | (g * (4 / G)); };
+        const uint32_t mine = pair_bits(gs.hs, gs.hz);
+        uint32_t w[G];
 #pragma unroll
-            for (int q = 1; q < 4; q <<= 1) {
-                mn[g] = min_nan(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], q));
-                mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], q));
-            }
+        for (int g = 0; g < G; ++g) {
+            const float A = __shfl_sync(0xffffffffu, gs.A, holder(g)), B = __shfl_sync(0xffffffffu, gs.B, holder(g));
+            const uint32_t par = __shfl_sync(0xffffffffu, mine, holder(g));
+            w[g] = kv4_codes(x[g], A, B, thr, by, par);
+            w[g] |= kv4_codes(x[g] + 4, A, B, thr, by, par) << 16;
         }
         if (s < 0) return;
         const int t = (int)s & (p.bs - 1);
         unsigned char* blk = static_cast<unsigned char*>(p.key_cache) + ((size_t)(s >> sh) * p.Hkv + o.h) * head_bytes;
-        __half hs[G], hz[G];
-        uint32_t w[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            kv4_params(mn[g], mx[g], hs[g], hz[g]);
-            w[g] = kv4_codes(y[g], __half2float(hs[g]), __half2float(hz[g]));
-        }
         store_words<G>(blk + 4 * F::k_word(t, 8 * c), w);
-        if (c < 2) {                              // lane 0 of a token's four: the scales, lane 1: the zeros
-            __half* par = reinterpret_cast<__half*>(blk + F::codes(p.bs)) + (c ? zeros : 0) + F::k_par(t, 0);
-#pragma unroll
-            for (int g = 0; g < G; g += 2)
-                reinterpret_cast<uint32_t*>(par)[g / 2] = c ? pair_bits(hz[g], hz[g + 1]) : pair_bits(hs[g], hs[g + 1]);
+        if (c % (4 / G) == 0) {
+            __half* par = reinterpret_cast<__half*>(blk + F::codes(p.bs)) + F::k_par(t, c / (4 / G));
+            par[0] = gs.hs;
+            par[zeros] = gs.hz;
         }
         return;
     }
-    // V: tokens 2c and 2c + 1, values 32 g + 4 r .. + 3
+    // V: tokens 2c and 2c + 1, values 32 g + 4 r .. + 3; (token, group) number G j + g
+    constexpr int Q = 2 * G;
     long long s[2];
-    uint32_t half[2][G];                          // 16 bits: four codes
-    __half hs[2][G], hz[2][G];
+    float x[Q][4], mn[Q], mx[Q];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         s[j] = __shfl_sync(0xffffffffu, o.slot, 2 * c + j);
         const size_t src = ((size_t)(o.i0 + 2 * c + j) * p.Hkv + o.h) * D + 4 * r;
-        float y[G][4];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (s[j] >= 0) {
-                load4<In>(p.value, src + 32 * g, y[g]);
-            } else {
-                y[g][0] = y[g][1] = y[g][2] = y[g][3] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (scaled)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[g][k] = __fdiv_rn(y[g][k], by);
-            float mn = min_nan(min_nan(y[g][0], y[g][1]), min_nan(y[g][2], y[g][3]));
-            float mx = fmaxf(fmaxf(y[g][0], y[g][1]), fmaxf(y[g][2], y[g][3]));
-#pragma unroll
-            for (int q = 4; q < 32; q <<= 1) {
-                mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, q));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
-            }
-            kv4_params(mn, mx, hs[j][g], hz[j][g]);
-            half[j][g] = kv4_codes(y[g], __half2float(hs[j][g]), __half2float(hz[j][g]));
+            float (&y)[4] = x[G * j + g];
+            if (s[j] >= 0) load4<In>(p.value, src + 32 * g, y);
+            else y[0] = y[1] = y[2] = y[3] = 0.f;
         }
     }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        mn[q] = min_nan(min_nan(x[q][0], x[q][1]), min_nan(x[q][2], x[q][3]));
+        mx[q] = fmaxf(fmaxf(x[q][0], x[q][1]), fmaxf(x[q][2], x[q][3]));
+    }
+    // over the pair's eight lanes: lane r ends with number r (d 64: r / 2)
+    halve<Q / 2, true>(mn, 16, r & 4);
+    halve<Q / 2, false>(mx, 16, r & 4);
+    halve<Q / 4, true>(mn, 8, r & 2);
+    halve<Q / 4, false>(mx, 8, r & 2);
+    if constexpr (G == 4) {
+        halve<1, true>(mn, 4, r & 1);
+        halve<1, false>(mx, 4, r & 1);
+    } else {
+        mn[0] = min_nan(mn[0], __shfl_xor_sync(0xffffffffu, mn[0], 4));
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], 4));
+    }
+    const GroupScale gs = group_scale(mn[0], mx[0], by, rby);
+    const float thr = 0.5f - warp_max(gs.slack);
+    auto holder = [&](int q) { return 4 * (q * (8 / Q)) + c; };
+    const uint32_t mine = pair_bits(gs.hs, gs.hz);
+    uint32_t code[Q];                             // 16 bits
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const float A = __shfl_sync(0xffffffffu, gs.A, holder(q)), B = __shfl_sync(0xffffffffu, gs.B, holder(q));
+        code[q] = kv4_codes(x[q], A, B, thr, by, __shfl_sync(0xffffffffu, mine, holder(q)));
+    }
+    // the same group's scale and zero of the pair's other token
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 16);
     auto block = [&](long long slot) {
         return static_cast<unsigned char*>(p.value_cache) + ((size_t)(slot >> sh) * p.Hkv + o.h) * head_bytes;
     };
+    const int own = r / (8 / Q), oj = own / G, og = own % G;   // this lane's (token, group)
+    const bool holds = r % (8 / Q) == 0;
     if (s[0] >= 0 && (s[0] & 1) == 0 && s[1] == s[0] + 1) {
         const int t = (int)s[0] & (p.bs - 1);
         unsigned char* blk = block(s[0]);
         uint32_t w[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) w[g] = half[0][g] | (half[1][g] << 16);
+        for (int g = 0; g < G; ++g) w[g] = code[g] | (code[G + g] << 16);
         store_words<G>(blk + 4 * F::v_word(t, 4 * r), w);
-        if (r < 2) {
-            uint32_t q[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) q[g] = r ? pair_bits(hz[0][g], hz[1][g]) : pair_bits(hs[0][g], hs[1][g]);
-            store_words<G>(reinterpret_cast<__half*>(blk + F::codes(p.bs)) + (r ? zeros : 0) + F::v_par(t, 0), q);
+        if (holds) {                              // the first token's lanes store scales, the second's zeros
+            uint32_t* par = reinterpret_cast<uint32_t*>(reinterpret_cast<__half*>(blk + F::codes(p.bs)) + F::v_par(t, og));
+            if (oj == 0) par[0] = __byte_perm(mine, other, 0x5410u);
+            else par[zeros / 2] = __byte_perm(other, mine, 0x7632u);
         }
         return;
     }
@@ -256,11 +332,13 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(Kv4Params p) {
         if (s[j] < 0) continue;
         const int t = (int)s[j] & (p.bs - 1);
         unsigned char* blk = block(s[j]);
-        __half* par = reinterpret_cast<__half*>(blk + F::codes(p.bs)) + (r ? zeros : 0);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            reinterpret_cast<uint16_t*>(blk)[2 * F::v_word(t, 32 * g + 4 * r) + t % 2] = (uint16_t)half[j][g];
-            if (r < 2) par[F::v_par(t, g)] = r ? hz[j][g] : hs[j][g];
+        for (int g = 0; g < G; ++g)
+            reinterpret_cast<uint16_t*>(blk)[2 * F::v_word(t, 32 * g + 4 * r) + t % 2] = (uint16_t)code[G * j + g];
+        if (holds && oj == j) {
+            __half* par = reinterpret_cast<__half*>(blk + F::codes(p.bs)) + F::v_par(t, og);
+            par[0] = gs.hs;
+            par[zeros] = gs.hz;
         }
     }
 }
