@@ -383,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile t's buffer is refilled once the unit that used it has issued its last S_t
         uint32_t un = 0, qu[2] = {0u, 0u};
         bool ok = true, bad = false;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
         for (;;) {
             const int slot = un & 1;
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
@@ -401,32 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bad = true;
                     break;
                 }
-                constexpr int CH = 2 * D / 16;           // 16-byte chunks per row
-                constexpr int kBatch = 16;               // loads in flight per lane
-                static_assert((kTileRows * CH / 32) % kBatch == 0, "Q load batches");
-                const int rows_here = min(kTileRows, rows - r0);
-                const uint32_t qdst = qbuf(t);
-                for (int it0 = 0; it0 < kTileRows * CH / 32; it0 += kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int idx = (it0 + k) * 32 + lane;
-                        const int r = idx / CH, c = idx % CH;
-                        v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < rows_here) {
-                            const int row = r0 + r;
-                            const int qi = row / p.g, hh = row - qi * p.g;
-                            const size_t off = ((size_t)(q0 + qi) * p.Hq + kvh * p.g + hh) * D + c * 8;
-                            v[k] = __ldg(reinterpret_cast<const uint4*>(q + off));
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int idx = (it0 + k) * 32 + lane;
-                        const int r = idx / CH, c = idx % CH;
-                        st_shared_v4(qdst + (c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[k]);
-                    }
-                }
+                load_q_rows<D, kTileRows>(p, q0, kvh, r0, rows - r0, qbuf(t));
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(bar(kBarQFull, t));
