@@ -217,4 +217,8 @@ cudaError_t launch_prefill_merge(const DecodeParams& p, const int32_t* query_sta
 // 64 values by min(bs, 32) tokens, 128-byte swizzle
 bool prefill_encode_kv_map(CUtensorMap* map, const void* base, const DecodeParams& p);
 
+// 3-D tensor map over the query [T, Hq, d]: boxes of 64 values by the g heads
+// of one K/V head by tile_queries queries, 128-byte swizzle
+bool prefill_encode_q_map(CUtensorMap* map, const DecodeParams& p, int T, int tile_queries);
+
 }  // namespace pkv

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPWarps * 32, 1)
             static_next += total_warps;
             if (v >= total_units) return false;
             QTile x;
-            if (!qtile_of<kRows>(p, query_start, T, max_q, v, rt_max, x)) continue;
+            if (!qtile_of<false>(p, query_start, T, max_q, v, rt_max, kRows, x)) continue;
             u = v;
             return true;
         }
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kPWarps * 32, 1)
                 claiming = false;
                 return false;
             }
-            qtile_of<kRows>(p, query_start, T, max_q, u, rt_max, iu);
+            qtile_of<false>(p, query_start, T, max_q, u, rt_max, kRows, iu);
             if (lane == 0) {
                 int4* e = queue + 3 * (q_tail % C::kQueue);
                 e[0] = make_int4(iu.s, iu.kvh, iu.rt, iu.part);
@@ -471,7 +471,9 @@ cudaError_t launch_prefill_d(const DecodeParams& p, const int32_t* query_start, 
 
 }  // namespace
 
-bool prefill_encode_kv_map(CUtensorMap* map, const void* base, const DecodeParams& p) {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
@@ -482,6 +484,26 @@ bool prefill_encode_kv_map(CUtensorMap* map, const void* base, const DecodeParam
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     });
+    return fn;
+}
+
+}  // namespace
+
+bool prefill_encode_q_map(CUtensorMap* map, const DecodeParams& p, int T, int tile_queries) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    // [T queries][Hq][d]: boxes of 64 values x one K/V head's query heads x the tile's queries
+    const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.Hq * p.d * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)p.g, (cuuint32_t)tile_queries};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool prefill_encode_kv_map(CUtensorMap* map, const void* base, const DecodeParams& p) {
+    auto fn = encode_fn();
     if (fn == nullptr) return false;
     // rows of one K/V head (d bf16 values), boxes of 64 values x one block
     // of at most 32 tokens, 128-byte swizzle

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v = __shfl_sync(0xffffffffu, v, 0);
                 static_next += gridDim.x;
                 if (v >= total_units) break;
-                if (qtile_of<kURows, WIN>(p, query_start, T, max_q, v, rt_max, x)) {
+                if (qtile_of<WIN>(p, query_start, T, max_q, v, rt_max, kURows, x)) {
                     have = true;
                     break;
                 }
@@ -383,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (un >= 2) ok = wait(bar(kBarQEmpty, qb), ((un >> 1) - 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int kvh = e0.y, rt = e0.z, q0 = e2.x, rows = e2.z;
-            load_q_rows<D, kURows>(p, q0, kvh, rt * kURows, rows - rt * kURows, qbuf(qb));
+            load_q_rows<D, kURows>(p, q0, kvh, rt * kURows, 0, kURows, rows - rt * kURows, qbuf(qb));
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kBarQFull, qb));

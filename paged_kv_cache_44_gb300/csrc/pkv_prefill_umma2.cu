@@ -119,11 +119,22 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
+// Q of a tile.  The g heads of a query are consecutive rows in memory, and a
+// tile may begin and end inside a query: of its 128 rows, as many whole
+// queries as any tile holds are one tensor copy per 64 values (its first row
+// is wherever the first whole query begins: the swizzle goes by the shared
+// address, which every row has 128 bytes of), and a warp copies the rows
+// before and after.  A window of 1,024 leaves nine stages per unit, so a
+// unit's start counts: 16 x 504-query chunks 140 us, and 162 when a warp
+// copies every row.
+__host__ __device__ __forceinline__ int box_queries(int g) { return (kTileRows - (kTileRows % g ? g - 1 : 0)) / g; }
+
 template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_umma2_kernel(const __grid_constant__ DecodeParams p, const int32_t* __restrict__ query_start, int T,
                          int max_q, const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, unsigned long long total_units, int rt_max) {
+                         const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap,
+                         unsigned long long total_units, int rt_max) {
     using C = UCfg<D>;
     constexpr int NK = C::kKItems, NV = C::kVItems;
     static_assert(NK <= 4 && NV <= 4, "barrier slots");
@@ -214,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v = __shfl_sync(0xffffffffu, v, 0);
                 static_next += gridDim.x;
                 if (v >= total_units) break;
-                if (qtile_of<kURows, WIN>(p, query_start, T, max_q, v, rt_max, x)) {
+                if (qtile_of<WIN>(p, query_start, T, max_q, v, rt_max, kURows, x)) {
                     have = true;
                     break;
                 }
@@ -383,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // tile t's buffer is refilled once the unit that used it has issued its last S_t
         uint32_t un = 0, qu[2] = {0u, 0u};
         bool ok = true, bad = false;
+        const int boxq = WIN ? box_queries(p.g) : 0;
         for (;;) {
             const int slot = un & 1;
             ok = wait(bar(kBarUFull, slot), (un >> 1) & 1, true);
@@ -400,7 +412,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bad = true;
                     break;
                 }
-                load_q_rows<D, kTileRows>(p, q0, kvh, r0, rows - r0, qbuf(t));
+                const int in_box = boxq * p.g, before = in_box > 0 ? (p.g - r0 % p.g) % p.g : 0;
+                if (in_box > 0 && lane == 0) {
+                    // queries past the sequence's last are other sequences' or zeros: their results are not stored
+                    mbar_expect_tx(bar(kBarQFull, t), (uint32_t)in_box * 2 * D);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tensor_load_3d(qbuf(t) + h * (kTileRows * 128) + before * 128, &qmap, 64 * h, kvh * p.g,
+                                       q0 + (r0 + before) / p.g, bar(kBarQFull, t));
+                }
+                load_q_rows<D, kTileRows>(p, q0, kvh, r0, 0, before, rows - r0, qbuf(t));
+                load_q_rows<D, kTileRows>(p, q0, kvh, r0, before + in_box, kTileRows, rows - r0, qbuf(t));
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(bar(kBarQFull, t));
@@ -409,6 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (bad) break;
             ++un;
         }
+        // copies still in flight land before the CTA leaves
+        for (int t = 0; t < 2; ++t)
+            if (qu[t] > 0) wait(bar(kBarQFull, t), (qu[t] - 1) & 1, false);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issue
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -446,11 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (e2.w == 0) break;
                 const int nst = (e1.y - e1.x + kTok - 1) / kTok;
                 const int nt = e0.z * kURows + kTileRows < e2.z ? 2 : 1;      // tiles with rows
-                for (int t = 0; t < nt && ok; ++t) ok = wait(bar(kBarQFull, t), qu[t] & 1, true);
-                // stage 0: each tile's S, once the tile's previous P . V has read its buffer
+                // stage 0: each tile's S, once its Q is there and its previous P . V has read the buffer
                 ok = ok && wait(bar(kBarKFull, g % NK), (g / NK) & 1, true);
                 for (int t = 0; t < nt && ok; ++t) {
-                    if (gt[t] > 0) ok = wait(bar(kBarPVDone, t), (gt[t] - 1) & 1, true);
+                    ok = wait(bar(kBarQFull, t), qu[t] & 1, true);
+                    if (ok && gt[t] > 0) ok = wait(bar(kBarPVDone, t), (gt[t] - 1) & 1, true);
                     if (!ok) break;
                     umma::fence_after_sync();
                     issue_s(t, g);
@@ -615,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                st_shared_v4(vb + h * (kTok * 128) + i * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+                                st_shared_v4(vb + h * (kTok * 128) + i * 128 + ((c ^ (i & 7)) << 4), make_uint4(0u, 0u, 0u, 0u));
                     }
                     fence_proxy_async();
                 }
@@ -673,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::fence_after_sync();
             const size_t hrow = (size_t)(q0 + qi) * p.Hq + kvh * p.g + hh;
             const float f = l > 0.f ? 1.f / l : 0.f;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
 #pragma unroll
             for (int c0 = 0; c0 < D / 32; ++c0) {
                 uint32_t ov[32];
@@ -680,13 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::tmem_wait_ld();
                 if (!rv) continue;
                 if (np == 1) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + hrow * D + 32 * c0);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(pack2<false>(__uint_as_float(ov[8 * k]) * f, __uint_as_float(ov[8 * k + 1]) * f),
-                                            pack2<false>(__uint_as_float(ov[8 * k + 2]) * f, __uint_as_float(ov[8 * k + 3]) * f),
-                                            pack2<false>(__uint_as_float(ov[8 * k + 4]) * f, __uint_as_float(ov[8 * k + 5]) * f),
-                                            pack2<false>(__uint_as_float(ov[8 * k + 6]) * f, __uint_as_float(ov[8 * k + 7]) * f));
+                    store_row32(static_cast<__nv_bfloat16*>(p.out) + hrow * D + 32 * c0, ov, f, wide);
                 } else {
                     uint4* dst = reinterpret_cast<uint4*>(p.part_acc + (hrow * p.Pmax + part) * D + 32 * c0);
 #pragma unroll
@@ -733,12 +754,14 @@ cudaError_t launch_umma2_d(const DecodeParams& p, const int32_t* query_start, in
     if (e != cudaSuccess) return e;
     CUtensorMap kmap, vmap;
     if (!prefill_encode_kv_map(&kmap, p.kc, p) || !prefill_encode_kv_map(&vmap, p.vc, p)) return cudaErrorInvalidValue;
+    CUtensorMap qmap = kmap;                 // unused without whole queries
+    if (WIN && box_queries(p.g) > 0 && !prefill_encode_q_map(&qmap, p, T, box_queries(p.g))) return cudaErrorInvalidValue;
     int rt_max = (max_q_len * p.g + kURows - 1) / kURows;
     if (rt_max < 1) rt_max = 1;
     const unsigned long long units = (unsigned long long)p.Pmax * p.S * p.Hkv * rt_max;
     int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;
-    kern<<<grid, kThreads, C::kSmemBytes, st>>>(p, query_start, T, max_q_len, kmap, vmap, units, rt_max);
+    kern<<<grid, kThreads, C::kSmemBytes, st>>>(p, query_start, T, max_q_len, kmap, vmap, qmap, units, rt_max);
     e = cudaGetLastError();
     if (e != cudaSuccess || !merge) return e;
     return launch_prefill_merge(p, query_start, T, kURows, max_q_len, st);

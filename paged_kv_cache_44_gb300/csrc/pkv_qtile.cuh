@@ -4,7 +4,7 @@
 // A sequence s with n tokens computes its last q_len tokens as queries
 // (a chunk of prefill, or the tokens a speculative decoder proposes).  For
 // K/V head kvh its rows are the pairs (query i, head kvh * g + j), row
-// r = i * g + j, cut into tiles of ROWS rows; a tile needs the keys up to
+// r = i * g + j, cut into tiles of tile_rows rows; a tile needs the keys up to
 // its last query's position n - q_len + i_last, cut into partitions of P
 // tokens.  Unit ids run partition-major, then sequence, K/V head, row tile,
 // so the tiles of one key range are claimed together and share the K/V
@@ -43,11 +43,12 @@ __device__ __forceinline__ int qtile_keys(const DecodeParams& p, int n, int ql, 
 // Unit id -> coordinates; false for ids that name no work.  A sequence whose
 // length exceeds the host bound, whose query count is outside [0, n] or
 // above the host's max_q, or whose queries leave [0, T) is skipped and
-// reported once.  rt_max = ceil(max_q * g / ROWS) tiles per (sequence, K/V
+// reported once.  rt_max = ceil(max_q * g / tile_rows) tiles per (sequence, K/V
 // head).
-template <int ROWS, bool WIN = false>
+template <bool WIN>
 __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* query_start, int T, int max_q,
-                                         unsigned long long u, int rt_max, QTile& x) {
+                                         unsigned long long u, int rt_max, int tile_rows,
+                                         QTile& x) {
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * rt_max;
     x.part = (int)(u / per_part);
     const unsigned long long rem = u - (unsigned long long)x.part * per_part;
@@ -64,10 +65,10 @@ __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* q
     }
     x.n = n;
     x.rows = x.ql * p.g;
-    if (x.rt * ROWS >= x.rows) return false;
-    const int last_row = min(x.rt * ROWS + ROWS - 1, x.rows - 1);
+    if (x.rt * tile_rows >= x.rows) return false;
+    const int last_row = min(x.rt * tile_rows + tile_rows - 1, x.rows - 1);
     int key_end;
-    if constexpr (WIN) key_end = qtile_keys(p, n, x.ql, x.rt * ROWS, last_row, x.first, x.span);
+    if constexpr (WIN) key_end = qtile_keys(p, n, x.ql, x.rt * tile_rows, last_row, x.first, x.span);
     else key_end = n - x.ql + last_row / p.g + 1;
     x.np = (key_end + p.P - 1) / p.P;
     if (x.part >= x.np) return false;
@@ -76,18 +77,20 @@ __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* q
     return true;
 }
 
-// One warp copies ROWS (query, head) rows of Q, from `row` of the chunk that
-// starts at query token q0, into a 128-byte-swizzled shared-memory tile (a
-// region of ROWS rows per 64 values); rows past `here` become zeros.  Every
-// copy is issued before the first is waited for, and a lane steps from row to
-// row (RPI rows on) without dividing: of the 16 x 512-query chunks under a
-// window of 1,024 the loader's divisions and its four round trips per tile
-// were a fifth of the time.  The caller fences and signals.
+// One warp copies (query, head) rows of Q into a 128-byte-swizzled
+// shared-memory tile (a region of ROWS rows per 64 values): rows [r0, r1) of
+// the tile whose first row is `row` of the chunk that starts at query token
+// q0; rows past `here` become zeros.  Every copy is issued before the first is
+// waited for, and a lane steps from row to row (RPI rows on) without dividing:
+// of the 16 x 512-query chunks under a window of 1,024 the divisions and four
+// round trips per tile were 30% of the time (256.8 -> 180.3 us).  The caller
+// waits (cp.async.wait_all), fences and signals.
 template <int D, int ROWS>
-__device__ __forceinline__ void load_q_rows(const DecodeParams& p, int q0, int kvh, int row, int here, uint32_t dst) {
+__device__ __forceinline__ void load_q_rows(const DecodeParams& p, int q0, int kvh, int row, int r0, int r1, int here,
+                                            uint32_t dst) {
     constexpr int CH = 2 * D / 16, RPI = 32 / CH;        // 16-byte chunks per row, rows per request
     const int lane = threadIdx.x & 31, c = lane % CH;
-    int r = lane / CH;
+    int r = r0 + lane / CH;
     const int qi = (row + r) / p.g;
     int hh = row + r - qi * p.g;
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
@@ -95,14 +98,13 @@ __device__ __forceinline__ void load_q_rows(const DecodeParams& p, int q0, int k
     const size_t next_query = (size_t)(p.Hq - p.g) * D;
     dst += (c >> 3) * (ROWS * 128);
 #pragma unroll 4
-    for (int it = 0; it < ROWS / RPI; ++it) {
+    for (; r < r1; r += RPI) {
         const uint32_t to = dst + r * 128 + (((c & 7) ^ (r & 7)) << 4);
         if (r < here) {
             tc::cp_async16(to, src);
         } else {
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0u) : "memory");
         }
-        r += RPI;
         hh += RPI;
         src += RPI * D;
         while (hh >= p.g) {
@@ -110,7 +112,27 @@ __device__ __forceinline__ void load_q_rows(const DecodeParams& p, int q0, int k
             src += next_query;
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// 32 values of one output row, times f, as bf16 at `dst`.  Every lane of a warp
+// stores to a row of its own, so a store's cost is its sectors: 32-byte stores
+// (wide: dst is 32-byte aligned) write whole ones, 16-byte ones halves.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&o)[32], float f, bool wide) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = tc::pack2<false>(__uint_as_float(o[16 * k + 2 * j]) * f, __uint_as_float(o[16 * k + 2 * j + 1]) * f);
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * k), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4*>(dst + 16 * k)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst + 16 * k)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
 }
 
 }  // namespace pkv
