@@ -132,15 +132,18 @@ def test_binding_refuses_wrong_tensors():
         pkv.paged_attention_decode_kv4(torch.empty_like(q), q, kc, kc, t(1, 4), t(2), 10, 0.1, 16)
 
 
-def test_binding_refuses_another_device(monkeypatch):
-    """Tensors of a device that is not the current one (none is needed here)."""
+def test_binding_refuses_another_device():
+    """Tensors of a device that is not the current one, strided ones (no GPU is needed for either)."""
     class Elsewhere:
         device = torch.device("cuda", 1)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    pkv._on_current_device(None)
-    with pytest.raises(ValueError):
-        pkv._on_current_device(Elsewhere())
+        get_device = staticmethod(lambda: 1)
+        is_contiguous = staticmethod(lambda: False)
+    assert pkv._at(None, 0) is None
+    for dev in (0, 1):
+        with pytest.raises(ValueError):
+            pkv._at(Elsewhere(), dev)
     for call in (pkv.paged_attention_decode_window, pkv.paged_attention_prefill_window, pkv.paged_kv4_write,
                  pkv.paged_kv4_read, pkv.paged_attention_decode_kv4, pkv.token_attention_decode_scored,
                  pkv.evict_tokens):
-        assert "_on_current_device(" in inspect.getsource(call)
+        text = inspect.getsource(call)
+        assert "_at(" in text and "_ptr(" not in text
