@@ -619,8 +619,9 @@ PKV_API pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, 
  * ------------------------------------------------------------------------ */
 
 /*
- * token_attention_decode_scored -- pkv_token_attention_decode (the same
- * output, bit for bit) that also adds, to scores[s][t] (fp32 [S, MT],
+ * token_attention_decode_scored -- pkv_token_attention_decode (with an
+ * explicit partition_size the same output, bit for bit; the library's choice
+ * splits a small launch further here) that also adds, to scores[s][t] (fp32 [S, MT],
  * row length MT as the table's) of every live token t, the attention weights
  * the sequence's query gives it, summed over the Hq query heads.  The sum
  * runs in a fixed order, so equal calls give equal bits; entries past

@@ -807,8 +807,10 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     p.out_scale = e4m3 ? v_scale : 1.f;
     set_workspace(p, pl, workspace, workspace_bytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = use_tc ? launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kWindow)
-                           : launch_decode_simt(p, q_dtype, cache_dtype, st);
+    const bool use_f32 = kernel == PKV_DECODE_AUTO && decode_f32_supports(cache_dtype, bs, NB);
+    cudaError_t e = use_tc    ? launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kWindow)
+                    : use_f32 ? launch_decode_f32(p, q_dtype, num_sms_current(), st)
+                              : launch_decode_simt(p, q_dtype, cache_dtype, st);
     if (e == cudaSuccess && pl.split) e = launch_decode_reduce(p, q_dtype, st);
     return from_cuda(e);
 }
@@ -896,7 +898,7 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
 
 size_t pkv_token_attention_scored_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_tokens,
                                                  int partition_size) {
-    const int P = resolve_partition(S, Hq, Hkv, d, bs, max_tokens, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, partition_size);
     return P < 0 ? 0 : make_scored_plan(S, Hq, Hkv, d, max_tokens, P).bytes;
 }
 
@@ -914,7 +916,7 @@ pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_d
                                              v_scale, partition_size, PKV_DECODE_TENSOR_CORES);
     if (chk != PKV_OK || S == 0) return chk;
     if (!scores || (reinterpret_cast<uintptr_t>(scores) & 3u)) return PKV_ERR_INVALID_ARG;
-    const int P = resolve_partition(S, Hq, Hkv, d, bs, max_tokens, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, partition_size);
     const ScoredPlan sp = make_scored_plan(S, Hq, Hkv, d, max_tokens, P);
     if (!workspace || workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;

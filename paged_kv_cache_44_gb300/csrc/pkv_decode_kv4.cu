@@ -564,8 +564,8 @@ cudaError_t launch_kv4_one(const DecodeParams& p, int num_sms, cudaStream_t st) 
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
     const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
-    const unsigned long long want = (units + C::kWarps - 1) / C::kWarps;
-    const int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
+    // a small launch puts its units on as many SMs as it has
+    const int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
     return launch_pdl(kern, dim3(grid < 1 ? 1 : grid), dim3(C::kWarps * 32), C::kSmemBytes, st, p, units, region_a,
                       nsets);
 }

@@ -813,7 +813,9 @@ cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
     const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
-    unsigned long long want = (units + C::kWarps - 1) / C::kWarps;
+    // with a window, or scored, a small launch puts its units on as many SMs as it has
+    const bool spread = MODE == DecodeMode::kWindow || MODE == DecodeMode::kScored;
+    unsigned long long want = spread ? units : (units + C::kWarps - 1) / C::kWarps;
     int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;
     return launch_pdl(kern, dim3(grid), dim3(C::kWarps * 32), C::kSmemBytes, st, p, kmap, vmap, units, region_a,

@@ -199,6 +199,9 @@ enum class DecodeMode {
 cudaError_t launch_decode_simt(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, cudaStream_t st);
 cudaError_t launch_decode_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms,
                              cudaStream_t st, DecodeMode mode = DecodeMode::kBlockTable);
+// the windowed decode over an fp32 cache
+bool decode_f32_supports(pkv_dtype c_dt, int bs, int NB);
+cudaError_t launch_decode_f32(const DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
 // scores[s][t] += the attention weights of a scored decode, rows of MT scores

@@ -46,7 +46,8 @@ def test_scored_decode(dtype, Hq, Hkv, d, bs, part):
     pkv.token_attention_decode_scored(out, q, k, v, slots, n, scores, max(lens), workspace=ws, err_word=err, **kw)
     pkv.token_attention_decode(plain, q, k, v, slots, n, max(lens), **kw)
     assert int(err) == 3
-    assert torch.equal(out, plain)
+    if part != 0:                                          # the library's own choice may split further
+        assert torch.equal(out, plain)
     again = before.clone()
     pkv.token_attention_decode_scored(out, q, k, v, slots, n, again, max(lens), workspace=ws, **kw)
     assert torch.equal(again, scores)
@@ -55,7 +56,9 @@ def test_scored_decode(dtype, Hq, Hkv, d, bs, part):
         assert torch.equal(scores[s, m:], before[s, m:])
         ok = slots[s, :m] < NB * bs
         idx = torch.where(ok, slots[s, :m], 0).long()
-        _, w, _, reach = P64.attend(q[s], flat[0][idx].double() * sc, flat[1][idx].double() * sc, ok, d ** -0.5)
+        o, w, mix, reach = P64.attend(q[s], flat[0][idx].double() * sc, flat[1][idx].double() * sc, ok, d ** -0.5)
+        p_eps, small = (2.0 ** -8, 0.0) if dtype == torch.bfloat16 else (2.0 ** -11, m * 2.0 ** -25 * 6.0)
+        P64.assert_within(out[s], o, P64.out_bound(o, mix, reach, d, p_eps, 2.0 ** -8, small), f"output of {m}")
         # a weight is off by the logits' error on both sides of the division and a few roundings;
         # the sum by a rounding per head
         rel = 2 * P64.logit_slack(reach, d)[:, None] + 2.0 ** -19 + Hq * 2.0 ** -24

@@ -91,7 +91,7 @@ def test_decode(dtype, shape, window, sinks):
     _decode_case(dtype, *shape, LENS, window, sinks, 0, "auto")
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, E4M3], ids=["f32", "bf16", "e4m3"])
 @pytest.mark.parametrize("part", [-1, 32, 64, 128])
 @pytest.mark.parametrize("kernel", ["auto", "cuda_cores"])
 def test_decode_partitions(dtype, part, kernel):
@@ -99,15 +99,30 @@ def test_decode_partitions(dtype, part, kernel):
     _decode_case(dtype, 8, 2, 64, 32, [5000, 1, 700], 1300, 70, part, kernel)
 
 
+def test_bf16_query_over_an_fp32_cache():
+    """The one mix of dtypes the tensor cores do not take."""
+    lens = [1, 40, 700]
+    seen_of = lambda s, n: P64.window_seen(n, n - 1, 300, 2)  # noqa: E731
+    (kc, vc), tables, dense, _ = _pool(lens, 2, 128, 16, torch.float32, 5, seen_of)
+    q = torch.randn(3, 12, 128, device="cuda").bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for kernel in ("auto", "cuda_cores"):
+        out = torch.empty_like(q)
+        pkv.paged_attention_decode_window(out, q, kc, vc, tables, n, 700, 0.1, 300, 2, kernel=kernel)
+        for s, m in enumerate(lens):
+            o, _, mix, reach = P64.attend(q[s], dense[0][s], dense[1][s], seen_of(s, m), 0.1)
+            P64.assert_within(out[s], o, P64.out_bound(o, mix, reach, 128, 0.0, 2.0 ** -8), f"{kernel} {m}")
+
+
 def test_window_of_every_token_equals_the_plain_decode():
-    for dtype in (torch.bfloat16, torch.float32):
+    for dtype, kernel in ((torch.bfloat16, "auto"), (torch.bfloat16, "cuda_cores"), (torch.float32, "cuda_cores")):
         lens = [1, 40, 700, 1500]
         (kc, vc), tables, _, _ = _pool(lens, 2, 128, 16, dtype, 5, lambda s, n: P64.window_seen(n, n, 0, 0))
         q = torch.randn(4, 12, 128, device="cuda").to(dtype)
         n = torch.tensor(lens, dtype=torch.int32, device="cuda")
         a, b = torch.empty_like(q), torch.empty_like(q)
-        pkv.paged_attention_decode(a, q, kc, vc, tables, n, 1500, 0.1, partition_size=128)
-        pkv.paged_attention_decode_window(b, q, kc, vc, tables, n, 1500, 0.1, 1500, 0, partition_size=128)
+        pkv.paged_attention_decode(a, q, kc, vc, tables, n, 1500, 0.1, partition_size=128, kernel=kernel)
+        pkv.paged_attention_decode_window(b, q, kc, vc, tables, n, 1500, 0.1, 1500, 0, partition_size=128, kernel=kernel)
         assert torch.equal(a, b)
 
 
