@@ -201,7 +201,7 @@ void set_workspace(DecodeParams& p, const DecodePlan& pl, void* workspace, size_
 // the logits of every token behind the partial results.
 struct ScoredPlan {
     DecodePlan pl;
-    size_t ml_offset, row_offset, logits_offset, bytes;
+    size_t ml_offset, logits_offset, bytes;
 };
 ScoredPlan make_scored_plan(int S, int Hq, int Hkv, int d, int max_tokens, int P) {
     ScoredPlan sp{};
@@ -210,8 +210,7 @@ ScoredPlan make_scored_plan(int S, int Hq, int Hkv, int d, int max_tokens, int P
     const int g = Hq / Hkv;
     const size_t sets = (size_t)S * Hkv * ((g + kHeadSet - 1) / kHeadSet);
     sp.ml_offset = sp.pl.split ? sp.pl.ml_offset : kWorkspaceHeaderBytes;
-    sp.row_offset = sp.pl.split ? sp.pl.bytes : sp.ml_offset;
-    sp.logits_offset = up(sp.row_offset + (size_t)S * Hq * 2 * sizeof(float));
+    sp.logits_offset = sp.pl.split ? sp.pl.bytes : up(sp.ml_offset + (size_t)S * Hq * 2 * sizeof(float));
     sp.bytes = up(sp.logits_offset + sets * max_tokens * score_width(g) * sizeof(float));
     return sp;
 }
@@ -933,12 +932,10 @@ pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_d
     set_workspace(p, sp.pl, workspace, workspace_bytes);
     char* ws = static_cast<char*>(workspace);
     p.part_ml = reinterpret_cast<float*>(ws + sp.ml_offset);
-    p.row_ml = reinterpret_cast<float*>(ws + sp.row_offset);
     p.logits = reinterpret_cast<float*>(ws + sp.logits_offset);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kScored);
-    if (e == cudaSuccess && sp.pl.split) e = launch_decode_reduce(p, q_dtype, st);
-    if (e == cudaSuccess) e = launch_score(p, scores, MT, st);
+    if (e == cudaSuccess) e = launch_score(p, q_dtype, sp.pl.split, scores, MT, st);
     return from_cuda(e);
 }
 

@@ -186,30 +186,9 @@ constexpr int kMergeWarps = 8;
 
 template <int D, typename QF>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_reduce_kernel(DecodeParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long gw = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();         // the decode's partial results
-    if (gw >= (long long)p.S * p.Hq) return;
-    const int s = (int)(gw / p.Hq), h = (int)(gw % p.Hq);
-    int n = p.context_lens[s];
-    n = n < 0 ? 0 : min(n, p.max_ctx);     // same clamp as the decode kernel: np <= Pmax
-    if (p.window > 0) n -= window_span(n - p.window, p.sinks, p.bs).gap;
-    const int np = num_partitions(n, p.P, p.Q, p.hold);
-    const size_t u0 = ((size_t)s * p.Hq + h) * p.Pmax;
-    if (np <= 1) {
-        // a scored decode wants every row's (max, sum) in one place; without tokens there is none
-        if (p.row_ml != nullptr && lane < 2) p.row_ml[2 * gw + lane] = n > 0 ? p.part_ml[2 * u0 + lane] : 0.f;
-        return;
-    }
-    float o[E], M;
-    const float L = merge_partitions<D>(p.part_ml + 2 * u0, p.part_acc + u0 * D, np, lane, o, &M);
-    if (p.row_ml != nullptr && lane == 0) reinterpret_cast<float2*>(p.row_ml)[gw] = make_float2(M, L);
-    const float f = L > 0.f ? p.out_scale / L : 0.f;
-    const size_t ob = ((size_t)s * p.Hq + h) * D + lane * E;
-#pragma unroll
-    for (int k = 0; k < E; ++k) store_elem<QF>(p.out, ob + k, o[k] * f);
+    merge_row<D, QF>(p, (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5), threadIdx.x & 31);
 }
 
 template <int D, typename QF>

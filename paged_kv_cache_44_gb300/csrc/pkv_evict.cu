@@ -8,6 +8,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "pkv_merge.cuh"
 #include "pkv_tc_common.cuh"
 #include "pkv_units.cuh"
 
@@ -22,66 +23,104 @@ namespace {
 // the sum is the same in every launch (no atomics).  The bound is the read
 // of the logits, 4 bytes per token and head: a head set's row of a token is
 // 32 consecutive bytes, a thread keeps kSets of them (two 16-byte loads
-// each) in flight.
+// each) in flight.  The decode's merge needs the same inputs and nothing of
+// this, so the grid's first blocks do it: one launch instead of two (one
+// sequence of 4,096 tokens: 22.7 -> 20.7 us; long launches the same).
 
-constexpr int kScoreThreads = 256;
+constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreRows = 512;          // (set, head) rows whose (M, 1 / L) are staged at a time
 constexpr int kSets = 4;                 // head sets a thread loads at once
 
-template <int W>                         // heads per row of logits
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, float* __restrict__ scores, int MT) {
+// (M, L) of another part of the same row joins (m, l).
+__device__ __forceinline__ void join(float& m, float& l, float M, float L) {
+    const float top = fmaxf(m, M);
+    const float a = m == top ? 1.f : exp2f(m - top), b = M == top ? 1.f : exp2f(M - top);   // -inf: no -inf - -inf
+    l = l * a + L * b;
+    m = top;
+}
+
+template <int W, int D, typename QF>     // W: heads per row of logits
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, float* __restrict__ scores, int MT,
+                                                              int merge_blocks, int chunks, int chunk) {
     __shared__ float2 ml[kScoreRows];    // (M, 1 / L); 1 / L = 0 for a row without weight or past the set's heads
-    const int s = blockIdx.y, tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
+    if ((int)blockIdx.x < merge_blocks) {
+        merge_row<D, QF>(p, (long long)blockIdx.x * kScoreWarps + warp, lane);
+        return;
+    }
+    const int job = blockIdx.x - merge_blocks, s = job / chunks, t0 = (job - s * chunks) * chunk;
     int n = p.context_lens[s];
     n = n < 0 ? 0 : min(n, p.max_ctx);   // the decode's clamp
-    if ((int)(blockIdx.x * kScoreThreads) >= n) return;
-    const int t = blockIdx.x * kScoreThreads + tid;
+    if (t0 >= n) return;
+    const int np = num_partitions(n, p.P, p.Q, p.hold);
     const int nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit, sets = p.Hkv * nsets;
     constexpr int kTile = kScoreRows / W;
-    float sum = 0.f;
-    for (int b0 = 0; b0 < sets; b0 += kTile) {
-        const int bn = min(kTile, sets - b0);
-        __syncthreads();
-        for (int i = tid; i < bn * W; i += kScoreThreads) {
-            const int set = b0 + i / W, kvh = set / nsets, hg = (set - kvh * nsets) * kHeadsPerUnit + i % W;
-            float2 v = make_float2(0.f, 0.f);
-            if (hg < p.g) v = __ldg(reinterpret_cast<const float2*>(p.row_ml) + (size_t)s * p.Hq + kvh * p.g + hg);
-            ml[i] = v.y > 0.f ? make_float2(v.x, 1.f / v.y) : make_float2(0.f, 0.f);
-        }
-        __syncthreads();
-        const float* x = p.logits + (((size_t)s * sets + b0) * p.max_ctx + t) * W;
-        const size_t set_stride = (size_t)p.max_ctx * W;
-        for (int b = 0; b < bn && t < n; b += kSets) {
-            float v[kSets][W];
+    const bool one_tile = sets <= kTile;
+    for (int tc0 = t0; tc0 < min(n, t0 + chunk); tc0 += kScoreThreads) {
+        const int t = tc0 + tid;
+        float sum = 0.f;
+        for (int b0 = 0; b0 < sets; b0 += kTile) {
+            const int bn = min(kTile, sets - b0);
+            if (!one_tile || tc0 == t0) {
+                // eight lanes per row, over its partitions
+                __syncthreads();
+                for (int i = tid / 8; i - (lane / 8) < bn * W; i += kScoreThreads / 8) {
+                    const int set = b0 + i / W, kvh = set / nsets;
+                    const int hg = (set - kvh * nsets) * kHeadsPerUnit + i % W;
+                    const bool on = i < bn * W && hg < p.g;
+                    float m = -CUDART_INF_F, l = 0.f;
+                    if (on) {
+                        const float2* src = reinterpret_cast<const float2*>(p.part_ml) +
+                                            ((size_t)s * p.Hq + kvh * p.g + hg) * p.Pmax;
+#pragma unroll 4
+                        for (int q = lane % 8; q < np; q += 8) {
+                            const float2 v = __ldcg(src + q);
+                            join(m, l, v.x, v.y);
+                        }
+                    }
 #pragma unroll
-            for (int k = 0; k < kSets; ++k) {
-                const float* src = x + (b + k) * set_stride;
+                    for (int o = 1; o < 8; o <<= 1) {
+                        const float M = __shfl_xor_sync(0xffffffffu, m, o), L = __shfl_xor_sync(0xffffffffu, l, o);
+                        join(m, l, M, L);
+                    }
+                    if (lane % 8 == 0 && i < bn * W) ml[i] = l != 0.f ? make_float2(m, 1.f / l) : make_float2(0.f, 0.f);
+                }
+                __syncthreads();
+            }
+            const float* x = p.logits + (((size_t)s * sets + b0) * p.max_ctx + t) * W;
+            const size_t set_stride = (size_t)p.max_ctx * W;
+            for (int b = 0; b < bn && t < n; b += kSets) {
+                float v[kSets][W];
 #pragma unroll
-                for (int j = 0; j < W; j += (W % 4 ? 2 : 4)) {
-                    if (b + k >= bn) continue;
-                    if constexpr (W % 4 == 0) {
-                        const float4 q = __ldcs(reinterpret_cast<const float4*>(src + j));
-                        v[k][j] = q.x; v[k][j + 1] = q.y; v[k][j + 2] = q.z; v[k][j + 3] = q.w;
-                    } else {
-                        const float2 q = __ldcs(reinterpret_cast<const float2*>(src + j));
-                        v[k][j] = q.x; v[k][j + 1] = q.y;
+                for (int k = 0; k < kSets; ++k) {
+                    const float* src = x + (b + k) * set_stride;
+#pragma unroll
+                    for (int j = 0; j < W; j += (W % 4 ? 2 : 4)) {
+                        if (b + k >= bn) continue;
+                        if constexpr (W % 4 == 0) {
+                            const float4 q = __ldcs(reinterpret_cast<const float4*>(src + j));
+                            v[k][j] = q.x; v[k][j + 1] = q.y; v[k][j + 2] = q.z; v[k][j + 3] = q.w;
+                        } else {
+                            const float2 q = __ldcs(reinterpret_cast<const float2*>(src + j));
+                            v[k][j] = q.x; v[k][j + 1] = q.y;
+                        }
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < kSets; ++k)
+                    if (b + k < bn)
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            const float2 a = ml[(b + k) * W + j];
+                            // a row without weight adds nothing, whatever its logits are (one with a NaN: NaN)
+                            if (a.y != 0.f) sum = fmaf(tc::fast_exp2(v[k][j] - a.x), a.y, sum);
+                        }
             }
-#pragma unroll
-            for (int k = 0; k < kSets; ++k)
-                if (b + k < bn)
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float2 a = ml[(b + k) * W + j];
-                        // a row without weight adds nothing, whatever its logits are
-                        if (a.y > 0.f) sum = fmaf(tc::fast_exp2(v[k][j] - a.x), a.y, sum);
-                    }
         }
+        if (t < n) scores[(size_t)s * MT + t] += sum;
     }
-    if (t < n) scores[(size_t)s * MT + t] += sum;
 }
 
 // ----------------------------------------------------------------- eviction
@@ -356,15 +395,29 @@ int evict_cluster(int S, int MT) {
 
 }  // namespace
 
-cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStream_t st) {
-    if (p.S == 0 || p.max_ctx == 0) return cudaSuccess;
-    const dim3 grid((unsigned)((p.max_ctx + kScoreThreads - 1) / kScoreThreads), (unsigned)p.S), block(kScoreThreads);
+template <int D, typename QF>
+static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scores, int MT, cudaStream_t st) {
+    const int merge_blocks = merge ? (int)(((long long)p.S * p.Hq + kScoreWarps - 1) / kScoreWarps) : 0;
+    // tokens per block: one per thread in a small launch, else four, so that the rows' (M, L) serve more
+    const long long small = (long long)p.S * ((p.max_ctx + kScoreThreads - 1) / kScoreThreads);
+    const int chunk = small <= 4 * 152 ? kScoreThreads : 4 * kScoreThreads;
+    const int chunks = (p.max_ctx + chunk - 1) / chunk;
+    const long long blocks = merge_blocks + (long long)p.S * chunks;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), block(kScoreThreads);
     switch (score_width(p.g)) {
-        case 2: return launch_pdl(score_kernel<2>, grid, block, 0, st, p, scores, MT);
-        case 4: return launch_pdl(score_kernel<4>, grid, block, 0, st, p, scores, MT);
-        case 6: return launch_pdl(score_kernel<6>, grid, block, 0, st, p, scores, MT);
-        default: return launch_pdl(score_kernel<8>, grid, block, 0, st, p, scores, MT);
+        case 2: return launch_pdl(score_kernel<2, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
+        case 4: return launch_pdl(score_kernel<4, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
+        case 6: return launch_pdl(score_kernel<6, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
+        default: return launch_pdl(score_kernel<8, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
     }
+}
+
+cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st) {
+    if (p.S == 0 || p.max_ctx == 0) return cudaSuccess;
+    if (p.d == 64)
+        return q_dt == PKV_F32 ? launch_score_d<64, F32>(p, merge, scores, MT, st) : launch_score_d<64, BF16>(p, merge, scores, MT, st);
+    return q_dt == PKV_F32 ? launch_score_d<128, F32>(p, merge, scores, MT, st) : launch_score_d<128, BF16>(p, merge, scores, MT, st);
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {

@@ -152,7 +152,6 @@ struct DecodeParams {
     // scored token-table decode: the logits (log2 units) of each unit's
     // tokens, rows of score_width(g) heads, [S][Hkv * head sets][max_ctx]
     float* logits;
-    float* row_ml;            // scored: the merged (max, sum) of every row, [S][Hq][2] (part_ml when not split)
 };
 
 struct EvictParams {
@@ -204,8 +203,8 @@ bool decode_f32_supports(pkv_dtype c_dt, int bs, int NB);
 cudaError_t launch_decode_f32(const DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
-// scores[s][t] += the attention weights of a scored decode, rows of MT scores
-cudaError_t launch_score(const DecodeParams& p, float* scores, int MT, cudaStream_t st);
+// after a scored decode: scores[s][t] += the attention weights (rows of MT scores) and, when split, the merge
+cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st);
 bool decode_tc_supports(pkv_dtype q_dt, pkv_dtype c_dt, int d, int bs, int NB);
 cudaError_t launch_prefill_tc(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                               bool merge, cudaStream_t st);

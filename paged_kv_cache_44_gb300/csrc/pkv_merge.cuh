@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "pkv_common.cuh"
+#include "pkv_internal.h"
 
 namespace pkv {
 
@@ -39,12 +40,11 @@ __device__ __forceinline__ void merge_load_row(const float* src, float (&a)[E], 
 
 // ml: the (m, l) pairs of the row's partitions [np][2]; acc: their rows
 // [np][D].  Lane i ends with o = elements [i*E, i*E+E) of sum 2^(m_p - M)
-// acc_p; returns L (the same on every lane) and, in *Mout, M.  The data were written by
+// acc_p; returns L (the same on every lane).  The data were written by
 // another kernel: loads go through L2 (ld.global.cg).
 template <int D>
 __device__ __forceinline__ float merge_partitions(const float* __restrict__ ml, const float* __restrict__ acc,
-                                                  int np, int lane, float (&o)[D / 32],
-                                                  float* Mout = nullptr) {
+                                                  int np, int lane, float (&o)[D / 32]) {
     constexpr int E = D / 32, B = kMergeChunk;
     const uint64_t once = l2_policy_evict_first();
     float M = -CUDART_INF_F, lpart = 0.f;
@@ -88,8 +88,28 @@ __device__ __forceinline__ float merge_partitions(const float* __restrict__ ml, 
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) lpart += __shfl_xor_sync(0xffffffffu, lpart, off);
-    if (Mout != nullptr) *Mout = M;
     return lpart;
+}
+
+// The output of row (sequence, query head) `row` of a decode, by one warp.
+// Sequences that fit one partition were finished by the decode kernel.
+template <int D, typename QF>
+__device__ __forceinline__ void merge_row(const DecodeParams& p, long long row, int lane) {
+    constexpr int E = D / 32;
+    if (row >= (long long)p.S * p.Hq) return;
+    const int s = (int)(row / p.Hq);
+    int n = p.context_lens[s];
+    n = n < 0 ? 0 : min(n, p.max_ctx);     // same clamp as the decode kernel: np <= Pmax
+    if (p.window > 0) n -= window_span(n - p.window, p.sinks, p.bs).gap;
+    const int np = num_partitions(n, p.P, p.Q, p.hold);
+    if (np <= 1) return;
+    const size_t u0 = (size_t)row * p.Pmax;
+    float o[E];
+    const float L = merge_partitions<D>(p.part_ml + 2 * u0, p.part_acc + u0 * D, np, lane, o);
+    const float f = L > 0.f ? p.out_scale / L : 0.f;
+    const size_t ob = (size_t)row * D + lane * E;
+#pragma unroll
+    for (int k = 0; k < E; ++k) store_elem<QF>(p.out, ob + k, o[k] * f);
 }
 
 }  // namespace pkv
