@@ -27,7 +27,7 @@ constexpr int kThreads = 128;
 constexpr int kChunk = 64;
 constexpr int kHeads = 8;       // query heads per CTA
 
-template <int D, typename QF, typename CF>
+template <int D, typename QF, typename CF, bool WIN>
 __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
     const int s = blockIdx.z;
     const int nsets = (p.g + kHeads - 1) / kHeads;
@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
     }
     // with a window, tokens are numbered without the blocks the query does not see
     const int first_seen = n - p.window;
-    WindowSpan span{n, 0};
-    if (p.window > 0) {
+    WindowSpan span{};
+    if constexpr (WIN) {
         span = window_span(first_seen, p.sinks, p.bs);
         n -= span.gap;
     }
@@ -80,8 +80,8 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(DecodeParams p) {
         const int cn = min(kChunk, t1 - c0);
         // physical row of each token of the chunk (-1 when its block id is bad or the query does not see it)
         for (int tt = threadIdx.x; tt < cn; tt += kThreads) {
-            const int t = span_token(span, c0 + tt);
-            if (p.window > 0 && t >= p.sinks && t < first_seen) {
+            const int t = WIN ? span_token(span, c0 + tt) : c0 + tt;
+            if (WIN && t >= p.sinks && t < first_seen) {
                 pb_s[tt] = -1;
                 continue;
             }
@@ -206,11 +206,16 @@ cudaError_t launch_reduce(const DecodeParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, decode_reduce_kernel<D, QF>, p);
 }
 
+template <int D, typename QF, bool WIN>
+cudaError_t launch_simt_win(const DecodeParams& p, pkv_dtype c_dt, dim3 grid, cudaStream_t st) {
+    if (c_dt == PKV_F32) return launch_pdl(decode_simt_kernel<D, QF, F32, WIN>, grid, dim3(kThreads), 0, st, p);
+    if (c_dt == PKV_BF16) return launch_pdl(decode_simt_kernel<D, QF, BF16, WIN>, grid, dim3(kThreads), 0, st, p);
+    return launch_pdl(decode_simt_kernel<D, QF, E4M3, WIN>, grid, dim3(kThreads), 0, st, p);
+}
+
 template <int D, typename QF>
 cudaError_t launch_simt_q(const DecodeParams& p, pkv_dtype c_dt, dim3 grid, cudaStream_t st) {
-    if (c_dt == PKV_F32) return launch_pdl(decode_simt_kernel<D, QF, F32>, grid, dim3(kThreads), 0, st, p);
-    if (c_dt == PKV_BF16) return launch_pdl(decode_simt_kernel<D, QF, BF16>, grid, dim3(kThreads), 0, st, p);
-    return launch_pdl(decode_simt_kernel<D, QF, E4M3>, grid, dim3(kThreads), 0, st, p);
+    return p.window > 0 ? launch_simt_win<D, QF, true>(p, c_dt, grid, st) : launch_simt_win<D, QF, false>(p, c_dt, grid, st);
 }
 
 }  // namespace

@@ -202,6 +202,10 @@ cudaError_t launch_decode_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_
 bool decode_f32_supports(pkv_dtype c_dt, int bs, int NB);
 cudaError_t launch_decode_f32(const DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st);
+// its modes, in translation units of their own
+cudaError_t launch_decode_tc_token(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_window(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_scored(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
 // after a scored decode: scores[s][t] += the attention weights (rows of MT scores) and, when split, the merge
 cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st);
