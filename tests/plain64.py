@@ -71,7 +71,8 @@ def assert_within(got, ref, bound, what=""):
 def kv4_values(x, by):
     """fp32 values that rows x (numpy float32 [..., d]) stand for after the
     4-bit write with tensor scale `by`: the definition's fp32 operations."""
-    y = (x.astype(np.float32) / np.float32(by)).astype(np.float32)
+    with np.errstate(over="ignore"):
+        y = (x.astype(np.float32) / np.float32(by)).astype(np.float32)
     y = np.clip(y, np.float32(-65504), np.float32(65504)).reshape(*x.shape[:-1], -1, 32)
     with np.errstate(invalid="ignore", divide="ignore"):
         zero = y.min(-1, keepdims=True).astype(np.float16).astype(np.float32)
@@ -80,7 +81,8 @@ def kv4_values(x, by):
         code = np.where(step > 0, np.clip(np.rint((y - zero) / step), 0, 15), np.float32(0)).astype(np.float32)
     bad = np.isnan(y).any(-1, keepdims=True)
     val = np.where(bad, np.float32(np.nan), zero + step * code)
-    return (val * np.float32(by)).astype(np.float32).reshape(x.shape)
+    with np.errstate(over="ignore"):
+        return (val * np.float32(by)).astype(np.float32).reshape(x.shape)
 
 
 def kv4_block(cache, block, head, bs, d, value):

@@ -114,6 +114,52 @@ def test_evict(kind, lens, budget, first, recent):
         assert ev[s].tolist() == c + [-9] * (MT - len(c))
 
 
+def test_evict_in_a_graph_over_a_cluster():
+    """A few long sequences (several blocks each), captured and replayed on other scores and counts, on two streams."""
+    S, MT = 2, 40000
+    rng = np.random.default_rng(7)
+    slots = torch.from_numpy(rng.permutation(S * MT).reshape(S, MT).astype(np.int32)).cuda()
+    scores, n = torch.zeros(S, MT, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    ns, nsc, nn, ev = torch.zeros_like(slots), torch.zeros_like(scores), torch.zeros_like(n), torch.zeros_like(slots)
+    call = lambda: pkv.evict_tokens(slots, scores, n, ns, nsc, nn, 5000, 4, 100, ev)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed, lens in ((1, [40000, 5001]), (2, [5000, 33333])):
+        x = _scores("ties", S, MT, np.random.default_rng(seed))
+        scores.copy_(torch.from_numpy(x))
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        other = [torch.zeros_like(t) for t in (ns, nsc, nn)]
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            pkv.evict_tokens(slots, scores, n, *other, 5000, 4, 100)
+        graph.replay()
+        torch.cuda.synchronize()
+        for s, m in enumerate(lens):
+            a, b, c = _evict_reference(slots[s].tolist(), x[s].tolist(), m, 5000, 4, 100)
+            assert ns[s, :len(a)].tolist() == a and ev[s, :len(c)].tolist() == c and int(nn[s]) == len(a)
+            assert other[0][s, :len(a)].tolist() == a
+            np.testing.assert_array_equal(nsc[s, :len(b)].cpu().numpy(), np.array(b, np.float32))
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scored_decode_with_other_logit_scales(scale):
+    S, MT, Hq, Hkv, d, bs = 2, 700, 6, 2, 64, 16
+    k, v, _ = _pools(100, bs, Hkv, d, torch.bfloat16, 3)
+    slots = torch.randperm(1600, device="cuda")[:S * MT].view(S, MT).int()
+    q = torch.randn(S, Hq, d, device="cuda").bfloat16()
+    n, scores = torch.tensor([700, 13], dtype=torch.int32, device="cuda"), torch.zeros(S, MT, device="cuda")
+    pkv.token_attention_decode_scored(torch.empty_like(q), q, k, v, slots, n, scores, MT, scale, partition_size=128)
+    for s, m in enumerate((700, 13)):
+        idx = slots[s, :m].long()
+        _, w, _, reach = P64.attend(q[s], k.flatten(0, 1)[idx], v.flatten(0, 1)[idx],
+                                    torch.ones(m, dtype=torch.bool, device="cuda"), scale)
+        P64.assert_within(scores[s, :m], w.sum(0), ((2 * P64.logit_slack(reach, d)[:, None] + 2.0 ** -18) * w).sum(0))
+
+
 def test_evict_without_a_list_and_with_bad_counts():
     S, MT = 3, 300
     rng = np.random.default_rng(1)

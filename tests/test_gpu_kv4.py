@@ -28,7 +28,7 @@ def _rows(T, Hkv, d, dtype, seed):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("T,Hkv,d,bs", [(1, 1, 64, 16), (37, 2, 128, 16), (100, 3, 64, 32), (333, 8, 128, 32)])
-@pytest.mark.parametrize("scales", [(1.0, 1.0), (0.37, 2.5)])
+@pytest.mark.parametrize("scales", [(1.0, 1.0), (0.37, 2.5), (1e-30, 1e30), (1e-40, 3e38)])
 def test_write_and_read(dtype, T, Hkv, d, bs, scales):
     NB = -(-T // bs) + 3
     key, k32 = _rows(T, Hkv, d, dtype, 1)
@@ -63,7 +63,10 @@ def test_write_and_read(dtype, T, Hkv, d, bs, scales):
                 for i, s in enumerate(slots):
                     if s >= 0 and s // bs == b:
                         want = P64.kv4_values(x[i, h], by).astype(np.float64)
-                        np.testing.assert_allclose(got[s % bs] * by, want, rtol=2.0 ** -22, equal_nan=True)
+                        # the call takes the scale as fp32 and rounds the product to fp32 (subnormal, or past its range)
+                        with np.errstate(over="ignore"):
+                            val = (got[s % bs] * np.float64(np.float32(by))).astype(np.float32).astype(np.float64)
+                        np.testing.assert_allclose(val, want, rtol=2.0 ** -22, atol=2.0 ** -148, equal_nan=True)
     fresh = np.setdiff1d(np.arange(NB * bs), slots)
     for b in sorted({int(s) // bs for s in fresh})[:4]:
         ref = np.full((1, 1, kn.shape[2]), 0xA5, np.uint8)
@@ -104,7 +107,7 @@ def test_bad_slots_are_reported_and_touch_nothing():
     assert int(err) == 3 and (out == 4).all()
 
 
-def _decode_case(Hq, Hkv, d, bs, lens, window, sinks, part, seed=1, scales=(0.5, 2.0)):
+def _decode_case(Hq, Hkv, d, bs, lens, window, sinks, part, seed=1, scales=(0.5, 2.0), scale=None):
     """The pool is written by the library; slots no query sees then get
     codes, scales and zeros of NaN, unseen blocks' entries go out of range."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -132,14 +135,14 @@ def _decode_case(Hq, Hkv, d, bs, lens, window, sinks, part, seed=1, scales=(0.5,
     q = torch.randn(len(lens), Hq, d, device="cuda", generator=g).bfloat16()
     n = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out, err = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
-    mx = max(lens)
+    mx, scale = max(lens), d ** -0.5 if scale is None else scale
     ws = pkv.make_window_workspace(len(lens), Hq, Hkv, d, bs, mx, window, sinks, part)
-    pkv.paged_attention_decode_kv4(out, q, kc, vc, tables, n, mx, d ** -0.5, bs, window, sinks, *scales,
+    pkv.paged_attention_decode_kv4(out, q, kc, vc, tables, n, mx, scale, bs, window, sinks, *scales,
                                    partition_size=part, workspace=ws, err_word=err)
     torch.cuda.synchronize()
     assert int(err) == 0
     for s, (k, v, seen) in enumerate(dense):
-        o, _, mix, reach = P64.attend(q[s], k, v, seen, d ** -0.5)
+        o, _, mix, reach = P64.attend(q[s], k, v, seen, scale)
         if not seen.any():
             assert (out[s] == 0).all()
             continue
@@ -163,11 +166,81 @@ def test_decode(shape, window, sinks):
     _decode_case(*shape, LENS, window, sinks, 0)
 
 
-@pytest.mark.parametrize("part", [-1, 32, 64, 128])
+@pytest.mark.parametrize("part", [-1, 16, 32, 48, 64, 128])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (777, 20)])
 def test_decode_partitions(part, window, sinks):
     _decode_case(16, 2, 128, 16, LENS, window, sinks, part)
-    _decode_case(8, 2, 64, 32, [5000, 1, 700], window, sinks, part)
+    _decode_case(8, 2, 64, 32, [5000, 1, 700], window, sinks, part if part % 32 == 0 else -1)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_decode_with_other_logit_scales(scale):
+    """Negative (the smallest product weighs most), zero (every token weighs the same), and large."""
+    _decode_case(12, 2, 128, 16, [1, 100, 1500], 0, 0, 128, scale=scale)
+    _decode_case(7, 1, 64, 32, [33, 700], 100, 5, 0, scale=scale)
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 bytes: write, read and decode in their last blocks."""
+    bs, Hkv, d, Hq, n = 16, 8, 128, 16, 300
+    NB = (1 << 32) // (Hkv * 1280) + 1000
+    kc, vc = (pkv.make_kv4_cache(NB, bs, Hkv, d) for _ in range(2))
+    assert kc.numel() > 1 << 32
+    pos = torch.arange(n, device="cuda")
+    ids = NB - 1 - torch.arange(-(-n // bs), device="cuda")
+    slots = ids[pos // bs] * bs + pos % bs
+    k, v = torch.randn(2, n, Hkv, d, device="cuda")
+    pkv.paged_kv4_write(k, v, kc, vc, slots, bs)
+    ko, vo = torch.zeros(2, n, Hkv, d, device="cuda")
+    pkv.paged_kv4_read(ko, vo, kc, vc, slots, bs)
+    np.testing.assert_array_equal(ko.cpu().numpy(), P64.kv4_values(k.cpu().numpy(), 1.0))
+    assert not kc[:1000].any() and not vc[:1000].any()
+    q = torch.randn(1, Hq, d, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    pkv.paged_attention_decode_kv4(out, q, kc, vc, ids.int()[None].contiguous(),
+                                   torch.tensor([n], dtype=torch.int32, device="cuda"), n, 0.1, bs)
+    o, _, mix, reach = P64.attend(q[0], ko, vo, torch.ones(n, dtype=torch.bool, device="cuda"), 0.1)
+    P64.assert_within(out[0], o, P64.out_bound(o, mix, 4 * reach, d, 2.0 ** -8, 2.0 ** -8) + 2.0 ** -7)
+
+
+def test_a_nan_reaches_its_head_only():
+    """A NaN written to one value of one token of K/V head 0 makes that head's queries NaN, and no others."""
+    bs, Hkv, d, Hq, n = 16, 2, 64, 8, 100
+    kc, vc = (pkv.make_kv4_cache(14, bs, Hkv, d) for _ in range(2))
+    k, v = torch.randn(2, 2 * 7 * bs, Hkv, d, device="cuda")
+    k[50, 0, 3] = float("nan")                              # sequence 0
+    pkv.paged_kv4_write(k, v, kc, vc, torch.arange(2 * 7 * bs, device="cuda"), bs)
+    q = torch.randn(2, Hq, d, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    tables = torch.arange(14, dtype=torch.int32, device="cuda").view(2, 7)
+    lens = torch.full((2,), n, dtype=torch.int32, device="cuda")
+    pkv.paged_attention_decode_kv4(out, q, kc, vc, tables, lens, n, 0.1, bs)
+    nan = torch.isnan(out).any(-1).cpu()
+    assert nan[0, :4].all() and not nan[0, 4:].any() and not nan[1].any()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with its own workspace and output."""
+    bs, Hkv, d, Hq, n = 16, 2, 128, 12, 3000
+    nb = -(-n // bs)
+    kc, vc = (pkv.make_kv4_cache(8 * nb, bs, Hkv, d) for _ in range(2))
+    k, v = torch.randn(2, 8 * nb * bs, Hkv, d, device="cuda").bfloat16()
+    pkv.paged_kv4_write(k, v, kc, vc, torch.randperm(8 * nb * bs, device="cuda"), bs)
+    tables = torch.randperm(8 * nb, device="cuda").int().view(8, nb)
+    lens = torch.full((8,), n, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 8, Hq, d, device="cuda").bfloat16()
+    ref, got = torch.empty_like(q), torch.empty_like(q)
+    ws = [pkv.make_window_workspace(8, Hq, Hkv, d, bs, n, 0) for _ in range(2)]
+    for i in range(2):
+        pkv.paged_attention_decode_kv4(ref[i], q[i], kc, vc, tables, lens, n, 0.1, bs, workspace=ws[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                pkv.paged_attention_decode_kv4(got[i], q[i], kc, vc, tables, lens, n, 0.1, bs, workspace=ws[i])
+    torch.cuda.synchronize()
+    assert torch.equal(ref, got)
 
 
 def test_decode_long_sequence():

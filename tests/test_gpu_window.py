@@ -53,7 +53,7 @@ def _pool(lens, Hkv, d, bs, dtype, seed, seen_of):
     return pools, tables.cuda(), dense, scale
 
 
-def _decode_case(dtype, Hq, Hkv, d, bs, lens, window, sinks, part, kernel, seed=1):
+def _decode_case(dtype, Hq, Hkv, d, bs, lens, window, sinks, part, kernel, seed=1, scale=None):
     seen_of = lambda s, n: P64.window_seen(n, n - 1, window, sinks)  # noqa: E731
     (kc, vc), tables, dense, sc = _pool(lens, Hkv, d, bs, dtype, seed, seen_of)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
@@ -62,9 +62,9 @@ def _decode_case(dtype, Hq, Hkv, d, bs, lens, window, sinks, part, kernel, seed=
     n = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out = torch.full_like(q, 7.0)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    mx = max(lens)
+    mx, scale = max(lens), d ** -0.5 if scale is None else scale
     ws = pkv.make_window_workspace(len(lens), Hq, Hkv, d, bs, mx, window, sinks, part)
-    pkv.paged_attention_decode_window(out, q, kc, vc, tables, n, mx, d ** -0.5, window, sinks, k_scale=sc, v_scale=sc,
+    pkv.paged_attention_decode_window(out, q, kc, vc, tables, n, mx, scale, window, sinks, k_scale=sc, v_scale=sc,
                                       partition_size=part, workspace=ws, err_word=err, kernel=kernel)
     torch.cuda.synchronize()
     assert int(err) == 0
@@ -73,7 +73,7 @@ def _decode_case(dtype, Hq, Hkv, d, bs, lens, window, sinks, part, kernel, seed=
     p_eps = (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11) if tc else 0.0
     for s, m in enumerate(lens):
         k, v = dense[0][s], dense[1][s]
-        o, _, mix, reach = P64.attend(q[s], k, v, seen_of(s, m), d ** -0.5)
+        o, _, mix, reach = P64.attend(q[s], k, v, seen_of(s, m), scale)
         small = m * 2.0 ** -25 * float(v.abs().max()) if tc and dtype == E4M3 and m else 0.0   # fp16 weights below 2^-14
         P64.assert_within(out[s], o, P64.out_bound(o, mix, reach, d, p_eps, P64.HALF[qdt], small),
                           f"sequence {s} of {m} tokens")
@@ -92,11 +92,37 @@ def test_decode(dtype, shape, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, E4M3], ids=["f32", "bf16", "e4m3"])
-@pytest.mark.parametrize("part", [-1, 32, 64, 128])
+@pytest.mark.parametrize("part", [-1, 16, 32, 48, 64, 128])
 @pytest.mark.parametrize("kernel", ["auto", "cuda_cores"])
 def test_decode_partitions(dtype, part, kernel):
     _decode_case(dtype, 16, 2, 128, 16, LENS, 777, 20, part, kernel)
-    _decode_case(dtype, 8, 2, 64, 32, [5000, 1, 700], 1300, 70, part, kernel)
+    _decode_case(dtype, 8, 2, 64, 32, [5000, 1, 700], 1300, 70, part if part % 32 == 0 else -1, kernel)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, E4M3], ids=["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 2.0])
+def test_decode_with_other_logit_scales(dtype, scale):
+    _decode_case(dtype, 12, 2, 128, 16, [1, 100, 1500], 900, 3, 128, "auto", scale=scale)
+    _decode_case(dtype, 7, 1, 64, 32, [33, 700], 100, 5, 0, "auto", scale=scale)
+
+
+def test_fp32_offsets_past_32_bits():
+    """An fp32 pool of more than 2^32 bytes, the sequence in its last blocks."""
+    bs, Hkv, d, Hq, n = 16, 8, 128, 16, 300
+    NB = (1 << 32) // (bs * Hkv * d * 4) + 100
+    kc, vc = torch.zeros(2, NB, bs, Hkv, d, device="cuda")
+    ids = NB - 1 - torch.arange(-(-n // bs), device="cuda")
+    for c in (kc, vc):
+        c[ids] = torch.randn(ids.numel(), bs, Hkv, d, device="cuda")
+    q = torch.randn(1, Hq, d, device="cuda")
+    for kernel in ("auto", "cuda_cores"):
+        out = torch.empty_like(q)
+        pkv.paged_attention_decode_window(out, q, kc, vc, ids.int()[None].contiguous(),
+                                          torch.tensor([n], dtype=torch.int32, device="cuda"), n, 0.1, 200, 4,
+                                          kernel=kernel)
+        o, _, mix, reach = P64.attend(q[0], kc[ids].flatten(0, 1)[:n], vc[ids].flatten(0, 1)[:n],
+                                      P64.window_seen(n, n - 1, 200, 4), 0.1)
+        P64.assert_within(out[0], o, P64.out_bound(o, mix, reach, d, 0.0, 2.0 ** -24), kernel)
 
 
 def test_bf16_query_over_an_fp32_cache():
@@ -126,7 +152,7 @@ def test_window_of_every_token_equals_the_plain_decode():
         assert torch.equal(a, b)
 
 
-def _prefill_case(Hq, Hkv, d, bs, chunks, window, sinks, part, seed=3):
+def _prefill_case(Hq, Hkv, d, bs, chunks, window, sinks, part, seed=3, scale=None):
     """chunks: (queries, length) per sequence."""
     def seen_of(s, n):
         ql = chunks[s][0]
@@ -144,7 +170,8 @@ def _prefill_case(Hq, Hkv, d, bs, chunks, window, sinks, part, seed=3):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     mq, mx = max(c[0] for c in chunks), max(lens)
     ws = pkv.make_prefill_window_workspace(len(chunks), T, mq, Hq, Hkv, d, bs, mx, window, sinks, part)
-    pkv.paged_attention_prefill_window(out, q, kc, vc, tables, n, start, mq, mx, d ** -0.5, window, sinks,
+    scale = d ** -0.5 if scale is None else scale
+    pkv.paged_attention_prefill_window(out, q, kc, vc, tables, n, start, mq, mx, scale, window, sinks,
                                        partition_size=part, workspace=ws, err_word=err)
     torch.cuda.synchronize()
     assert int(err) == 0
@@ -153,7 +180,7 @@ def _prefill_case(Hq, Hkv, d, bs, chunks, window, sinks, part, seed=3):
         rows = range(ql) if ql <= 40 else sorted({0, 1, ql // 3, ql // 2, ql - 2, ql - 1, 18 % ql, 37 % ql})
         for i in rows:
             o, _, mix, reach = P64.attend(q[at + i], dense[0][s], dense[1][s],
-                                          P64.window_seen(m, m - ql + i, window, sinks), d ** -0.5)
+                                          P64.window_seen(m, m - ql + i, window, sinks), scale)
             P64.assert_within(out[at + i], o, P64.out_bound(o, mix, reach, d, 2.0 ** -8, 2.0 ** -8),
                               f"query {i} of {ql}, length {m}")
         at += ql
@@ -172,6 +199,19 @@ def test_prefill(shape, window, sinks, part):
 
 def test_prefill_few_queries_takes_the_single_tile_kernel():
     _prefill_case(28, 4, 128, 16, [(5, 3000), (5, 5), (2, 1200)], 1000, 4, 0)
+
+
+@pytest.mark.parametrize("g", [1, 2, 3, 5, 6, 9, 12, 28, 48, 100, 128, 130])
+def test_prefill_group_sizes(g):
+    """Tiles that begin and end inside a query, hold one query, or less than one."""
+    ql = max(4, 600 // g)
+    _prefill_case(g, 1, 128, 16, [(ql, ql + 100), (ql // 2, ql // 2), (3, 400)], 130, 3, 0)
+    _prefill_case(2 * g, 2, 64, 32, [(ql, ql)], 64, 0, 0)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_prefill_with_other_logit_scales(scale):
+    _prefill_case(14, 2, 128, 16, [(200, 700), (1, 50)], 150, 4, 0, scale=scale)
 
 
 def test_bad_block_and_length_are_reported():
