@@ -546,10 +546,9 @@ def make_kv4_cache(NB: int, block_size: int, Hkv: int, d: int, device=None) -> t
 
 
 def _check_kv4(key_cache: torch.Tensor, value_cache: torch.Tensor, block_size: int, Hkv: int, d: int) -> None:
-    n = kv4_block_bytes(block_size, Hkv, d)
-    if key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8 or key_cache.dim() != 3 or \
-            value_cache.shape != key_cache.shape or key_cache.shape[1] != Hkv or \
-            (n != 0 and key_cache.shape[2] * Hkv != n):
+    shape = key_cache.shape
+    if key_cache.dtype != torch.uint8 or value_cache.dtype != torch.uint8 or len(shape) != 3 or \
+            value_cache.shape != shape or shape[1] != Hkv or shape[2] != block_size * (d // 2 + d // 8):
         raise ValueError("4-bit caches are uint8 [NB, Hkv, kv4_block_bytes(block_size, Hkv, d) // Hkv]")
 
 
@@ -675,13 +674,14 @@ def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: to
     """Cut every sequence to `budget` tokens: its first num_first, its last
     num_recent and the highest scores of the rest, in order, into new_slots,
     new_scores [S, MT] and new_num [S]; the dropped slots go to evicted."""
-    S, MT = token_slots.shape
-    for t, dt, shape in ((token_slots, torch.int32, (S, MT)), (scores, torch.float32, (S, MT)),
-                         (num_tokens, torch.int32, (S,)), (new_slots, torch.int32, (S, MT)),
-                         (new_scores, torch.float32, (S, MT)), (new_num, torch.int32, (S,)),
-                         (evicted, torch.int32, (S, MT))):
-        if t is not None and (t.dtype != dt or tuple(t.shape) != shape):
-            raise ValueError("tables are int32 and scores float32, [S, MT]; counts are int32 [S]")
+    S, MT = table = token_slots.shape
+    i32, f32 = torch.int32, torch.float32
+    if token_slots.dtype != i32 or scores.dtype != f32 or num_tokens.dtype != i32 or new_slots.dtype != i32 or \
+            new_scores.dtype != f32 or new_num.dtype != i32 or (evicted is not None and evicted.dtype != i32):
+        raise ValueError("tables and counts are int32, scores float32")
+    if scores.shape != table or new_slots.shape != table or new_scores.shape != table or \
+            (evicted is not None and evicted.shape != table) or num_tokens.shape != (S,) or new_num.shape != (S,):
+        raise ValueError("tables and scores are [S, MT], counts [S]")
     dev = torch.cuda.current_device()
     _check("evict_tokens", lib.pkv_evict_tokens(
         _at(token_slots, dev), _at(scores, dev), _at(num_tokens, dev), S, MT, int(budget), int(num_first),
