@@ -162,14 +162,14 @@ def version() -> str:
     return lib.pkv_version().decode()
 
 
+_DTYPE_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3, torch.uint8: FP8_E4M3}
+
+
 def dtype_code(t: torch.dtype) -> int:
-    if t == torch.float32:
-        return F32
-    if t == torch.bfloat16:
-        return BF16
-    if t in (torch.float8_e4m3fn, torch.uint8):
-        return FP8_E4M3
-    raise TypeError(f"unsupported dtype {t}")
+    code = _DTYPE_CODES.get(t)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t}")
+    return code
 
 
 # the current stream's handle without building a Stream object (0.1 us instead of 3)
@@ -431,15 +431,20 @@ def repack_tokens(key_caches: Sequence[torch.Tensor], value_caches: Sequence[tor
                                                   token_bytes, _ptr(err_word), _stream(stream)))
 
 
-def _at(t: Optional[torch.Tensor], dev: int) -> Optional[int]:
-    """_ptr of a tensor on device `dev`, the current one: the launch goes there."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise ValueError(f"pkv calls take tensors of the current CUDA device ({dev}), got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError("pkv calls take contiguous tensors")
-    return t.data_ptr()
+def _pointers(*tensors: Optional[torch.Tensor]) -> list:
+    """The tensors' addresses (None stays).  The launch goes to the current
+    device: tensors of another one are refused, and so are strided ones."""
+    dev, out = torch.cuda.current_device(), []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() != dev:
+            raise ValueError(f"pkv calls take tensors of the current CUDA device ({dev}), got one on {t.device}")
+        elif not t.is_contiguous():
+            raise ValueError("pkv calls take contiguous tensors")
+        else:
+            out.append(t.data_ptr())
+    return out
 
 
 # ---- sliding window with sinks
@@ -475,13 +480,13 @@ def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_ca
     if workspace is None:
         workspace = make_window_workspace(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks, partition_size,
                                           device=query.device)
-    dev = torch.cuda.current_device()
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
+        out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
     _check("paged_attention_decode_window", lib.pkv_paged_attention_decode_window(
-        _at(out, dev), _at(query, dev), dtype_code(query.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        dtype_code(key_cache.dtype), _at(block_tables, dev), block_tables.shape[1], _at(context_lens, dev), S,
-        int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(window),
-        int(num_sinks), int(partition_size), _at(workspace, dev), workspace.numel() * workspace.element_size(),
-        _at(err_word, dev), _stream(stream), KERNELS[kernel]))
+        p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_bt, block_tables.shape[1], p_cl,
+        S, int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(window),
+        int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
+        _stream(stream), KERNELS[kernel]))
     return out
 
 
@@ -520,13 +525,13 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     if workspace is None:
         workspace = make_prefill_window_workspace(S, T, max_query_len, Hq, Hkv, d, bs, max_context_len, window,
                                                   num_sinks, partition_size, device=query.device)
-    dev = torch.cuda.current_device()
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_qs, p_ws, p_err = _pointers(
+        out, query, key_cache, value_cache, block_tables, context_lens, query_start, workspace, err_word)
     _check("paged_attention_prefill_window", lib.pkv_paged_attention_prefill_window(
-        _at(out, dev), _at(query, dev), dtype_code(query.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        dtype_code(key_cache.dtype), _at(block_tables, dev), block_tables.shape[1], _at(context_lens, dev),
-        _at(query_start, dev), S, T, int(max_query_len), int(max_context_len), Hq, Hkv, d, bs, NB, float(scale),
-        int(window), int(num_sinks), int(partition_size), _at(workspace, dev),
-        workspace.numel() * workspace.element_size(), _at(err_word, dev), _stream(stream)))
+        p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_bt, block_tables.shape[1], p_cl,
+        p_qs, S, T, int(max_query_len), int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), int(window),
+        int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
+        _stream(stream)))
     return out
 
 
@@ -570,11 +575,11 @@ def paged_kv4_write(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Ten
         raise ValueError("key and value must share shape and dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [T]")
-    dev = torch.cuda.current_device()
+    p_k, p_v, p_kc, p_vc, p_sm, p_err = _pointers(
+        key, value, key_cache, value_cache, slot_mapping, err_word)
     _check("paged_kv4_write", lib.pkv_paged_kv4_write(
-        _at(key, dev), _at(value, dev), dtype_code(key.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        _at(slot_mapping, dev), T,
-        key_cache.shape[0], block_size, Hkv, d, float(k_scale), float(v_scale), _at(err_word, dev), _stream(stream)))
+        p_k, p_v, dtype_code(key.dtype), p_kc, p_vc, p_sm, T, key_cache.shape[0], block_size, Hkv, d, float(k_scale),
+        float(v_scale), p_err, _stream(stream)))
 
 
 def paged_kv4_read(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -588,11 +593,11 @@ def paged_kv4_read(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tens
         raise ValueError("key and value must share shape and dtype")
     if slots.dtype != torch.int64 or slots.numel() != T:
         raise ValueError("slots must be int64 [T]")
-    dev = torch.cuda.current_device()
+    p_k, p_v, p_kc, p_vc, p_sl, p_err = _pointers(
+        key, value, key_cache, value_cache, slots, err_word)
     _check("paged_kv4_read", lib.pkv_paged_kv4_read(
-        _at(key, dev), _at(value, dev), dtype_code(key.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        _at(slots, dev), T,
-        key_cache.shape[0], block_size, Hkv, d, float(k_scale), float(v_scale), _at(err_word, dev), _stream(stream)))
+        p_k, p_v, dtype_code(key.dtype), p_kc, p_vc, p_sl, T, key_cache.shape[0], block_size, Hkv, d, float(k_scale),
+        float(v_scale), p_err, _stream(stream)))
 
 
 def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -612,13 +617,12 @@ def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache
     if workspace is None:
         workspace = make_window_workspace(S, Hq, Hkv, d, block_size, max_context_len, window, num_sinks,
                                           partition_size, device=query.device)
-    dev = torch.cuda.current_device()
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
+        out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
     _check("paged_attention_decode_kv4", lib.pkv_paged_attention_decode_kv4(
-        _at(out, dev), _at(query, dev), dtype_code(query.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        _at(block_tables, dev),
-        block_tables.shape[1], _at(context_lens, dev), S, int(max_context_len), Hq, Hkv, d, block_size,
-        key_cache.shape[0], float(scale), float(k_scale), float(v_scale), int(window), int(num_sinks),
-        int(partition_size), _at(workspace, dev), workspace.numel() * workspace.element_size(), _at(err_word, dev),
+        p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, p_bt, block_tables.shape[1], p_cl, S, int(max_context_len), Hq,
+        Hkv, d, block_size, key_cache.shape[0], float(scale), float(k_scale), float(v_scale), int(window),
+        int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
         _stream(stream)))
     return out
 
@@ -657,13 +661,12 @@ def token_attention_decode_scored(out: torch.Tensor, query: torch.Tensor, key_ca
         raise ValueError("scores must be float32 of the token table's shape")
     if workspace is None:
         workspace = make_scored_workspace(S, Hq, Hkv, d, bs, max_tokens, partition_size, device=query.device)
-    dev = torch.cuda.current_device()
+    p_o, p_q, p_kc, p_vc, p_ts, p_nt, p_sc, p_ws, p_err = _pointers(
+        out, query, key_cache, value_cache, token_slots, num_tokens, scores, workspace, err_word)
     _check("token_attention_decode_scored", lib.pkv_token_attention_decode_scored(
-        _at(out, dev), _at(query, dev), dtype_code(query.dtype), _at(key_cache, dev), _at(value_cache, dev),
-        dtype_code(key_cache.dtype), _at(token_slots, dev), token_slots.shape[1], _at(num_tokens, dev),
-        _at(scores, dev), S,
-        int(max_tokens), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(partition_size),
-        _at(workspace, dev), workspace.numel() * workspace.element_size(), _at(err_word, dev), _stream(stream)))
+        p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_ts, token_slots.shape[1], p_nt,
+        p_sc, S, int(max_tokens), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale),
+        int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err, _stream(stream)))
     return out
 
 
@@ -682,11 +685,10 @@ def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: to
     if scores.shape != table or new_slots.shape != table or new_scores.shape != table or \
             (evicted is not None and evicted.shape != table) or num_tokens.shape != (S,) or new_num.shape != (S,):
         raise ValueError("tables and scores are [S, MT], counts [S]")
-    dev = torch.cuda.current_device()
+    p_ts, p_sc, p_nt, p_ns, p_nsc, p_nn, p_ev, p_err = _pointers(
+        token_slots, scores, num_tokens, new_slots, new_scores, new_num, evicted, err_word)
     _check("evict_tokens", lib.pkv_evict_tokens(
-        _at(token_slots, dev), _at(scores, dev), _at(num_tokens, dev), S, MT, int(budget), int(num_first),
-        int(num_recent),
-        _at(new_slots, dev), _at(new_scores, dev), _at(new_num, dev), _at(evicted, dev), _at(err_word, dev),
+        p_ts, p_sc, p_nt, S, MT, int(budget), int(num_first), int(num_recent), p_ns, p_nsc, p_nn, p_ev, p_err,
         _stream(stream)))
 
 

@@ -132,18 +132,19 @@ def test_binding_refuses_wrong_tensors():
         pkv.paged_attention_decode_kv4(torch.empty_like(q), q, kc, kc, t(1, 4), t(2), 10, 0.1, 16)
 
 
-def test_binding_refuses_another_device():
+def test_binding_refuses_another_device(monkeypatch):
     """Tensors of a device that is not the current one, strided ones (no GPU is needed for either)."""
     class Elsewhere:
         device = torch.device("cuda", 1)
         get_device = staticmethod(lambda: 1)
         is_contiguous = staticmethod(lambda: False)
-    assert pkv._at(None, 0) is None
     for dev in (0, 1):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
+        assert pkv._pointers(None, None) == [None, None]
         with pytest.raises(ValueError):
-            pkv._at(Elsewhere(), dev)
+            pkv._pointers(None, Elsewhere())
     for call in (pkv.paged_attention_decode_window, pkv.paged_attention_prefill_window, pkv.paged_kv4_write,
                  pkv.paged_kv4_read, pkv.paged_attention_decode_kv4, pkv.token_attention_decode_scored,
                  pkv.evict_tokens):
         text = inspect.getsource(call)
-        assert "_at(" in text and "_ptr(" not in text
+        assert "_pointers(" in text and "_ptr(" not in text
