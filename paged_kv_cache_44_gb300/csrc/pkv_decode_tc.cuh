@@ -39,12 +39,19 @@
 // Through a token table (TT): "LLM推論の「見えないメモリ問題」を解く … vToken",
 // token-level virtualisation: each live token of a sequence, in logical
 // order, names its own slot (block * bs + offset), so a stage's 32 tokens
-// may come from anywhere in the pool.  The issue side then copies each
-// token's row with 16-byte cp.async requests (eight lanes per 128-byte line)
-// straight into the same swizzled stage layout, and the stage's mbarrier
-// counts one arrival per lane when its copies land; the math is unchanged.
-// (A tensor copy that gathers rows could write only whole 1024-byte swizzle
-// atoms, which four 128-byte rows do not fill.)
+// may come from anywhere in the pool.  Where every 16 tokens of a stage name
+// slots that follow one another (a table that no deletion has touched), they
+// are boxes of 16 rows, as through a block table; otherwise the issue side
+// copies each token's row with 16-byte cp.async requests (eight lanes per
+// 128-byte line) straight into the same swizzled stage layout, and the
+// stage's mbarrier counts one arrival per lane when its copies land; the math
+// is unchanged.  (A tensor copy that gathers rows could write only whole
+// 1024-byte swizzle atoms, which four 128-byte rows do not fill.)  A stage's
+// slots are read one stage ahead.  32 sequences of 256..16,384 tokens in
+// blocks of 16: E4M3 80.4 us with rows copied by lanes alone, 69.8 now; 64
+// bf16 ones of 512..4,096: 37.3 and 33.4.  Half-deleted tables, without runs, read
+// at 6.42 TB/s either way; without the slots read ahead, the test for runs
+// cost them 2%.
 //
 // With a sliding window and sinks (WIN) a unit's tokens are numbered without
 // the blocks no query sees (window_span): the copies, the masks and the
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     const unsigned long long total_warps = (unsigned long long)gridDim.x * kWarps;
     const unsigned long long my_warp = (unsigned long long)blockIdx.x * kWarps + warp;
     unsigned long long static_next = my_warp;
-    constexpr int bs = TT ? 16 : BS;                       // (token tables copy rows, not blocks)
+    constexpr int bs = TT ? 16 : BS;                       // (a token table's boxes are runs of 16 rows)
     constexpr int box_rows = bs < kTok ? bs : kTok;        // tokens one box covers
     constexpr int boxes_per_stage = kTok / box_rows;       // 2 (bs 16, 32-token stages) or 1
     constexpr uint32_t box_bytes = (uint32_t)box_rows * C::kBoxRow;
@@ -309,6 +316,8 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
                 tab_chunk = 0;
                 tab = load_chunk(0);
                 tab_next = load_chunk(1);
+            } else if (iu.t0 + lane < iu.t1) {
+                tab = __ldg(p.token_slots + (size_t)iu.s * p.MT + iu.t0 + lane);
             }
         }
         const int slot = g_issue % C::kStages;
@@ -319,14 +328,38 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             // lane i: the slot of token ts + i; -1 when past the unit or out of the pool
             int tslot = -1;
             if (lane < tn) {
-                tslot = __ldg(p.token_slots + (size_t)iu.s * p.MT + ts + lane);
+                tslot = tab;
                 if (tslot < 0 || (long long)tslot >= (long long)p.NB * p.bs) {
                     report(p.err, PKV_DEVERR_SLOT);
                     tslot = -1;
                 }
             }
+            if (ts + kTok + lane < iu.t1) tab = __ldg(p.token_slots + (size_t)iu.s * p.MT + ts + kTok + lane);
             const uint32_t m = __ballot_sync(0xffffffffu, tslot >= 0);
-            // lanes cover token rows 16 bytes each: CPR lanes per row, 32 / CPR rows per request
+            // every 16 tokens whose slots follow one another (a block no token was dropped from) are boxes of
+            // 16 rows, as through a block table: lane (half, K or V, 128-byte half row) issues its box
+            const int run_of = __shfl_sync(0xffffffffu, tslot, lane & 16);
+            const bool runs = __all_sync(0xffffffffu, lane >= kTok || (tslot >= 0 && tslot == run_of + (lane & 15)));
+            if (runs) {
+                constexpr int nbox = kTok / 16 * 2 * C::kHalves;
+                const int b = lane / (2 * C::kHalves), kv = (lane / C::kHalves) & 1, h = lane % C::kHalves;
+                const int row_box = __shfl_sync(0xffffffffu, tslot, (16 * b) & 31);
+                if (lane == 0) {
+                    masks[slot] = m;
+                    mbar_arrive_expect_tx(bar(slot), nbox * box_bytes);
+                }
+                __syncwarp();
+                if (lane < nbox)
+                    tensor_load_2d_hint((kv ? stage_v(slot) : stage_k(slot)) + h * (kTok * C::kBoxRow) +
+                                            b * 16 * C::kBoxRow,
+                                        kv ? &vmap : &kmap, iu.kvh * D + h * (C::kBoxRow / (FP8 ? 1 : 2)), row_box,
+                                        bar(slot), kv_pol);
+                cp_async_mbar_arrive_noinc(bar(slot));         // (the barrier counts every lane)
+                ++g_issue;
+                ++i_stage;
+                return true;
+            }
+            // else lanes cover token rows 16 bytes each: CPR lanes per row, 32 / CPR rows per request
             constexpr int CPR = C::kRowBytes / 16;
             constexpr int TPI = 32 / CPR;
             const int j = lane % CPR;
@@ -786,14 +819,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // length = Hkv * d elements; a box is (one 128-byte half-row of one K/V
 // head) x (min(bs, tokens per stage) consecutive tokens of one block).
 template <int D, bool FP8>
-bool encode_cache_map(CUtensorMap* map, const void* base, const DecodeParams& p) {
+bool encode_cache_map(CUtensorMap* map, const void* base, const DecodeParams& p, int box_rows) {
     using C = Cfg<D, FP8, 2>;
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const int esize = FP8 ? 1 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)p.Hkv * D, (cuuint64_t)p.NB * p.bs};
     const cuuint64_t strides[1] = {(cuuint64_t)p.Hkv * D * esize};
-    const cuuint32_t box[2] = {(cuuint32_t)(C::kBoxRow / esize), (cuuint32_t)(p.bs < C::kTok ? p.bs : C::kTok)};
+    const cuuint32_t box[2] = {(cuuint32_t)(C::kBoxRow / esize), (cuuint32_t)(box_rows < C::kTok ? box_rows : C::kTok)};
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapSwizzle sw = C::kBoxRow == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const CUresult rc = fn(map, FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
@@ -810,7 +843,8 @@ cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
     cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), C::kSmemBytes);
     if (e != cudaSuccess) return e;
     CUtensorMap kmap, vmap;
-    if (!encode_cache_map<D, FP8>(&kmap, p.kc, p) || !encode_cache_map<D, FP8>(&vmap, p.vc, p))
+    const int box_rows = BS ? BS : 16;
+    if (!encode_cache_map<D, FP8>(&kmap, p.kc, p, box_rows) || !encode_cache_map<D, FP8>(&vmap, p.vc, p, box_rows))
         return cudaErrorInvalidValue;
     const int nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit;
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;

@@ -66,6 +66,50 @@ def test_scored_decode(dtype, Hq, Hkv, d, bs, part):
         P64.assert_within(scores[s, :m], want, (rel * w).sum(0) + 2.0 ** -24 * want + 1e-30, f"scores of {m}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,d,bs", [(12, 2, 128, 16), (7, 1, 64, 32)])
+def test_tables_whose_slots_follow_one_another(dtype, Hq, Hkv, d, bs):
+    """Runs of 16 and more, from the pool's first slot, at odd slots across blocks, up to its last slot, broken by one
+    slot, by an absent one or in falling order: the same bits as the same rows scattered over another pool."""
+    NB, MT = 40, 640
+    P = NB * bs
+    k, v, sc = _pools(NB, bs, Hkv, d, dtype, 11)
+    up = lambda a, m: list(range(a, a + m))  # noqa: E731
+    rows = [up(0, 640), up(P - 640, 640), up(7, 331), up(0, 16) + up(64, 16) + up(1, 48) + up(P - 33, 33),
+            up(0, 40) + [90] + up(41, 200), up(0, 100) + [P + 3] + up(101, 100), up(32, 64)[::-1] + up(0, 64),
+            up(48, 8) + up(48, 8) + up(48, 16), up(5, 16), up(5, 15), []]
+    S = len(rows)
+    slots = torch.full((S, MT), -5, dtype=torch.int32)
+    for s, row in enumerate(rows):
+        slots[s, :len(row)] = torch.tensor(row, dtype=torch.int32)
+    slots = slots.cuda()
+    n = torch.tensor([len(r) for r in rows], dtype=torch.int32, device="cuda")
+    move = torch.randperm(P, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    assert int((move[1:] == move[:-1] + 1).sum()) < 16
+    k2, v2 = (torch.empty_like(c) for c in (k, v))
+    k2.flatten(0, 1)[move], v2.flatten(0, 1)[move] = k.flatten(0, 1), v.flatten(0, 1)
+    live = (slots >= 0) & (slots < P)
+    slots2 = torch.where(live, move[torch.where(live, slots, 0).long()].int(), slots)
+    q = torch.randn(S, Hq, d, device="cuda").bfloat16()
+    kw = dict(scale=d ** -0.5, k_scale=sc, v_scale=sc, partition_size=128)
+    got = []
+    for kc, vc, tab in ((k, v, slots), (k2, v2, slots2)):
+        out, scored, weights = torch.empty_like(q), torch.empty_like(q), torch.zeros(S, MT, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pkv.token_attention_decode(out, q, kc, vc, tab, n, MT, err_word=err, **kw)
+        pkv.token_attention_decode_scored(scored, q, kc, vc, tab, n, weights, MT, **kw)
+        assert int(err) == 3 and torch.equal(out, scored)
+        got.append((out, weights))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    p_eps, small = (2.0 ** -8, 0.0) if dtype == torch.bfloat16 else (2.0 ** -11, MT * 2.0 ** -25 * 6.0)
+    for s, row in enumerate(rows):
+        ok = live[s, :len(row)]
+        idx = torch.where(ok, slots[s, :len(row)], 0).long()
+        o, w, mix, reach = P64.attend(q[s], k.flatten(0, 1)[idx].double() * sc, v.flatten(0, 1)[idx].double() * sc, ok,
+                                      d ** -0.5)
+        P64.assert_within(got[0][0][s], o, P64.out_bound(o, mix, reach, d, p_eps, 2.0 ** -8, small), f"row {s}")
+
+
 def _evict_reference(slots, scores, n, budget, first, recent):
     if n <= budget:
         keep = list(range(n))
