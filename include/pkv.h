@@ -573,7 +573,9 @@ PKV_API size_t pkv_kv4_block_bytes(int bs, int Hkv, int d);
 
 /*
  * paged_kv4_write -- pkv_paged_kv_write into a 4-bit cache: key/value
- * [T, Hkv, d] (F32 or BF16), slot_mapping [T] as there.
+ * [T, Hkv, d] (F32 or BF16), slot_mapping [T] as there; of a slot that one
+ * call names twice the values are unspecified (codes of one token may meet
+ * the scale of the other).
  */
 PKV_API pkv_status pkv_paged_kv4_write(const void* key, const void* value, pkv_dtype in_dtype,
                                        void* key_cache, void* value_cache, const int64_t* slot_mapping, int T,
@@ -621,9 +623,9 @@ PKV_API pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, 
 /*
  * token_attention_decode_scored -- pkv_token_attention_decode (with an
  * explicit partition_size the same output, bit for bit; the library's choice
- * splits a small launch further here) that also adds, to scores[s][t] (fp32 [S, MT],
- * row length MT as the table's) of every live token t, the attention weights
- * the sequence's query gives it, summed over the Hq query heads.  The sum
+ * splits a small launch further here) that also adds, to scores[s][t] (fp32
+ * [S, MT], row length MT as the table's) of every live token t, the attention
+ * weights the sequence's query gives it, summed over the Hq query heads.  The sum
  * runs in a fixed order, so equal calls give equal bits; entries past
  * num_tokens[s] are left as they were, and a slot outside the pool gets
  * weight 0.  `workspace` must hold

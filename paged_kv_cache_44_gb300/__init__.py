@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from functools import partial
 from typing import Optional, Sequence
 
 import numpy as np
@@ -186,6 +187,17 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _own_workspace(stream, make, *sizes, device) -> torch.Tensor:
+    """A call's own workspace, allocated and zeroed on the call's stream: the
+    fill precedes the launch, and the memory is reused behind it."""
+    if stream is None:
+        return make(*sizes, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make(*sizes, device=device)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
@@ -260,7 +272,8 @@ def paged_attention_decode(out: torch.Tensor, query: torch.Tensor, key_cache: to
         raise ValueError("block_tables and context_lens must be int32")
     MB = block_tables.shape[1]
     if workspace is None:          # convenience: a fresh one per call (pass one in to avoid the allocation)
-        workspace = make_workspace(S, Hq, Hkv, d, bs, max_context_len, partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_workspace, S, Hq, Hkv, d, bs, max_context_len, partition_size,
+                                   device=query.device)
     ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check("paged_attention_decode", lib.pkv_paged_attention_decode_ex(
         _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
@@ -322,7 +335,7 @@ def paged_attention_prefill(out: torch.Tensor, query: torch.Tensor, key_cache: t
         raise ValueError("query_start, context_lens and block_tables must be int32")
     if workspace is None:
         n = prefill_workspace_size(S, T, max_query_len, Hq, Hkv, d, bs, max_context_len, partition_size)
-        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=query.device)
+        workspace = _own_workspace(stream, partial(torch.zeros, dtype=torch.uint8), max(n, 256), device=query.device)
     _check("paged_attention_prefill", lib.pkv_paged_attention_prefill_ex(
         _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
         dtype_code(key_cache.dtype), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
@@ -373,7 +386,8 @@ def paged_kv_write_decode(out: torch.Tensor, query: torch.Tensor, key: torch.Ten
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or block_tables.dim() != 2:
         raise ValueError("block_tables and context_lens must be int32")
     if workspace is None:
-        workspace = make_workspace(S, Hq, Hkv, d, bs, max_context_len, partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_workspace, S, Hq, Hkv, d, bs, max_context_len, partition_size,
+                                   device=query.device)
     ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check("paged_kv_write_decode", lib.pkv_paged_kv_write_decode(
         _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key), _ptr(value), dtype_code(key.dtype),
@@ -398,7 +412,8 @@ def token_attention_decode(out: torch.Tensor, query: torch.Tensor, key_cache: to
     if token_slots.dtype != torch.int32 or num_tokens.dtype != torch.int32 or token_slots.dim() != 2:
         raise ValueError("token_slots and num_tokens must be int32")
     if workspace is None:
-        workspace = make_workspace(S, Hq, Hkv, d, bs, max_tokens, partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_workspace, S, Hq, Hkv, d, bs, max_tokens, partition_size,
+                                   device=query.device)
     ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check("token_attention_decode", lib.pkv_token_attention_decode(
         _ptr(out), _ptr(query), dtype_code(query.dtype), _ptr(key_cache), _ptr(value_cache),
@@ -478,8 +493,8 @@ def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_ca
         raise ValueError("shape or dtype mismatch")
     _check_tables(block_tables, context_lens, S)
     if workspace is None:
-        workspace = make_window_workspace(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks, partition_size,
-                                          device=query.device)
+        workspace = _own_workspace(stream, make_window_workspace, S, Hq, Hkv, d, bs, max_context_len, window,
+                                   num_sinks, partition_size, device=query.device)
     p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
         out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
     _check("paged_attention_decode_window", lib.pkv_paged_attention_decode_window(
@@ -523,8 +538,8 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     if query_start.dtype != torch.int32:
         raise ValueError("query_start must be int32")
     if workspace is None:
-        workspace = make_prefill_window_workspace(S, T, max_query_len, Hq, Hkv, d, bs, max_context_len, window,
-                                                  num_sinks, partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_prefill_window_workspace, S, T, max_query_len, Hq, Hkv, d, bs,
+                                   max_context_len, window, num_sinks, partition_size, device=query.device)
     p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_qs, p_ws, p_err = _pointers(
         out, query, key_cache, value_cache, block_tables, context_lens, query_start, workspace, err_word)
     _check("paged_attention_prefill_window", lib.pkv_paged_attention_prefill_window(
@@ -615,8 +630,8 @@ def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache
         raise ValueError("shape or dtype mismatch")
     _check_tables(block_tables, context_lens, S)
     if workspace is None:
-        workspace = make_window_workspace(S, Hq, Hkv, d, block_size, max_context_len, window, num_sinks,
-                                          partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_window_workspace, S, Hq, Hkv, d, block_size, max_context_len, window,
+                                   num_sinks, partition_size, device=query.device)
     p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
         out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
     _check("paged_attention_decode_kv4", lib.pkv_paged_attention_decode_kv4(
@@ -660,7 +675,8 @@ def token_attention_decode_scored(out: torch.Tensor, query: torch.Tensor, key_ca
     if scores.dtype != torch.float32 or scores.shape != token_slots.shape:
         raise ValueError("scores must be float32 of the token table's shape")
     if workspace is None:
-        workspace = make_scored_workspace(S, Hq, Hkv, d, bs, max_tokens, partition_size, device=query.device)
+        workspace = _own_workspace(stream, make_scored_workspace, S, Hq, Hkv, d, bs, max_tokens, partition_size,
+                                   device=query.device)
     p_o, p_q, p_kc, p_vc, p_ts, p_nt, p_sc, p_ws, p_err = _pointers(
         out, query, key_cache, value_cache, token_slots, num_tokens, scores, workspace, err_word)
     _check("token_attention_decode_scored", lib.pkv_token_attention_decode_scored(
