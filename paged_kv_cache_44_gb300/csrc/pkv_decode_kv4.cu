@@ -33,6 +33,13 @@
 //
 // Rounding: p to fp16 and s * p to fp16 (2^-11 each); everything else
 // accumulates in fp32.
+//
+// 32 sequences of 32,768 tokens (64 / 8 heads of 128, 1.34 GB): 226 us, 5.95
+// TB/s, 88% of the measured copy rate; the same tokens take 388 us from an
+// E4M3 cache and 645 from a bf16 one.  A 16-token tile is 268 instructions of
+// those 436 slots.  Warps x tokens per stage (two stages each, what shared
+// memory holds): 11 x 64 226 us, 10 x 64 226, 8 x 64 254, 16 x 32 270, 14 x 32
+// 284.  The whole launch is one kernel and the partitions' merge.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 

@@ -25,7 +25,11 @@ namespace {
 // 32 consecutive bytes, a thread keeps kSets of them (two 16-byte loads
 // each) in flight.  The decode's merge needs the same inputs and nothing of
 // this, so the grid's first blocks do it: one launch instead of two (one
-// sequence of 4,096 tokens: 22.7 -> 20.7 us; long launches the same).
+// sequence of 4,096 tokens: 22.7 -> 20.7 us; long launches the same).  Beside
+// the decode it costs 6 us of 64 bf16 sequences of 512..4,096 tokens (33.4 us
+// without scores, 39.5 with) and 11 us of 32 E4M3 ones of 256..16,384 (69.8 and
+// 81.1), 34 MB of logits: with three blocks on an SM it waits for loads, a
+// third of HBM's rate.  Four with 64 registers each spill (83.6).
 
 constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreRows = 512;          // (set, head) rows whose (M, 1 / L) are staged at a time
@@ -40,7 +44,7 @@ __device__ __forceinline__ void join(float& m, float& l, float M, float L) {
 }
 
 template <int W, int D, typename QF>     // W: heads per row of logits
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, float* __restrict__ scores, int MT,
+__global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(DecodeParams p, float* __restrict__ scores, int MT,
                                                               int merge_blocks, int chunks, int chunk) {
     __shared__ float2 ml[kScoreRows];    // (M, 1 / L); 1 / L = 0 for a row without weight or past the set's heads
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -134,14 +138,16 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(DecodeParams p, fl
 // before it.  A kept token's place is the number kept before it, a dropped
 // one's the number dropped before it: the order is preserved.
 //
-// The floor is 8 bytes in and 8 (kept) or 4 (dropped) out per token, a few
-// us even for 64 sequences of 32,768; what costs is the chain of dependent
-// steps.  So a sequence is spread over a cluster of CTAs that keep their
-// share of the keys in registers (one read of the scores), add up their
-// histograms and counts through distributed shared memory, and each find T
-// for themselves: four cluster barriers in all.  The cluster grows while the
-// grid still fits the GPU in one wave; a share that does not fit the
-// registers (more than 8,192 tokens) is read again in every step instead.
+// The floor is 8 bytes in and 8 (kept) or 4 (dropped) out per token, 3 us for
+// 64 sequences of 16,384..32,768; what costs is the chain of dependent steps,
+// 20.6 us there (four sequences of 300..1,000: 5.6).  So a sequence is spread over a
+// cluster of CTAs that keep their share of the keys in shared memory (one read
+// of the scores), add up their histograms and counts through distributed
+// shared memory, and each find T for themselves: four cluster barriers in all.
+// The cluster grows while the grid still fits the GPU in one wave (clusters of
+// 8 for the 64 sequences: 28.3 us, of 2: 30.5); a share above kEvictHeld
+// tokens is read again in every step instead.  Counting equal bins of a warp
+// before the atomics was slower (the bins' conflicts cost less than the match).
 
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictHeld = 16384;                    // keys per CTA, in shared memory
@@ -398,9 +404,10 @@ int evict_cluster(int S, int MT) {
 template <int D, typename QF>
 static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scores, int MT, cudaStream_t st) {
     const int merge_blocks = merge ? (int)(((long long)p.S * p.Hq + kScoreWarps - 1) / kScoreWarps) : 0;
-    // tokens per block: one per thread in a small launch, else four, so that the rows' (M, L) serve more
+    // tokens per thread: as many as leave every SM a few blocks, so that the rows' (M, L) serve more (64 bf16
+    // sequences of 512..4,096: two 39.5 us, four 41.0; 32 E4M3 ones of 256..16,384: 82.3 and 81.1)
     const long long small = (long long)p.S * ((p.max_ctx + kScoreThreads - 1) / kScoreThreads);
-    const int chunk = small <= 4 * 152 ? kScoreThreads : 4 * kScoreThreads;
+    const int chunk = kScoreThreads * (small <= 4 * 152 ? 1 : small <= 8 * 152 ? 2 : 4);
     const int chunks = (p.max_ctx + chunk - 1) / chunk;
     const long long blocks = merge_blocks + (long long)p.S * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
