@@ -138,16 +138,20 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(DecodeParams p,
 // before it.  A kept token's place is the number kept before it, a dropped
 // one's the number dropped before it: the order is preserved.
 //
-// The floor is 8 bytes in and 8 (kept) or 4 (dropped) out per token, 3 us for
-// 64 sequences of 16,384..32,768; what costs is the chain of dependent steps,
-// 20.6 us there (four sequences of 300..1,000: 5.6).  So a sequence is spread over a
-// cluster of CTAs that keep their share of the keys in shared memory (one read
-// of the scores), add up their histograms and counts through distributed
-// shared memory, and each find T for themselves: four cluster barriers in all.
+// The floor is 8 bytes in and 8 (kept) or 4 (dropped) out per token, 4 us for
+// 64 sequences of 32,768; what costs is the chain of dependent steps, 19.3 us
+// there (7.3 when nothing is dropped; one sequence of 1,000: 5.8, of 131,072:
+// 14.5).  So a sequence is spread over a cluster of CTAs that keep their share
+// of the keys in shared memory (one read of the scores), add up their
+// histograms through distributed shared memory, and each find T for
+// themselves, 2.5 us and a cluster barrier per digit.  The same histograms say
+// how many of the CTAs before keep and how many of their keys equal T, so the
+// places need no further exchange (one more barrier and its counts: 1.5 us).
 // The cluster grows while the grid still fits the GPU in one wave (clusters of
-// 8 for the 64 sequences: 28.3 us, of 2: 30.5); a share above kEvictHeld
-// tokens is read again in every step instead.  Counting equal bins of a warp
-// before the atomics was slower (the bins' conflicts cost less than the match).
+// 8 for the 64 sequences: 28 us, of 2: 30); a share above kEvictHeld tokens is
+// read again in every step instead.  Slower were: counting equal bins of a
+// warp before the atomics, and a list of the first digit's candidates in every
+// CTA so that the other digits need no cluster (20-22 us).
 
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictHeld = 16384;                    // keys per CTA, in shared memory
@@ -184,12 +188,14 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     extern __shared__ __align__(16) uint32_t keys[];   // HELD: of this CTA's tokens, in order
     __shared__ __align__(16) uint32_t hist[3][kBins];
     __shared__ __align__(16) uint32_t coarse[3][kBins / 32];
-    __shared__ uint32_t warp_a[kEvictWarps], warp_b[kEvictWarps], pick[2], counts[2];
+    __shared__ uint2 warp_count[kEvictWarps];
+    __shared__ uint32_t pick[4];
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int s = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     for (int i = tid; i < 3 * kBins / 4; i += kEvictThreads)
         reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
     pdl_wait();
     int n = p.num_tokens[s];
     if (n < 0 || n > p.MT) {
@@ -212,8 +218,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         if (t < lo || t >= hi || all) return kFixed;
         return need > 0 ? score_key(sc) : 1u;
     };
-    constexpr int kBatch = 8;                        // loads in flight per thread
-    if (HELD && need > 0) {
+    // fixed tokens among the first m
+    auto fixed_before = [&](int m) { return m > n ? (all ? n : lo + n - hi) : all ? m : min(m, lo) + max(0, m - hi); };
+    constexpr int kBatch = 8;                       // loads in flight per thread
+    if (HELD && need > 0) {                          // the keys, and the first digit's histogram
         for (int i0 = 0; i0 < turns; i0 += kBatch) {
             float v[kBatch];
 #pragma unroll
@@ -223,7 +231,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
-                if (i0 + j < turns) own[32 * (i0 + j) + lane] = key_of(base + 32 * (i0 + j), v[j]);
+                if (i0 + j < turns) {
+                    const uint32_t k = key_of(base + 32 * (i0 + j), v[j]);
+                    own[32 * (i0 + j) + lane] = k;
+                    if (k != kFixed) atomicAdd(&hist[0][k >> 21], 1u);
+                }
         }
         __syncwarp();
     }
@@ -249,10 +261,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     };
 
     uint32_t T = kFixed - 1u, left = 0;              // keep keys above T, and `left` of key T
+    uint32_t a = fixed_before(base - lane), b = 0;   // before this warp: kept for certain, and of key T
+    uint32_t ties = 0;                               // of key T in this warp
     if (need > 0) {
         T = 0;
         left = need;
-        __syncthreads();
+        uint32_t lower = 0;                          // warp 0: competing keys above T in the ranks before this one
         // one copy of the code for the three digits: a launch runs it once, and fetching it is part of the time
 #pragma unroll 1
         for (int step = 0; step < 3; ++step) {
@@ -260,8 +274,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             const int width = step == 2 ? 10 : 11;
             const uint32_t mask = (1u << width) - 1u;
             uint32_t* bins = hist[step];
-            if (step == 0) {
-                each([&](uint32_t k) { atomicAdd(&bins[k >> 21], 1u); });
+            if (step == 0) {                             // (the fixed tokens do not compete)
+                if constexpr (!HELD)
+                    each([&](uint32_t k) {
+                        if (k != kFixed) atomicAdd(&bins[k >> 21], 1u);
+                    });
             } else {
                 const uint32_t prefix = T >> (shift + width);
                 each([&](uint32_t k) {
@@ -269,10 +286,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
                 });
             }
             __syncthreads();
-            if (step == 0) {                             // the fixed tokens do not compete
-                if (tid == 0) bins[kBins - 1] = 0;
-                __syncthreads();
-            }
             // sums of 32 bins: eight threads of four bins each
             const uint4 v = reinterpret_cast<const uint4*>(bins)[tid];
             uint32_t sum = v.x + v.y + v.z + v.w;
@@ -283,12 +296,14 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             else __syncthreads();
             // one warp reads the cluster's 64 sums, then the 32 bins of the sum that T's digit is in
             if (warp == 0) {
-                uint32_t h0 = 0, h1 = 0;                 // sums 2 lane, 2 lane + 1
+                uint32_t h0 = 0, h1 = 0, l0 = 0, l1 = 0; // sums 2 lane, 2 lane + 1; l: of the ranks before
 #pragma unroll 8
                 for (int r = 0; r < ranks; ++r) {
                     const uint2 u = reinterpret_cast<const uint2*>(cluster.map_shared_rank(&coarse[step][0], r))[lane];
                     h0 += u.x;
                     h1 += u.y;
+                    l0 += r < rank ? u.x : 0u;
+                    l1 += r < rank ? u.y : 0u;
                 }
                 uint32_t above = lanes_above(h0 + h1, lane);
                 const bool here = above < left && above + h0 + h1 >= left;
@@ -297,61 +312,47 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
                 const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
                 const int group = __shfl_sync(0xffffffffu, 2 * lane + (upper ? 1 : 0), src);
                 const uint32_t want = left - __shfl_sync(0xffffffffu, above, src);
-                uint32_t h = 0;                          // bin 32 group + lane
+                uint32_t h = 0, l = 0;                   // bin 32 group + lane
 #pragma unroll 8
-                for (int r = 0; r < ranks; ++r) h += cluster.map_shared_rank(bins, r)[32 * group + lane];
+                for (int r = 0; r < ranks; ++r) {
+                    const uint32_t u = cluster.map_shared_rank(bins, r)[32 * group + lane];
+                    h += u;
+                    l += r < rank ? u : 0u;
+                }
                 above = lanes_above(h, lane);
-                if (above < want && above + h >= want) {
+                const int at = __ffs(__ballot_sync(0xffffffffu, above < want && above + h >= want)) - 1;
+                lower += __reduce_add_sync(0xffffffffu, (2 * lane > group ? l0 : 0u) + (2 * lane + 1 > group ? l1 : 0u) +
+                                                            (lane > at ? l : 0u));
+                if (lane == at) {
                     pick[0] = (uint32_t)(32 * group + lane);
                     pick[1] = want - above;
+                    pick[2] = lower;
+                    pick[3] = l;                         // the last time: of key T in the ranks before this one
                 }
             }
             __syncthreads();
             T |= pick[0] << shift;
             left = pick[1];
         }
-    }
-    uint32_t a = 0, b = 0;                           // this warp's tokens kept for certain, and of key T
-    if (need > 0) {
+        // no CTA leaves while another may still read its histograms
+        if (ranks > 1) cluster.barrier_arrive();
+        uint32_t ca = 0;
         each([&](uint32_t k) {
-            a += k > T;
-            b += k == T;
+            ca += k > T;
+            ties += k == T;
         });
-    } else {
-        for (int i = 0; i < turns; ++i) a += key_of(base + 32 * i, 0.f) == kFixed;
-    }
-    a = __reduce_add_sync(0xffffffffu, a);
-    b = __reduce_add_sync(0xffffffffu, b);
-    const uint32_t ties = b;
-    __syncthreads();
-    if (lane == 0) {
-        warp_a[warp] = a;
-        warp_b[warp] = b;
-    }
-    __syncthreads();
-    uint32_t ta = 0, tb = 0;                         // before this warp, first in the CTA
-    a = b = 0;
-    for (int w = 0; w < kEvictWarps; ++w) {
-        if (w == warp) {
-            a = ta;
-            b = tb;
+        ca = __reduce_add_sync(0xffffffffu, ca);
+        ties = __reduce_add_sync(0xffffffffu, ties);
+        if (lane == 0) warp_count[warp] = make_uint2(ca, ties);
+        __syncthreads();
+        a = pick[2] + fixed_before(rank * kEvictThreads * turns);
+        b = pick[3];
+#pragma unroll
+        for (int w = 0; w < kEvictWarps; ++w) {
+            const uint2 c = warp_count[w];
+            a += w < warp ? c.x : 0u;
+            b += w < warp ? c.y : 0u;
         }
-        ta += warp_a[w];
-        tb += warp_b[w];
-    }
-    if (ranks > 1) {
-        if (tid == 0) {
-            counts[0] = ta;
-            counts[1] = tb;
-        }
-        cluster.sync();
-        for (int r = 0; r < rank; ++r) {
-            const uint32_t* c = cluster.map_shared_rank(&counts[0], r);
-            a += c[0];
-            b += c[1];
-        }
-        // no CTA leaves while another may still read its counts
-        cluster.barrier_arrive();
     }
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = 0; i0 < turns; i0 += kBatch) {
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             b += __popc(bb);
         }
     }
-    if (ranks > 1) cluster.barrier_wait();
+    if (ranks > 1 && need > 0) cluster.barrier_wait();
 }
 
 // CTAs per sequence: a cluster of up to 16, doubled while a share is above
