@@ -559,6 +559,12 @@ pkv_status pkv_paged_attention_decode(void* out, const void* query, pkv_dtype q_
 namespace pkv {
 namespace {
 
+bool prefill_two_tiles(int S, int T, int g) {
+    // two query tiles per unit pay when a (sequence, K/V head) has 256 or
+    // more (query, head) rows on average: prompt chunks, not speculative tokens
+    return (long long)T * g >= 2LL * kPrefillTileRows * S;
+}
+
 // Prefill partition size (0 = no split; -1 = invalid): tiles of 16 (query,
 // head) rows already give parallelism, so split only when there are few.
 // keys: the most a tile's queries reach (max_ctx without a window).
@@ -574,6 +580,42 @@ int resolve_prefill_partition(int S, int max_q_len, int Hq, int Hkv, int d, int 
     int P = 1 << 20;
     while (P > kMinDefaultPartition && tiles * ((keys + P - 1) / P) < kPrefillTargetUnits) P >>= 1;
     return P >= keys ? 0 : P;
+}
+
+// The same under a window, whose keys are few and a little more than a power
+// of two: the number of equal partitions (of whole 128-key stages) with the
+// least estimated time, in tenths of a microsecond.  A unit is a tile of 256
+// rows (128 in the one-tile kernel); its time was fitted to 16 shapes, a
+// stage 1.8 us (1.0), the rest 7.4 (6), and 6.6 (2) more to store a partial
+// result; the merge takes 3 and reads 512 bytes per row and partition.  512
+// queries, 64 / 8 heads, window 1,024: 26.8 us in one partition, 68 in the
+// three that the plain rule takes; 4 x 512 queries, 28 / 4 heads, window
+// 4,096: 136 and 170 (two); 128 queries: 69.8 in one, 25.2 in the nine of 512.
+int resolve_prefill_window_partition(int S, int T, int max_q_len, int Hq, int Hkv, int d, int bs, int max_ctx, int keys,
+                                     int req) {
+    const int P = resolve_prefill_partition(S, max_q_len, Hq, Hkv, d, bs, max_ctx, keys, req);
+    if (P < 0 || req != 0 || T < 1 || S < 1 || max_q_len < 1) return P;
+    const int g = Hq / Hkv;
+    const bool two = prefill_two_tiles(S, T, g);
+    const long long rows = two ? 2 * kPrefillTileRows : kPrefillTileRows;
+    const long long dense = S * (((long long)max_q_len * g + rows - 1) / rows), ragged = (long long)T * g / rows + S;
+    const long long tiles = (dense < ragged ? dense : ragged) * Hkv;
+    long long best = 0;
+    int best_P = 0;
+    for (int np = 1; np <= 16; ++np) {
+        const int part = ((keys + np - 1) / np + 127) / 128 * 128;
+        if (part >= keys && np > 1) break;
+        const int n = np > 1 ? (keys + part - 1) / part : 1;
+        const long long stages = ((n > 1 ? part : keys) + 127) / 128;
+        const long long unit = stages * (two ? 18 : 10) + (two ? 74 : 60) + (n > 1 ? (two ? 66 : 20) : 0);
+        const long long cost =
+            (tiles * n + 151) / 152 * unit + (n > 1 ? 30 + (long long)T * Hq * n * 512 / 650000 : 0);
+        if (np == 1 || cost < best) {
+            best = cost;
+            best_P = n > 1 ? part : 0;
+        }
+    }
+    return best_P;
 }
 
 // Keys of the longest tile under a window: a tile of either kernel (up to
@@ -638,7 +680,10 @@ pkv_status prefill_call(void* out, const void* query, pkv_dtype q_dtype, const v
         return PKV_ERR_INVALID_ARG;
     clamp_window(max_context_len, window, sinks);
     const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, sinks);
-    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys, partition_size);
+    const int P = window > 0 ? resolve_prefill_window_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs,
+                                                                max_context_len, keys, partition_size)
+                             : resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys,
+                                                         partition_size);
     if (P < 0) return PKV_ERR_INVALID_ARG;
     const PrefillPlan pl = plan_prefill(num_query_tokens, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
@@ -665,11 +710,8 @@ pkv_status prefill_call(void* out, const void* query, pkv_dtype q_dtype, const v
     if (kernel == PKV_PREFILL_MMA_SYNC)
         return from_cuda(launch_prefill_tc(p, query_start, num_query_tokens, max_query_len, num_sms_current(),
                                            pl.split, st));
-    // two query tiles per unit pay when a (sequence, K/V head) has 256 or
-    // more (query, head) rows on average: prompt chunks, not speculative tokens
     const bool two_tiles = kernel == PKV_PREFILL_TCGEN05_2TILE ||
-                           (kernel == PKV_PREFILL_AUTO &&
-                            (long long)num_query_tokens * (Hq / Hkv) >= 2LL * kPrefillTileRows * S);
+                           (kernel == PKV_PREFILL_AUTO && prefill_two_tiles(S, num_query_tokens, Hq / Hkv));
     if (two_tiles)
         return from_cuda(launch_prefill_umma2(p, query_start, num_query_tokens, max_query_len, num_sms_current(),
                                               pl.split, st));
@@ -697,7 +739,8 @@ size_t pkv_prefill_window_workspace_size(int S, int num_query_tokens, int max_qu
     if (!decode_shape_ok(S, Hq, Hkv, d, bs, max_context_len)) return 0;
     clamp_window(max_context_len, window, num_sinks);
     const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, num_sinks);
-    const int P = resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys, partition_size);
+    const int P = resolve_prefill_window_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs, max_context_len,
+                                                   keys, partition_size);
     if (P < 0) return 0;
     return plan_prefill(num_query_tokens, Hq, d, keys, P).bytes;
 }

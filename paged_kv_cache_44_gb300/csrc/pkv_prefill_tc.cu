@@ -443,8 +443,11 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(DecodeParams p, cons
     const float L = merge_partitions<D>(p.part_ml + 2 * u0, p.part_acc + u0 * D, np, lane, acc);
     const float f = L > 0.f ? 1.f / L : 0.f;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((size_t)tq * p.Hq + h) * D + lane * E;
+    uint32_t w[E / 2];                         // (a lane's values in one store)
 #pragma unroll
-    for (int k = 0; k < E; ++k) out[k] = __float2bfloat16_rn(acc[k] * f);
+    for (int k = 0; k < E / 2; ++k) w[k] = tc::pack2<false>(acc[2 * k] * f, acc[2 * k + 1] * f);
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
 template <int D>

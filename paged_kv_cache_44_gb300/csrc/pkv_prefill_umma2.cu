@@ -577,17 +577,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) umma::mbar_arrive(bar(kBarMaskEmpty, g & 3));
                 const bool all_present = (mw[0] & mw[1] & mw[2] & mw[3]) == 0xffffffffu;
                 // rows past the tile's last take the same path: their output is never stored
-                bool seen_all = lim >= kTok - 1 && all_present;
                 uint32_t rw[4];                                  // this row's visible tokens, with a window
+                bool seen = lim >= kTok - 1 && all_present;
                 if constexpr (WIN) {
-                    const int v0 = k0 + j * kTok;
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         rw[w] = mw[w] & bits_below(lim + 1 - 32 * w) &
-                                ~bits_between(v0 + 32 * w, p.sinks, pos - p.window + 1);
-                    seen_all = (rw[0] & rw[1] & rw[2] & rw[3]) == 0xffffffffu;
+                                ~bits_between(k0 + j * kTok + 32 * w, p.sinks, pos - p.window + 1);
+                    seen = (rw[0] & rw[1] & rw[2] & rw[3]) == 0xffffffffu;
                 }
-                const bool whole = (seen_all || !rv) && scl > 0.f;
+                bool whole = (seen || !rv) && scl > 0.f;
+                if constexpr (WIN) whole = __all_sync(0xffffffffu, whole);
                 uint32_t sr[4][32];
 #pragma unroll
                 for (int qq = 0; qq < 4; ++qq) umma::tmem_ld32(tmem + lane_base + s_col + 32 * qq, sr[qq]);
@@ -602,12 +602,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int bb = 0; bb < 32; ++bb) mx8[bb & 7] = fmaxf(mx8[bb & 7], __uint_as_float(sr[qq][bb]));
 #pragma unroll
                     for (int k = 0; k < 8; ++k) mx8[k] *= scl;
+                } else if constexpr (WIN) {
+                    // -inf where this row does not see the token; words of 32 tokens that every row of the
+                    // warp sees need no selection
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                        for (int bb = 0; bb < 32; ++bb) sr[w][bb] = __float_as_uint(__uint_as_float(sr[w][bb]) * scl);
+                        if (!__all_sync(0xffffffffu, rw[w] == 0xffffffffu || !rv)) {
+#pragma unroll
+                            for (int bb = 0; bb < 32; ++bb)
+                                if (!((rw[w] >> bb) & 1u)) sr[w][bb] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int bb = 0; bb < 32; ++bb) mx8[bb & 7] = fmaxf(mx8[bb & 7], __uint_as_float(sr[w][bb]));
+                    }
                 } else {
 #pragma unroll
                     for (int qq = 0; qq < 4; ++qq)
 #pragma unroll
                         for (int bb = 0; bb < 32; ++bb) {
-                            const bool live = WIN ? ((rw[qq] >> bb) & 1u) : ((mw[qq] >> bb) & 1u) && (32 * qq + bb) <= lim;
+                            const bool live = ((mw[qq] >> bb) & 1u) && (32 * qq + bb) <= lim;
                             const float xv = live ? __uint_as_float(sr[qq][bb]) * scl : -CUDART_INF_F;
                             sr[qq][bb] = __float_as_uint(xv);
                             mx8[bb & 7] = fmaxf(mx8[bb & 7], xv);
@@ -709,9 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (np == 1) {
                     store_row32(static_cast<__nv_bfloat16*>(p.out) + hrow * D + 32 * c0, ov, f, wide);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_acc + (hrow * p.Pmax + part) * D + 32 * c0);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+                    store_part32(p.part_acc + (hrow * p.Pmax + part) * D + 32 * c0, ov,
+                                 (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
                 }
             }
             if (rv && np > 1) {

@@ -135,4 +135,21 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
     }
 }
 
+// The same 32 values as fp32, unscaled: a line of a partition's partial result.
+__device__ __forceinline__ void store_part32(float* dst, const uint32_t (&o)[32], bool wide) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 8 * k), "r"(o[8 * k]),
+                         "r"(o[8 * k + 1]), "r"(o[8 * k + 2]), "r"(o[8 * k + 3]), "r"(o[8 * k + 4]), "r"(o[8 * k + 5]),
+                         "r"(o[8 * k + 6]), "r"(o[8 * k + 7])
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4*>(dst + 8 * k)[0] = make_uint4(o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3]);
+            reinterpret_cast<uint4*>(dst + 8 * k)[1] =
+                make_uint4(o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]);
+        }
+    }
+}
+
 }  // namespace pkv
