@@ -853,7 +853,7 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     cudaError_t e = use_tc    ? launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kWindow)
                     : use_f32 ? launch_decode_f32(p, q_dtype, num_sms_current(), st)
                               : launch_decode_simt(p, q_dtype, cache_dtype, st);
-    if (e == cudaSuccess && pl.split) e = launch_decode_reduce(p, q_dtype, st);
+    if (e == cudaSuccess && pl.split && !p.local) e = launch_decode_reduce(p, q_dtype, st);
     return from_cuda(e);
 }
 
@@ -932,7 +932,7 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
     set_workspace(p, pl, workspace, workspace_bytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_decode_kv4(p, num_sms_current(), st);
-    if (e == cudaSuccess && pl.split) e = launch_decode_reduce(p, q_dtype, st);
+    if (e == cudaSuccess && pl.split && !p.local) e = launch_decode_reduce(p, q_dtype, st);
     return from_cuda(e);
 }
 

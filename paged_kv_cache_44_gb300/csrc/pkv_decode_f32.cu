@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(FCfg<D>::kWarps * 32, 1)
         }
     }
 
+    if (p.local) merge_set<D, QF>(p, nsets, C::kWarps);
+
     // ---- leave the scheduling counters at zero for the next launch
     if (p.sched != nullptr && lane == 0) {
         unsigned long long* ctr = reinterpret_cast<unsigned long long*>(p.sched);
@@ -420,7 +422,7 @@ bool encode_map(CUtensorMap* map, const void* base, const DecodeParams& p) {
 }
 
 template <int D, typename QF>
-cudaError_t launch_f32_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_f32_one(DecodeParams& p, int num_sms, cudaStream_t st) {
     using C = FCfg<D>;
     auto kern = decode_f32_kernel<D, QF>;
     static SmemOptIn optin;
@@ -433,7 +435,11 @@ cudaError_t launch_f32_one(const DecodeParams& p, int num_sms, cudaStream_t st) 
     const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
     // a small launch puts its units on as many SMs as it has
-    const int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
+    int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
+    if ((p.local = merges_itself(p, per_part, units, C::kWarps, num_sms))) {
+        grid = (int)per_part;
+        p.sched = nullptr;
+    }
     return launch_pdl(kern, dim3(grid < 1 ? 1 : grid), dim3(C::kWarps * 32), C::kSmemBytes, st, p, kmap, vmap, units,
                       region_a, nsets);
 }
@@ -444,7 +450,7 @@ bool decode_f32_supports(pkv_dtype c_dt, int bs, int NB) {
     return c_dt == PKV_F32 && (long long)NB * bs < (1LL << 31);      // TMA row coordinates are 32-bit
 }
 
-cudaError_t launch_decode_f32(const DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st) {
+cudaError_t launch_decode_f32(DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
     if (p.d == 64) return q_dt == PKV_F32 ? launch_f32_one<64, F32>(p, num_sms, st) : launch_f32_one<64, BF16>(p, num_sms, st);
     return q_dt == PKV_F32 ? launch_f32_one<128, F32>(p, num_sms, st) : launch_f32_one<128, BF16>(p, num_sms, st);

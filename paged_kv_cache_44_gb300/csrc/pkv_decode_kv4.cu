@@ -548,6 +548,8 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
         }
     }
 
+    if (p.local) merge_set<D, BF16>(p, nsets, C::kWarps);
+
     // ---- leave the scheduling counters at zero for the next launch
     if (p.sched != nullptr && lane == 0) {
         unsigned long long* ctr = reinterpret_cast<unsigned long long*>(p.sched);
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
 }
 
 template <int D, int BS, bool WIN>
-cudaError_t launch_kv4_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_kv4_one(DecodeParams& p, int num_sms, cudaStream_t st) {
     using C = KCfg<D>;
     auto kern = decode_kv4_kernel<D, BS, WIN>;
     static SmemOptIn optin;
@@ -572,19 +574,23 @@ cudaError_t launch_kv4_one(const DecodeParams& p, int num_sms, cudaStream_t st) 
     const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
     // a small launch puts its units on as many SMs as it has
-    const int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
+    int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
+    if ((p.local = merges_itself(p, per_part, units, C::kWarps, num_sms))) {
+        grid = (int)per_part;
+        p.sched = nullptr;
+    }
     return launch_pdl(kern, dim3(grid < 1 ? 1 : grid), dim3(C::kWarps * 32), C::kSmemBytes, st, p, units, region_a,
                       nsets);
 }
 
 template <int D, bool WIN>
-cudaError_t launch_kv4_bs(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_kv4_bs(DecodeParams& p, int num_sms, cudaStream_t st) {
     return p.bs == 16 ? launch_kv4_one<D, 16, WIN>(p, num_sms, st) : launch_kv4_one<D, 32, WIN>(p, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_decode_kv4(DecodeParams& p, int num_sms, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
     if (p.window > 0) return p.d == 64 ? launch_kv4_bs<64, true>(p, num_sms, st) : launch_kv4_bs<128, true>(p, num_sms, st);
     return p.d == 64 ? launch_kv4_bs<64, false>(p, num_sms, st) : launch_kv4_bs<128, false>(p, num_sms, st);

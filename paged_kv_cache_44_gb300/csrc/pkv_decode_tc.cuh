@@ -789,6 +789,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     // copies of this lane still in flight land before the warp leaves
     if constexpr (TT) asm volatile("cp.async.wait_all;" ::: "memory");
 
+    if constexpr (WIN)
+        if (p.local) merge_set<D, QF>(p, nsets, kWarps);
+
     // ---- leave the scheduling counters at zero for the next launch
     if (p.sched != nullptr && lane == 0) {
         unsigned long long* ctr = reinterpret_cast<unsigned long long*>(p.sched);
@@ -838,7 +841,7 @@ bool encode_cache_map(CUtensorMap* map, const void* base, const DecodeParams& p,
 }
 
 template <int D, bool FP8, typename QF, DecodeMode MODE, int BS>
-cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_one(DecodeParams& p, int num_sms, cudaStream_t st) {
     using C = Cfg<D, FP8, QF::bytes>;
     auto kern = decode_tc_kernel<D, FP8, QF, MODE, BS>;
     static SmemOptIn optin;
@@ -857,12 +860,17 @@ cudaError_t launch_one(const DecodeParams& p, int num_sms, cudaStream_t st) {
     unsigned long long want = spread ? units : (units + C::kWarps - 1) / C::kWarps;
     int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;
+    if constexpr (MODE == DecodeMode::kWindow)
+        if ((p.local = merges_itself(p, per_part, units, C::kWarps, num_sms))) {
+            grid = (int)per_part;
+            p.sched = nullptr;
+        }
     return launch_pdl(kern, dim3(grid), dim3(C::kWarps * 32), C::kSmemBytes, st, p, kmap, vmap, units, region_a,
                       nsets);
 }
 
 template <int D, bool FP8, typename QF, DecodeMode MODE>
-cudaError_t launch_bs(const DecodeParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_bs(DecodeParams& p, int num_sms, cudaStream_t st) {
     if constexpr (MODE == DecodeMode::kTokenTable || MODE == DecodeMode::kScored)
         return launch_one<D, FP8, QF, MODE, 0>(p, num_sms, st);
     else
@@ -871,7 +879,7 @@ cudaError_t launch_bs(const DecodeParams& p, int num_sms, cudaStream_t st) {
 }
 
 template <DecodeMode MODE>
-cudaError_t launch_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st) {
+cudaError_t launch_tc(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st) {
     if (c_dt == PKV_BF16)
         return p.d == 64 ? launch_bs<64, false, BF16, MODE>(p, num_sms, st) : launch_bs<128, false, BF16, MODE>(p, num_sms, st);
     if (q_dt == PKV_BF16)

@@ -3,7 +3,7 @@
 
 namespace pkv {
 
-cudaError_t launch_decode_tc_token(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st) {
+cudaError_t launch_decode_tc_token(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st) {
     return launch_tc<DecodeMode::kTokenTable>(p, q_dt, c_dt, num_sms, st);
 }
 

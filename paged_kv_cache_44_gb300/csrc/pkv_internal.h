@@ -128,6 +128,7 @@ struct DecodeParams {
     float* part_ml;       // [S][Hq][Pmax][2]: running max (log2 units) and sum
     float* part_acc;      // [S][Hq][Pmax][d]: un-normalised weighted sums of V
     unsigned* sched;      // scheduling counters in the workspace header (or null)
+    int local;            // the launch merges its own partitions (merges_itself); else a merge kernel follows
     int32_t* err;
     int S, MB, Hq, Hkv, g, d, bs, NB;
     int MT;               // row length of token_slots
@@ -196,16 +197,17 @@ enum class DecodeMode {
 };
 
 cudaError_t launch_decode_simt(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, cudaStream_t st);
-cudaError_t launch_decode_tc(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms,
+cudaError_t launch_decode_tc(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms,
                              cudaStream_t st, DecodeMode mode = DecodeMode::kBlockTable);
 // the windowed decode over an fp32 cache
 bool decode_f32_supports(pkv_dtype c_dt, int bs, int NB);
-cudaError_t launch_decode_f32(const DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st);
-cudaError_t launch_decode_kv4(const DecodeParams& p, int num_sms, cudaStream_t st);
+// p.local: set where the launch merges its partitions itself, so that no merge kernel follows
+cudaError_t launch_decode_f32(DecodeParams& p, pkv_dtype q_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_kv4(DecodeParams& p, int num_sms, cudaStream_t st);
 // its modes, in translation units of their own
-cudaError_t launch_decode_tc_token(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
-cudaError_t launch_decode_tc_window(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
-cudaError_t launch_decode_tc_scored(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_token(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_window(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_scored(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
 // after a scored decode: scores[s][t] += the attention weights (rows of MT scores) and, when split, the merge
 cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st);

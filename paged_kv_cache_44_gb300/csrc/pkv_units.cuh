@@ -5,6 +5,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "pkv_merge.cuh"
 
 namespace pkv {
 
@@ -79,6 +80,28 @@ __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long lon
     }
     partition_range(n, p.P, p.Q, p.hold, x.part, x.t0, x.t1);
     return true;
+}
+
+// A launch of at most one CTA per (sequence, head set) and one warp per
+// partition: warp w of CTA b then takes, as its first and only unit, unit
+// w * CTAs + b, which is partition w of set b (the ids above), so a set's
+// partial results are all its CTA's, and the CTA merges them without a second
+// launch.  One 4-bit sequence of 301 tokens: 8.9 us with the merge kernel, 7.2
+// without (and 2 us less of the host's time).
+inline bool merges_itself(const DecodeParams& p, unsigned long long per_part, unsigned long long units, int warps,
+                          int num_sms) {
+    return p.Pmax > 1 && per_part <= (unsigned long long)num_sms && units <= per_part * warps;
+}
+
+// The merge of such a CTA's set, by all its warps.
+template <int D, typename QF>
+__device__ __forceinline__ void merge_set(const DecodeParams& p, int nsets, int warps) {
+    __threadfence();
+    __syncthreads();
+    const int set = blockIdx.x % nsets, kvh = blockIdx.x / nsets % p.Hkv, s = blockIdx.x / (nsets * p.Hkv);
+    const int nh = min(kHeadsPerUnit, p.g - set * kHeadsPerUnit);
+    for (int h = threadIdx.x / 32; h < nh; h += warps)
+        merge_row<D, QF>(p, (long long)s * p.Hq + kvh * p.g + set * kHeadsPerUnit + h, threadIdx.x & 31);
 }
 
 }  // namespace pkv
