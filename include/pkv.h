@@ -666,6 +666,27 @@ PKV_API pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* sco
                                     int32_t* err_word, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The calls of the three sections above with their arguments in one array,
+ * for callers whose foreign-function interface pays per argument (the Python
+ * binding's converts 27 arguments in 2.4 us and one in 0.3).  words[i] is the
+ * call's argument i as 64 bits: pointers and sizes as they are, integers and
+ * enumerations sign-extended, floats as doubles.  Returns what the call
+ * returns, PKV_ERR_INVALID_ARG for an unknown call, no array, or an integer
+ * that does not fit its parameter.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    PKV_CALL_DECODE_WINDOW = 0,    /* pkv_paged_attention_decode_window */
+    PKV_CALL_PREFILL_WINDOW = 1,   /* pkv_paged_attention_prefill_window */
+    PKV_CALL_KV4_WRITE = 2,        /* pkv_paged_kv4_write */
+    PKV_CALL_KV4_READ = 3,         /* pkv_paged_kv4_read */
+    PKV_CALL_DECODE_KV4 = 4,       /* pkv_paged_attention_decode_kv4 */
+    PKV_CALL_DECODE_SCORED = 5,    /* pkv_token_attention_decode_scored */
+    PKV_CALL_EVICT = 6             /* pkv_evict_tokens */
+} pkv_call;
+PKV_API pkv_status pkv_invoke(int call, const void* words);
+
+
+/* ------------------------------------------------------------------------
  * Host block manager: the bookkeeping that produces the block tables, slot
  * mappings and copy-on-write pairs the device calls consume.  Host memory
  * only; nothing here touches the GPU.

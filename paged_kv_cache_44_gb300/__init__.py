@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from functools import partial
 from typing import Optional, Sequence
 
@@ -46,7 +47,8 @@ EXPORTED = ("pkv_paged_kv_write", "pkv_decode_workspace_size", "pkv_decode_parti
             "pkv_decode_window_workspace_size", "pkv_paged_attention_decode_window",
             "pkv_prefill_window_workspace_size", "pkv_paged_attention_prefill_window", "pkv_kv4_block_bytes",
             "pkv_paged_kv4_write", "pkv_paged_kv4_read", "pkv_paged_attention_decode_kv4",
-            "pkv_token_attention_scored_workspace_size", "pkv_token_attention_decode_scored", "pkv_evict_tokens")
+            "pkv_token_attention_scored_workspace_size", "pkv_token_attention_decode_scored", "pkv_evict_tokens",
+            "pkv_invoke")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -149,6 +151,8 @@ def _load() -> ctypes.CDLL:
     lib.pkv_token_attention_decode_scored.restype = i32
     lib.pkv_evict_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     lib.pkv_evict_tokens.restype = i32
+    lib.pkv_invoke.argtypes = [i32, ctypes.c_char_p]
+    lib.pkv_invoke.restype = i32
     lib.pkv_status_string.argtypes = [i32]
     lib.pkv_status_string.restype = ctypes.c_char_p
     lib.pkv_version.argtypes = []
@@ -206,6 +210,18 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if not t.is_contiguous():
         raise ValueError("pkv calls take contiguous tensors")
     return t.data_ptr()
+
+
+def _packed(number: int, symbol: str):
+    """A call of the library through pkv_invoke: one conversion of all arguments instead of one each."""
+    kinds = {ctypes.c_void_p: "Q", ctypes.c_int: "q", ctypes.c_float: "d", ctypes.c_size_t: "Q"}
+    pack, invoke = struct.Struct("=" + "".join(kinds[t] for t in getattr(lib, symbol).argtypes)).pack, lib.pkv_invoke
+
+    def call(*args) -> None:
+        st = invoke(number, pack(*args))
+        if st != 0:
+            raise PkvError(symbol[4:], st)
+    return call
 
 
 def _check(call: str, st: int) -> None:
@@ -446,20 +462,31 @@ def repack_tokens(key_caches: Sequence[torch.Tensor], value_caches: Sequence[tor
                                                   token_bytes, _ptr(err_word), _stream(stream)))
 
 
-def _pointers(*tensors: Optional[torch.Tensor]) -> list:
-    """The tensors' addresses (None stays).  The launch goes to the current
-    device: tensors of another one are refused, and so are strided ones."""
+def _pointers(stream, *tensors: Optional[torch.Tensor]) -> list:
+    """The tensors' addresses (0 for None), then the stream's handle.  The
+    launch goes to the current device: tensors of another one are refused,
+    and so are strided ones."""
     dev, out = torch.cuda.current_device(), []
     for t in tensors:
         if t is None:
-            out.append(None)
+            out.append(0)
         elif t.get_device() != dev:
             raise ValueError(f"pkv calls take tensors of the current CUDA device ({dev}), got one on {t.device}")
         elif not t.is_contiguous():
             raise ValueError("pkv calls take contiguous tensors")
         else:
             out.append(t.data_ptr())
+    out.append(_raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream))
     return out
+
+
+_decode_window = _packed(0, "pkv_paged_attention_decode_window")
+_prefill_window = _packed(1, "pkv_paged_attention_prefill_window")
+_kv4_write = _packed(2, "pkv_paged_kv4_write")
+_kv4_read = _packed(3, "pkv_paged_kv4_read")
+_decode_kv4 = _packed(4, "pkv_paged_attention_decode_kv4")
+_decode_scored = _packed(5, "pkv_token_attention_decode_scored")
+_evict = _packed(6, "pkv_evict_tokens")
 
 
 # ---- sliding window with sinks
@@ -495,13 +522,13 @@ def paged_attention_decode_window(out: torch.Tensor, query: torch.Tensor, key_ca
     if workspace is None:
         workspace = _own_workspace(stream, make_window_workspace, S, Hq, Hkv, d, bs, max_context_len, window,
                                    num_sinks, partition_size, device=query.device)
-    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
-        out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
-    _check("paged_attention_decode_window", lib.pkv_paged_attention_decode_window(
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err, p_st = _pointers(
+        stream, out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
+    _decode_window(
         p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_bt, block_tables.shape[1], p_cl,
         S, int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale), int(window),
         int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
-        _stream(stream), KERNELS[kernel]))
+        p_st, KERNELS[kernel])
     return out
 
 
@@ -540,13 +567,13 @@ def paged_attention_prefill_window(out: torch.Tensor, query: torch.Tensor, key_c
     if workspace is None:
         workspace = _own_workspace(stream, make_prefill_window_workspace, S, T, max_query_len, Hq, Hkv, d, bs,
                                    max_context_len, window, num_sinks, partition_size, device=query.device)
-    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_qs, p_ws, p_err = _pointers(
-        out, query, key_cache, value_cache, block_tables, context_lens, query_start, workspace, err_word)
-    _check("paged_attention_prefill_window", lib.pkv_paged_attention_prefill_window(
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_qs, p_ws, p_err, p_st = _pointers(
+        stream, out, query, key_cache, value_cache, block_tables, context_lens, query_start, workspace, err_word)
+    _prefill_window(
         p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_bt, block_tables.shape[1], p_cl,
         p_qs, S, T, int(max_query_len), int(max_context_len), Hq, Hkv, d, bs, NB, float(scale), int(window),
         int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
-        _stream(stream)))
+        p_st)
     return out
 
 
@@ -590,11 +617,11 @@ def paged_kv4_write(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Ten
         raise ValueError("key and value must share shape and dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [T]")
-    p_k, p_v, p_kc, p_vc, p_sm, p_err = _pointers(
-        key, value, key_cache, value_cache, slot_mapping, err_word)
-    _check("paged_kv4_write", lib.pkv_paged_kv4_write(
+    p_k, p_v, p_kc, p_vc, p_sm, p_err, p_st = _pointers(
+        stream, key, value, key_cache, value_cache, slot_mapping, err_word)
+    _kv4_write(
         p_k, p_v, dtype_code(key.dtype), p_kc, p_vc, p_sm, T, key_cache.shape[0], block_size, Hkv, d, float(k_scale),
-        float(v_scale), p_err, _stream(stream)))
+        float(v_scale), p_err, p_st)
 
 
 def paged_kv4_read(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -608,11 +635,11 @@ def paged_kv4_read(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tens
         raise ValueError("key and value must share shape and dtype")
     if slots.dtype != torch.int64 or slots.numel() != T:
         raise ValueError("slots must be int64 [T]")
-    p_k, p_v, p_kc, p_vc, p_sl, p_err = _pointers(
-        key, value, key_cache, value_cache, slots, err_word)
-    _check("paged_kv4_read", lib.pkv_paged_kv4_read(
+    p_k, p_v, p_kc, p_vc, p_sl, p_err, p_st = _pointers(
+        stream, key, value, key_cache, value_cache, slots, err_word)
+    _kv4_read(
         p_k, p_v, dtype_code(key.dtype), p_kc, p_vc, p_sl, T, key_cache.shape[0], block_size, Hkv, d, float(k_scale),
-        float(v_scale), p_err, _stream(stream)))
+        float(v_scale), p_err, p_st)
 
 
 def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -632,13 +659,13 @@ def paged_attention_decode_kv4(out: torch.Tensor, query: torch.Tensor, key_cache
     if workspace is None:
         workspace = _own_workspace(stream, make_window_workspace, S, Hq, Hkv, d, block_size, max_context_len, window,
                                    num_sinks, partition_size, device=query.device)
-    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err = _pointers(
-        out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
-    _check("paged_attention_decode_kv4", lib.pkv_paged_attention_decode_kv4(
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_ws, p_err, p_st = _pointers(
+        stream, out, query, key_cache, value_cache, block_tables, context_lens, workspace, err_word)
+    _decode_kv4(
         p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, p_bt, block_tables.shape[1], p_cl, S, int(max_context_len), Hq,
         Hkv, d, block_size, key_cache.shape[0], float(scale), float(k_scale), float(v_scale), int(window),
         int(num_sinks), int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err,
-        _stream(stream)))
+        p_st)
     return out
 
 
@@ -677,12 +704,12 @@ def token_attention_decode_scored(out: torch.Tensor, query: torch.Tensor, key_ca
     if workspace is None:
         workspace = _own_workspace(stream, make_scored_workspace, S, Hq, Hkv, d, bs, max_tokens, partition_size,
                                    device=query.device)
-    p_o, p_q, p_kc, p_vc, p_ts, p_nt, p_sc, p_ws, p_err = _pointers(
-        out, query, key_cache, value_cache, token_slots, num_tokens, scores, workspace, err_word)
-    _check("token_attention_decode_scored", lib.pkv_token_attention_decode_scored(
+    p_o, p_q, p_kc, p_vc, p_ts, p_nt, p_sc, p_ws, p_err, p_st = _pointers(
+        stream, out, query, key_cache, value_cache, token_slots, num_tokens, scores, workspace, err_word)
+    _decode_scored(
         p_o, p_q, dtype_code(query.dtype), p_kc, p_vc, dtype_code(key_cache.dtype), p_ts, token_slots.shape[1], p_nt,
         p_sc, S, int(max_tokens), Hq, Hkv, d, bs, NB, float(scale), float(k_scale), float(v_scale),
-        int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err, _stream(stream)))
+        int(partition_size), p_ws, workspace.numel() * workspace.element_size(), p_err, p_st)
     return out
 
 
@@ -701,11 +728,11 @@ def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: to
     if scores.shape != table or new_slots.shape != table or new_scores.shape != table or \
             (evicted is not None and evicted.shape != table) or num_tokens.shape != (S,) or new_num.shape != (S,):
         raise ValueError("tables and scores are [S, MT], counts [S]")
-    p_ts, p_sc, p_nt, p_ns, p_nsc, p_nn, p_ev, p_err = _pointers(
-        token_slots, scores, num_tokens, new_slots, new_scores, new_num, evicted, err_word)
-    _check("evict_tokens", lib.pkv_evict_tokens(
+    p_ts, p_sc, p_nt, p_ns, p_nsc, p_nn, p_ev, p_err, p_st = _pointers(
+        stream, token_slots, scores, num_tokens, new_slots, new_scores, new_num, evicted, err_word)
+    _evict(
         p_ts, p_sc, p_nt, S, MT, int(budget), int(num_first), int(num_recent), p_ns, p_nsc, p_nn, p_ev, p_err,
-        _stream(stream)))
+        p_st)
 
 
 def vtoken_plan(token_slots: np.ndarray, num_tokens: np.ndarray, block_size: int, num_blocks: int):

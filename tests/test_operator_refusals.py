@@ -1,6 +1,8 @@
 """Arguments the windowed, 4-bit and eviction calls refuse, on the host: no
 GPU is needed, and a call that got past its checks would answer 4 here."""
+import ctypes
 import inspect
+import struct
 
 import pytest
 import torch
@@ -140,11 +142,43 @@ def test_binding_refuses_another_device(monkeypatch):
         is_contiguous = staticmethod(lambda: False)
     for dev in (0, 1):
         monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
-        assert pkv._pointers(None, None) == [None, None]
+        assert pkv._pointers(3, None, None) == [0, 0, 3]
         with pytest.raises(ValueError):
-            pkv._pointers(None, Elsewhere())
+            pkv._pointers(None, None, Elsewhere())
     for call in (pkv.paged_attention_decode_window, pkv.paged_attention_prefill_window, pkv.paged_kv4_write,
                  pkv.paged_kv4_read, pkv.paged_attention_decode_kv4, pkv.token_attention_decode_scored,
                  pkv.evict_tokens):
         text = inspect.getsource(call)
         assert "_pointers(" in text and "_ptr(" not in text
+
+
+def test_arguments_in_one_array():
+    """pkv_invoke gives each call its arguments: refusals are the call's own, wherever the bad argument stands."""
+    symbols = ["pkv_paged_attention_decode_window", "pkv_paged_attention_prefill_window", "pkv_paged_kv4_write",
+               "pkv_paged_kv4_read", "pkv_paged_attention_decode_kv4", "pkv_token_attention_decode_scored",
+               "pkv_evict_tokens"]
+    good = [  # no sequences or tokens: accepted without a launch
+        (0, 0, 1, 0, 0, 1, 0, 4, 0, 0, 64, 8, 2, 128, 16, 9, 0.1, 1.0, 1.0, 5, 4, 0, 0, 0, 0, 0, 0),
+        (0, 0, 1, 0, 0, 1, 0, 4, 0, 0, 0, 0, 0, 64, 8, 2, 128, 16, 9, 0.1, 5, 4, 0, 0, 0, 0, 0),
+        (0, 0, 1, 0, 0, 0, 0, 9, 16, 2, 128, 1.0, 1.0, 0, 0), (0, 0, 1, 0, 0, 0, 0, 9, 16, 2, 128, 1.0, 1.0, 0, 0),
+        (0, 0, 1, 0, 0, 0, 4, 0, 0, 64, 8, 2, 128, 16, 9, 0.1, 1.0, 1.0, 5, 4, 0, 0, 0, 0, 0),
+        (0, 0, 1, 0, 0, 1, 0, 64, 0, 0, 0, 64, 8, 2, 128, 16, 9, 0.1, 1.0, 1.0, 0, 0, 0, 0, 0),
+        (0, 0, 0, 0, 7, 4, 1, 1, 0, 0, 0, 0, 0, 0)]
+    for number, (symbol, args) in enumerate(zip(symbols, good)):
+        f = getattr(pkv.lib, symbol)
+        assert len(f.argtypes) == len(args)
+        kinds = {ctypes.c_void_p: "Q", ctypes.c_int: "q", ctypes.c_float: "d", ctypes.c_size_t: "Q"}
+        pack = struct.Struct("=" + "".join(kinds[t] for t in f.argtypes)).pack
+        assert f(*args) == 0 and pkv.lib.pkv_invoke(number, pack(*args)) == 0
+        refused = 0
+        for i, t in enumerate(f.argtypes):
+            for bad in {ctypes.c_int: (-7, 12345), ctypes.c_float: (float("nan"),)}.get(t, ()):
+                other = args[:i] + (bad,) + args[i + 1:]
+                want = f(*other)
+                assert pkv.lib.pkv_invoke(number, pack(*other)) == want, (symbol, i, bad)
+                refused += want != 0
+            if t == ctypes.c_int:
+                assert pkv.lib.pkv_invoke(number, pack(*args[:i], 1 << 32, *args[i + 1:])) == 1, (symbol, i)
+        assert refused > 4
+    assert pkv.lib.pkv_invoke(7, bytes(400)) == 1 and pkv.lib.pkv_invoke(-1, bytes(400)) == 1
+    assert pkv.lib.pkv_invoke(0, None) == 1
