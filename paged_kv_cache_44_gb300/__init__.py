@@ -13,6 +13,17 @@ section 4):
 * :func:`paged_attention_decode` -- one query token per sequence against the
   paged K/V pool, through block tables;
 * :func:`copy_blocks` -- copy-on-write duplication of shared blocks.
+
+Around them: query chunks (:func:`paged_attention_prefill`), token tables and
+repacking (:func:`token_attention_decode`, :func:`repack_tokens`), the host
+block manager (:class:`BlockPool`), and what bounds a cache's size:
+
+* :func:`paged_attention_decode_window`, :func:`paged_attention_prefill_window`
+  -- a sliding window with sinks; blocks no query sees are not read;
+* :func:`paged_kv4_write`, :func:`paged_kv4_read`,
+  :func:`paged_attention_decode_kv4` -- a cache in 4 bits;
+* :func:`token_attention_decode_scored`, :func:`evict_tokens` -- attention
+  weights accumulated per token, and the tokens with the least dropped.
 """
 from __future__ import annotations
 
