@@ -71,16 +71,25 @@ int resolve_partition(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int re
 // heads 14.6 / 17.0 / 20.6 / 55.5.  Beyond 48 partitions a row's merge costs
 // what that saves (one 4-bit sequence of 32,768 tokens: 69 us in 64, 45 in
 // 128, 28.7 in 256; a window of 4,100 bf16 tokens: 18.5 and 18.7).
-constexpr int kMinSplit = 64, kMaxSmallSplits = 48;
-int resolve_split(int S, int Hq, int Hkv, int d, int bs, int keys, int req) {
+// The windowed fp32 decode, 1.8 us per 16-token stage, goes down to 32 while
+// every unit has a worker (152 SMs x 6): one sequence of 400 tokens, 4 K/V
+// heads, in 32 / 64 / 128: 11.8 / 15.4 / 22.4 us; eight of 1,000 (1,024
+// units) 20.8 / 17.2 / 23.7.
+constexpr int kMaxSmallSplits = 48;
+struct SplitRule {
+    int smallest;
+    long long units;
+};
+constexpr SplitRule kSplit{64, kSmallLaunchUnits}, kSplitF32{32, 152LL * 6};
+int resolve_split(int S, int Hq, int Hkv, int d, int bs, int keys, int req, SplitRule rule = kSplit) {
     const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, req);
-    if (P < 0 || req != 0 || keys <= kMinSplit) return P;
+    if (P < 0 || req != 0 || keys <= rule.smallest) return P;
     const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);
     int p = P > 0 ? P : keys;
-    while (p > kMinSplit) {
-        const int half = max(kMinSplit, (p / 2 + 31) / 32 * 32);
+    while (p > rule.smallest) {
+        const int half = max(rule.smallest, (p / 2 + 31) / 32 * 32);
         const int n = (keys + half - 1) / half;
-        if (half >= p || sets * n > kSmallLaunchUnits || n > kMaxSmallSplits) break;
+        if (half >= p || sets * n > rule.units || n > kMaxSmallSplits) break;
         p = half;
     }
     return p < keys ? p : 0;
@@ -814,7 +823,10 @@ size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, i
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
     const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
-    return P < 0 ? 0 : make_plan(S, Hq, d, keys, P).bytes;
+    if (P < 0) return 0;
+    // whatever the cache's dtype
+    const int P_f32 = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size, kSplitF32);
+    return max(make_plan(S, Hq, d, keys, P).bytes, make_plan(S, Hq, d, keys, P_f32).bytes);
 }
 
 pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
@@ -831,8 +843,9 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     if (chk != PKV_OK || S == 0) return chk;
     clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
     const bool use_tc = kernel != PKV_DECODE_CUDA_CORES && decode_tc_supports(q_dtype, cache_dtype, d, bs, NB);
+    const bool use_f32 = kernel == PKV_DECODE_AUTO && decode_f32_supports(cache_dtype, bs, NB);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size, use_f32 ? kSplitF32 : kSplit);
     const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
@@ -849,7 +862,6 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     p.out_scale = e4m3 ? v_scale : 1.f;
     set_workspace(p, pl, workspace, workspace_bytes);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool use_f32 = kernel == PKV_DECODE_AUTO && decode_f32_supports(cache_dtype, bs, NB);
     cudaError_t e = use_tc    ? launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kWindow)
                     : use_f32 ? launch_decode_f32(p, q_dtype, num_sms_current(), st)
                               : launch_decode_simt(p, q_dtype, cache_dtype, st);

@@ -861,7 +861,8 @@ cudaError_t launch_one(DecodeParams& p, int num_sms, cudaStream_t st) {
     int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;
     if constexpr (MODE == DecodeMode::kWindow)
-        if ((p.local = merges_itself(p, per_part, units, C::kWarps, num_sms))) {
+        // (an E4M3 worker's pace is its arithmetic: one per scheduler)
+        if ((p.local = merges_itself(p, per_part, units, FP8 ? 4 : C::kWarps, num_sms))) {
             grid = (int)per_part;
             p.sched = nullptr;
         }

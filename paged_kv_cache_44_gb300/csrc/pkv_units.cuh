@@ -86,8 +86,11 @@ __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long lon
 // partition: warp w of CTA b then takes, as its first and only unit, unit
 // w * CTAs + b, which is partition w of set b (the ids above), so a set's
 // partial results are all its CTA's, and the CTA merges them without a second
-// launch.  One 4-bit sequence of 301 tokens: 8.9 us with the merge kernel, 7.2
-// without (and 2 us less of the host's time).
+// launch.  One 4-bit sequence of 301 tokens: 8.9 us with the merge kernel, 7.9
+// without (and 2 us less of the host's time).  `warps` is what a set may take
+// on one SM: a bf16, fp32 or 4-bit worker waits mostly for its own copies and
+// sums, an E4M3 one is busy converting, and from five on the spread launch
+// with its merge kernel is faster (640 tokens in 10 partitions: 9.3 and 12.8 us).
 inline bool merges_itself(const DecodeParams& p, unsigned long long per_part, unsigned long long units, int warps,
                           int num_sms) {
     return p.Pmax > 1 && per_part <= (unsigned long long)num_sms && units <= per_part * warps;
