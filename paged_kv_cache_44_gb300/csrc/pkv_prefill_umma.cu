@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(ctlp + kTmemSlot);
+    // the previous kernel of the stream (a write of the step's tokens, say) is complete from here on
+    pdl_wait();
 
     // bounded wait; false once the limit passes or another role gave up
     auto wait = [&](uint32_t b, uint32_t parity, bool abortable) -> bool {
@@ -696,8 +698,8 @@ cudaError_t launch_umma_d(const DecodeParams& p, const int32_t* query_start, int
     const unsigned long long units = (unsigned long long)p.Pmax * p.S * p.Hkv * rt_max;
     int grid = (int)(units < (unsigned long long)num_sms ? units : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;
-    kern<<<grid, kThreads, C::kSmemBytes, st>>>(p, query_start, T, max_q_len, kmap, vmap, units, rt_max);
-    e = cudaGetLastError();
+    e = launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, st, p, query_start, T, max_q_len, kmap, vmap, units,
+                   rt_max);
     if (e != cudaSuccess || !merge) return e;
     return launch_prefill_merge(p, query_start, T, kURows, max_q_len, st);
 }
