@@ -474,9 +474,11 @@ def repack_tokens(key_caches: Sequence[torch.Tensor], value_caches: Sequence[tor
 
 
 def _pointers(stream, *tensors: Optional[torch.Tensor]) -> list:
-    """The tensors' addresses (0 for None), then the stream's handle.  The
-    launch goes to the current device: tensors of another one are refused,
-    and so are strided ones."""
+    """The tensors' addresses (0 for None), then the stream's handle; the last
+    tensor is the error word.  The launch goes to the current device: tensors
+    of another one are refused, and so are strided ones."""
+    if tensors[-1] is not None and tensors[-1].dtype != torch.int32:
+        raise ValueError("the error word must be int32")
     dev, out = torch.cuda.current_device(), []
     for t in tensors:
         if t is None:

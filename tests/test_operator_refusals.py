@@ -143,8 +143,10 @@ def test_binding_refuses_another_device(monkeypatch):
     for dev in (0, 1):
         monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
         assert pkv._pointers(3, None, None) == [0, 0, 3]
-        with pytest.raises(ValueError):
-            pkv._pointers(None, None, Elsewhere())
+        with pytest.raises(ValueError, match="contiguous" if dev else "device"):
+            pkv._pointers(None, Elsewhere(), None)
+        with pytest.raises(ValueError, match="int32"):
+            pkv._pointers(None, None, torch.zeros(4, dtype=torch.uint8))
     for call in (pkv.paged_attention_decode_window, pkv.paged_attention_prefill_window, pkv.paged_kv4_write,
                  pkv.paged_kv4_read, pkv.paged_attention_decode_kv4, pkv.token_attention_decode_scored,
                  pkv.evict_tokens):
