@@ -141,7 +141,7 @@ def test_binding_refuses_another_device(monkeypatch):
         get_device = staticmethod(lambda: 1)
         is_contiguous = staticmethod(lambda: False)
     for dev in (0, 1):
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: dev)
+        monkeypatch.setattr(pkv, "_current_device", lambda: dev)
         assert pkv._pointers(3, None, None) == [0, 0, 3]
         with pytest.raises(ValueError, match="contiguous" if dev else "device"):
             pkv._pointers(None, Elsewhere(), None)
