@@ -22,18 +22,19 @@ namespace {
 // its partitions.  One thread owns a token and adds its heads in order, so
 // the sum is the same in every launch (no atomics).  The bound is the read
 // of the logits, 4 bytes per token and head: a head set's row of a token is
-// 32 consecutive bytes, a thread keeps kSets of them (two 16-byte loads
-// each) in flight.  The decode's merge needs the same inputs and nothing of
-// this, so the grid's first blocks do it: one launch instead of two (one
-// sequence of 4,096 tokens: 22.7 -> 20.7 us; long launches the same).  Beside
-// the decode it costs 6 us of 64 bf16 sequences of 512..4,096 tokens (33.4 us
-// without scores, 39.5 with) and 11 us of 32 E4M3 ones of 256..16,384 (69.8 and
-// 81.1), 34 MB of logits: with three blocks on an SM it waits for loads, a
-// third of HBM's rate.  Four with 64 registers each spill (83.6).
+// 32 consecutive bytes (two 16-byte loads), and a thread requests its next
+// step's rows before it merges or uses the ones it has.  The decode's merge
+// needs the same inputs and nothing of this, so the grid's first blocks do it:
+// one launch instead of two (one sequence of 4,096 tokens: 22.7 -> 20.7 us;
+// long launches the same).  Beside the decode it costs 2 us of 64 bf16
+// sequences of 512..4,096 tokens (33.4 us without scores, 35.0 with) and 8 us
+// of 32 E4M3 ones of 256..16,384 (69.8 and 77.9), 34 MB of logits, a third of
+// HBM's rate.  Four head sets per step with two blocks per SM are faster
+// where that is one wave (one sequence of 4,096: 13.2 us, 14.1 with three
+// blocks and two sets), slower in a large launch (79.2 and 77.9).
 
 constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreRows = 512;          // (set, head) rows whose (M, 1 / L) are staged at a time
-constexpr int kSets = 4;                 // head sets a thread loads at once
 
 // (M, L) of another part of the same row joins (m, l).
 __device__ __forceinline__ void join(float& m, float& l, float M, float L) {
@@ -43,9 +44,11 @@ __device__ __forceinline__ void join(float& m, float& l, float M, float L) {
     m = top;
 }
 
-template <int W, int D, typename QF>     // W: heads per row of logits
-__global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(DecodeParams p, float* __restrict__ scores, int MT,
-                                                              int merge_blocks, int chunks, int chunk) {
+// W: heads per row of logits; ONE: the grid is one wave of two blocks per SM
+template <int W, int D, typename QF, bool ONE>
+__global__ void __launch_bounds__(kScoreThreads, ONE ? 2 : 3)
+    score_kernel(DecodeParams p, float* __restrict__ scores, int MT, int merge_blocks, int chunks, int chunk) {
+    constexpr int kSets = ONE ? 4 : 2;   // head sets a thread loads at once
     __shared__ float2 ml[kScoreRows];    // (M, 1 / L); 1 / L = 0 for a row without weight or past the set's heads
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
@@ -60,70 +63,81 @@ __global__ void __launch_bounds__(kScoreThreads, 3) score_kernel(DecodeParams p,
     if (t0 >= n) return;
     const int np = num_partitions(n, p.P, p.Q, p.hold);
     const int nsets = (p.g + kHeadsPerUnit - 1) / kHeadsPerUnit, sets = p.Hkv * nsets;
-    constexpr int kTile = kScoreRows / W;
+    constexpr int kTile = kScoreRows / W / kSets * kSets;    // head sets whose rows are staged
     const bool one_tile = sets <= kTile;
-    for (int tc0 = t0; tc0 < min(n, t0 + chunk); tc0 += kScoreThreads) {
-        const int t = tc0 + tid;
-        float sum = 0.f;
-        for (int b0 = 0; b0 < sets; b0 += kTile) {
-            const int bn = min(kTile, sets - b0);
-            if (!one_tile || tc0 == t0) {
-                // eight lanes per row, over its partitions
-                __syncthreads();
-                for (int i = tid / 8; i - (lane / 8) < bn * W; i += kScoreThreads / 8) {
-                    const int set = b0 + i / W, kvh = set / nsets;
-                    const int hg = (set - kvh * nsets) * kHeadsPerUnit + i % W;
-                    const bool on = i < bn * W && hg < p.g;
-                    float m = -CUDART_INF_F, l = 0.f;
-                    if (on) {
-                        const float2* src = reinterpret_cast<const float2*>(p.part_ml) +
-                                            ((size_t)s * p.Hq + kvh * p.g + hg) * p.Pmax;
-#pragma unroll 4
-                        for (int q = lane % 8; q < np; q += 8) {
-                            const float2 v = __ldcg(src + q);
-                            join(m, l, v.x, v.y);
-                        }
-                    }
+    const int end = min(n, t0 + chunk);
+    // kSets head sets' logits of token tc + tid, from set b on
+    const float* x = p.logits + ((size_t)s * sets * p.max_ctx + tid) * W;
+    auto load = [&](float (&v)[kSets][W], int tc, int b) {
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) {
-                        const float M = __shfl_xor_sync(0xffffffffu, m, o), L = __shfl_xor_sync(0xffffffffu, l, o);
-                        join(m, l, M, L);
-                    }
-                    if (lane % 8 == 0 && i < bn * W) ml[i] = l != 0.f ? make_float2(m, 1.f / l) : make_float2(0.f, 0.f);
+        for (int k = 0; k < kSets; ++k) {
+            if (b + k >= sets || tc + tid >= n) continue;
+            const float* src = x + ((size_t)(b + k) * p.max_ctx + tc) * W;
+#pragma unroll
+            for (int j = 0; j < W; j += (W % 4 ? 2 : 4)) {
+                if constexpr (W % 4 == 0) {
+                    const float4 q = __ldcs(reinterpret_cast<const float4*>(src + j));
+                    v[k][j] = q.x; v[k][j + 1] = q.y; v[k][j + 2] = q.z; v[k][j + 3] = q.w;
+                } else {
+                    const float2 q = __ldcs(reinterpret_cast<const float2*>(src + j));
+                    v[k][j] = q.x; v[k][j + 1] = q.y;
                 }
-                __syncthreads();
-            }
-            const float* x = p.logits + (((size_t)s * sets + b0) * p.max_ctx + t) * W;
-            const size_t set_stride = (size_t)p.max_ctx * W;
-            for (int b = 0; b < bn && t < n; b += kSets) {
-                float v[kSets][W];
-#pragma unroll
-                for (int k = 0; k < kSets; ++k) {
-                    const float* src = x + (b + k) * set_stride;
-#pragma unroll
-                    for (int j = 0; j < W; j += (W % 4 ? 2 : 4)) {
-                        if (b + k >= bn) continue;
-                        if constexpr (W % 4 == 0) {
-                            const float4 q = __ldcs(reinterpret_cast<const float4*>(src + j));
-                            v[k][j] = q.x; v[k][j + 1] = q.y; v[k][j + 2] = q.z; v[k][j + 3] = q.w;
-                        } else {
-                            const float2 q = __ldcs(reinterpret_cast<const float2*>(src + j));
-                            v[k][j] = q.x; v[k][j + 1] = q.y;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kSets; ++k)
-                    if (b + k < bn)
-#pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            const float2 a = ml[(b + k) * W + j];
-                            // a row without weight adds nothing, whatever its logits are (one with a NaN: NaN)
-                            if (a.y != 0.f) sum = fmaf(tc::fast_exp2(v[k][j] - a.x), a.y, sum);
-                        }
             }
         }
-        if (t < n) scores[(size_t)s * MT + t] += sum;
+    };
+    // steps of kSets sets: a step's logits are requested before the rows of the step before are merged or used
+    float v[kSets][W], next[kSets][W], sum = 0.f;
+    load(v, t0, 0);
+    for (int tc = t0, b = 0;;) {
+        const int nb = b + kSets < sets ? b + kSets : 0, ntc = nb > 0 ? tc : tc + kScoreThreads;
+        if (ntc < end) load(next, ntc, nb);
+        if (b % kTile == 0 && (!one_tile || tc == t0)) {
+            // eight lanes per row, over its partitions
+            const int bn = min(kTile, sets - b);
+            __syncthreads();
+            for (int i = tid / 8; i - (lane / 8) < bn * W; i += kScoreThreads / 8) {
+                const int set = b + i / W, kvh = set / nsets;
+                const int hg = (set - kvh * nsets) * kHeadsPerUnit + i % W;
+                const bool on = i < bn * W && hg < p.g;
+                float m = -CUDART_INF_F, l = 0.f;
+                if (on) {
+                    const float2* src = reinterpret_cast<const float2*>(p.part_ml) +
+                                        ((size_t)s * p.Hq + kvh * p.g + hg) * p.Pmax;
+#pragma unroll 4
+                    for (int q = lane % 8; q < np; q += 8) {
+                        const float2 u = __ldcg(src + q);
+                        join(m, l, u.x, u.y);
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    const float M = __shfl_xor_sync(0xffffffffu, m, o), L = __shfl_xor_sync(0xffffffffu, l, o);
+                    join(m, l, M, L);
+                }
+                if (lane % 8 == 0 && i < bn * W) ml[i] = l != 0.f ? make_float2(m, 1.f / l) : make_float2(0.f, 0.f);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+            if (b + k < sets && tc + tid < n)
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const float2 a = ml[(b % kTile + k) * W + j];
+                    // a row without weight adds nothing, whatever its logits are (one with a NaN: NaN)
+                    if (a.y != 0.f) sum = fmaf(tc::fast_exp2(v[k][j] - a.x), a.y, sum);
+                }
+        if (nb == 0) {
+            if (tc + tid < n) scores[(size_t)s * MT + tc + tid] += sum;
+            sum = 0.f;
+        }
+        if (ntc >= end) break;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[k][j] = next[k][j];
+        tc = ntc;
+        b = nb;
     }
 }
 
@@ -413,11 +427,15 @@ static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scor
     const long long blocks = merge_blocks + (long long)p.S * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks), block(kScoreThreads);
+    auto launch = [&](auto kernel) {
+        return launch_pdl(kernel, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
+    };
+    const bool one = blocks <= 2 * 152;
     switch (score_width(p.g)) {
-        case 2: return launch_pdl(score_kernel<2, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
-        case 4: return launch_pdl(score_kernel<4, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
-        case 6: return launch_pdl(score_kernel<6, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
-        default: return launch_pdl(score_kernel<8, D, QF>, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
+        case 2: return one ? launch(score_kernel<2, D, QF, true>) : launch(score_kernel<2, D, QF, false>);
+        case 4: return one ? launch(score_kernel<4, D, QF, true>) : launch(score_kernel<4, D, QF, false>);
+        case 6: return one ? launch(score_kernel<6, D, QF, true>) : launch(score_kernel<6, D, QF, false>);
+        default: return one ? launch(score_kernel<8, D, QF, true>) : launch(score_kernel<8, D, QF, false>);
     }
 }
 
