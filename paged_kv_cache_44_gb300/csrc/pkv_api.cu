@@ -75,16 +75,38 @@ int resolve_partition(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int re
 // every unit has a worker (152 SMs x 6): one sequence of 400 tokens, 4 K/V
 // heads, in 32 / 64 / 128: 11.8 / 15.4 / 22.4 us; eight of 1,000 (1,024
 // units) 20.8 / 17.2 / 23.7.
-constexpr int kMaxSmallSplits = 48;
+//
+// A bf16 or E4M3 launch of up to three units per worker is a few rounds of
+// whole partitions, so it takes a partition that fills whole rounds: under a
+// window (most sequences fill it) as many equal ones per sequence as all
+// workers take at once; without one sets * keys / (1.6 workers) tokens
+// (lengths then reach down from the longest; at half of it on average one
+// round is four fifths full).  The plain rule's partition and this one: 32
+// E4M3 sequences of 256..16,384 tokens, scored, 78 us (512) and 67 (800); 16
+// bf16 ones 68 and 58 (640); 64 E4M3 ones under a window of 4,096: 54 and 50
+// (704); 32 bf16 ones 49 (384) and 42 (544); 256 of 1,056 tokens 93 (512) and
+// 88 (whole), in E4M3 73 and 56.  Lengths of 2,000..6,000, two thirds of the longest on average,
+// lose: 48 E4M3 sequences 53 and 56.5.  In 4 bits it gains 12% on the first
+// and loses 15% on 64 sequences of 512..4,096, so it is not taken there.
+constexpr int kMaxSmallSplits = 48, kMinWavePartition = 384, kMaxWavePartition = 1024;
 struct SplitRule {
     int smallest;
     long long units;
+    int workers;                          // of a full GB300; 0: no partition by rounds
 };
-constexpr SplitRule kSplit{64, kSmallLaunchUnits}, kSplitF32{32, 152LL * 6};
-int resolve_split(int S, int Hq, int Hkv, int d, int bs, int keys, int req, SplitRule rule = kSplit) {
+constexpr SplitRule kSplitBf16{64, kSmallLaunchUnits, 152 * 7}, kSplitE4m3{64, kSmallLaunchUnits, 152 * 11},
+    kSplitKv4{64, kSmallLaunchUnits, 0}, kSplitF32{32, 152LL * 6, 0};
+int resolve_split(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int keys, int req, SplitRule rule) {
     const int P = resolve_partition(S, Hq, Hkv, d, bs, keys, req);
     if (P < 0 || req != 0 || keys <= rule.smallest) return P;
     const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);
+    if (P >= kMinWavePartition && sets * ((keys + P - 1) / P) < 3LL * rule.workers) {
+        const long long parts = rule.workers / sets;
+        const long long wave = keys < max_ctx ? (parts > 0 ? keys / parts : 0) : sets * keys * 10 / (rule.workers * 16LL);
+        const int p = (int)((min(wave, 2LL * kMaxWavePartition) + 31) / 32 * 32);
+        if (p >= keys) return 0;
+        if (p >= kMinWavePartition && p <= kMaxWavePartition) return p;
+    }
     int p = P > 0 ? P : keys;
     while (p > rule.smallest) {
         const int half = max(rule.smallest, (p / 2 + 31) / 32 * 32);
@@ -822,11 +844,13 @@ size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, i
     if (window < 0 || num_sinks < 0 || !decode_shape_ok(S, Hq, Hkv, d, bs, max_context_len)) return 0;
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
-    if (P < 0) return 0;
-    // whatever the cache's dtype
-    const int P_f32 = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size, kSplitF32);
-    return max(make_plan(S, Hq, d, keys, P).bytes, make_plan(S, Hq, d, keys, P_f32).bytes);
+    size_t bytes = 0;                     // whatever the cache's dtype
+    for (const SplitRule rule : {kSplitBf16, kSplitE4m3, kSplitKv4, kSplitF32}) {
+        const int P = resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, rule);
+        if (P < 0) return 0;
+        bytes = max(bytes, make_plan(S, Hq, d, keys, P).bytes);
+    }
+    return bytes;
 }
 
 pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
@@ -845,7 +869,8 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
     const bool use_tc = kernel != PKV_DECODE_CUDA_CORES && decode_tc_supports(q_dtype, cache_dtype, d, bs, NB);
     const bool use_f32 = kernel == PKV_DECODE_AUTO && decode_f32_supports(cache_dtype, bs, NB);
-    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size, use_f32 ? kSplitF32 : kSplit);
+    const SplitRule rule = use_f32 ? kSplitF32 : cache_dtype == PKV_FP8_E4M3 ? kSplitE4m3 : kSplitBf16;
+    const int P = resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, rule);
     const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
@@ -928,7 +953,7 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
     if (chk != PKV_OK || S == 0) return chk;
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_split(S, Hq, Hkv, d, bs, keys, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, kSplitKv4);
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
     if (pl.split && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
@@ -952,8 +977,13 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
 
 size_t pkv_token_attention_scored_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_tokens,
                                                  int partition_size) {
-    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, partition_size);
-    return P < 0 ? 0 : make_scored_plan(S, Hq, Hkv, d, max_tokens, P).bytes;
+    size_t bytes = 0;                     // whatever the cache's dtype
+    for (const SplitRule rule : {kSplitBf16, kSplitE4m3}) {
+        const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, max_tokens, partition_size, rule);
+        if (P < 0) return 0;
+        bytes = max(bytes, make_scored_plan(S, Hq, Hkv, d, max_tokens, P).bytes);
+    }
+    return bytes;
 }
 
 pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
@@ -970,7 +1000,8 @@ pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_d
                                              v_scale, partition_size, PKV_DECODE_TENSOR_CORES);
     if (chk != PKV_OK || S == 0) return chk;
     if (!scores || (reinterpret_cast<uintptr_t>(scores) & 3u)) return PKV_ERR_INVALID_ARG;
-    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, partition_size);
+    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, max_tokens, partition_size,
+                                cache_dtype == PKV_FP8_E4M3 ? kSplitE4m3 : kSplitBf16);
     const ScoredPlan sp = make_scored_plan(S, Hq, Hkv, d, max_tokens, P);
     if (!workspace || workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
