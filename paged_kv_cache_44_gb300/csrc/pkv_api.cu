@@ -85,9 +85,10 @@ int resolve_partition(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int re
 // E4M3 sequences of 256..16,384 tokens, scored, 78 us (512) and 67 (800); 16
 // bf16 ones 68 and 58 (640); 64 E4M3 ones under a window of 4,096: 54 and 50
 // (704); 32 bf16 ones 49 (384) and 42 (544); 256 of 1,056 tokens 93 (512) and
-// 88 (whole), in E4M3 73 and 56.  Lengths of 2,000..6,000, two thirds of the longest on average,
-// lose: 48 E4M3 sequences 53 and 56.5.  In 4 bits it gains 12% on the first
-// and loses 15% on 64 sequences of 512..4,096, so it is not taken there.
+// 88 (whole), in E4M3 73 and 56.  Lengths of 2,000..6,000, two thirds of the
+// longest on average, lose: 48 E4M3 sequences 53 and 56.5.  In 4 bits it gains
+// 12% on the first and loses 15% on 64 sequences of 512..4,096, so it is not
+// taken there.
 constexpr int kMaxSmallSplits = 48, kMinWavePartition = 384, kMaxWavePartition = 1024;
 struct SplitRule {
     int smallest;

@@ -57,8 +57,8 @@
 // the blocks no query sees (window_span): the copies, the masks and the
 // partitions of the visible tokens are those of a shorter sequence, so the
 // bytes read are the visible blocks' and the rate is the decode's: 256 bf16
-// sequences of 1..8,192 under a window of 1,024 take 88 us, 5.6 TB/s, 128 E4M3
-// ones of 256..16,384 under 4,096 94 us, 5.3 TB/s.
+// sequences of 1..8,192 under a window of 1,024 take 81 us, 6.1 TB/s, 128 E4M3
+// ones of 256..16,384 under 4,096 91 us, 5.4 TB/s.
 //
 // Scored (SCORED): also stores the logits of a token table's tokens, 4 bytes
 // per token and query head, and every unit's (max, sum).  A weight

@@ -26,10 +26,10 @@ namespace {
 // step's rows before it merges or uses the ones it has.  The decode's merge
 // needs the same inputs and nothing of this, so the grid's first blocks do it:
 // one launch instead of two (one sequence of 4,096 tokens: 22.7 -> 20.7 us;
-// long launches the same).  Beside the decode it costs 2 us of 64 bf16
+// long launches the same).  With the same partitions it costs 2 us of 64 bf16
 // sequences of 512..4,096 tokens (33.4 us without scores, 35.0 with) and 8 us
-// of 32 E4M3 ones of 256..16,384 (69.8 and 77.9), 34 MB of logits, a third of
-// HBM's rate.  Four head sets per step with two blocks per SM are faster
+// of 32 E4M3 ones of 256..16,384 (69.8 and 77.9; 67.2 with the partitions the
+// scored decode takes), 34 MB of logits, a third of HBM's rate.  Four head sets per step with two blocks per SM are faster
 // where that is one wave (one sequence of 4,096: 13.2 us, 14.1 with three
 // blocks and two sets), slower in a large launch (79.2 and 77.9).
 
