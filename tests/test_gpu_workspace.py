@@ -63,3 +63,35 @@ def test_longest_length_zero(name):
     calls, q = _inputs()
     out = calls[name](torch.full_like(q, 7.0), 0)
     assert torch.equal(out, torch.zeros_like(q))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3", "kv4"])
+@pytest.mark.parametrize("d,part", [(64, 64), (128, 64), (128, 128), (128, 32)])
+def test_small_and_large_launches_agree(kind, d, part):
+    """Few (sequence, head set) pairs, whose partitions one launch merges, and the same sequences among many, whose
+    partitions a second launch merges: the same bits, with lengths from none to all partitions."""
+    lens, few, many, hkv = [0, 1, part, part + 1, 3 * part - 5, 4 * part], 6, 84, 2
+    n = max(lens)
+    nblk = -(-n // BS)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tables = torch.randperm(few * nblk, device="cuda", generator=g).view(few, nblk).int()
+    k, v = (torch.randn(few * nblk, BS, hkv, d, device="cuda", generator=g) for _ in range(2))
+    if kind == "kv4":
+        kc, vc = (pkv.make_kv4_cache(few * nblk, BS, hkv, d) for _ in range(2))
+        pkv.paged_kv4_write(k.flatten(0, 1), v.flatten(0, 1), kc, vc, torch.arange(few * nblk * BS, device="cuda"), BS)
+    else:
+        kc, vc = (x.to({"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[kind]) for x in (k, v))
+    q = torch.randn(few, 10, d, device="cuda", generator=g).bfloat16()
+    c = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    outs = []
+    for copies in (1, many // few):
+        qs, ts, cs = (x.repeat(copies, *[1] * (x.dim() - 1)) for x in (q, tables, c))
+        out = torch.full_like(qs, float("nan"))
+        if kind == "kv4":
+            pkv.paged_attention_decode_kv4(out, qs, kc, vc, ts, cs, n, d ** -0.5, BS, partition_size=part)
+        else:
+            pkv.paged_attention_decode_window(out, qs, kc, vc, ts, cs, n, d ** -0.5, n, 0, partition_size=part)
+        outs.append(out)
+    assert not outs[0].isnan().any() and (outs[0][0] == 0).all()
+    for i in range(many // few):
+        assert torch.equal(outs[1][i * few:(i + 1) * few], outs[0])
