@@ -32,7 +32,17 @@
 //    g is added to the group's values at the end.
 //
 // Rounding: p to fp16 and s * p to fp16 (2^-11 each); everything else
-// accumulates in fp32.
+// accumulates in fp32.  The weights carry 2^12 (into the exponential's
+// argument, off again at the unit's end), so that neither p nor s * p is below
+// fp16's smallest normal number where it counts: of the zeros' part a token of
+// weight p then loses no more than of the codes' part, whose loss would pull
+// the result towards the groups' minima (values of 1e-3, 32,768 tokens whose
+// logits have a deviation of 3: 37% off without it).  A group with a scale of
+// 2 or more (values that span 30 tensor scales) takes its weights times 2^-j,
+// so that s * p stays below 2^16, and its accumulators carry the 2^-j.  The
+// test for such scales is two loads, four ORs and a vote per stage: 32 x 32,768
+// tokens take 223.8 us with and without all this, 267 with a scale of 2 or more
+// in every stage.
 //
 // 32 sequences of 32,768 tokens (64 / 8 heads of 128, 1.34 GB): 226 us, 5.95
 // TB/s, 88% of the measured copy rate; the same tokens take 388 us from an
@@ -76,9 +86,10 @@ struct KCfg {
     static constexpr int kPartBytes = kTok * (D / 2 + D / 8);       // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kPartBytes;
     static constexpr int kQueue = kStages;
-    // trailer per worker: barriers, stage masks, the queue of claimed units (16-byte aligned)
+    // trailer per worker: barriers, stage masks, the queue of claimed units (16-byte aligned), the unit's shifts
     static constexpr int kQueueOff = (8 * kStages + 4 * kMasks * kStages + 15) / 16 * 16;
-    static constexpr int kCtlBytes = kQueueOff + 32 * kQueue;
+    static constexpr int kShiftOff = kQueueOff + 32 * kQueue;
+    static constexpr int kCtlBytes = kShiftOff + 16;
     static constexpr int kWarpBytes = kStages * kStageBytes + kCtlBytes;
     static constexpr int kSmemBytes = kWarps * kWarpBytes;
     static_assert(kTok == 32 || kTok == 64, "whole blocks of 16 or 32 tokens");
@@ -123,6 +134,10 @@ __device__ __forceinline__ float weight(float x, float xs, float mu) {
 }
 
 constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;   // codes at 2^-24 and at 2^-20
+constexpr float kWeightLog2 = 12.f, kWeightInv = 1.f / 4096.f;   // what the weights carry
+
+// 2^x, x in [-126, 127]
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(127 + x) << 23); }
 
 template <int D, int BS, bool WIN>
 __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
@@ -292,6 +307,9 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
     uint32_t qs = 0;                      // the group sums' fragment of the zeros' product
     float o[2 * G][4], zo[4];             // V's codes' part; zeros' part: group r, heads 2c, 2c + 1
     float m_ref[2];                       // reference maximum of heads 2c, 2c + 1
+    // byte g: group g's values are accumulated times 2^-j, j <= 16; bit 30: some j is not 0 (in shared memory: one
+    // register more is a spill, 2% of the launch)
+    uint32_t* shift_word = reinterpret_cast<uint32_t*>(ctl + C::kShiftOff);
     // Logits are kept in units of code * |q| sums: x = xs * x', xs >= 0 (the query carries the sign)
     const float xs = 4194304.f * fabsf(p.logit_scale_log2);
     const float q_sign = p.logit_scale_log2 < 0.f ? -1.f : 1.f;
@@ -316,6 +334,8 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
             for (int t = 0; t < 2 * G; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
             zo[0] = zo[1] = zo[2] = zo[3] = 0.f;
             m_ref[0] = m_ref[1] = -CUDART_INF_F;
+            if (lane == 0) *shift_word = 0;
+            __syncwarp();
         }
         const int slot = g_cons % C::kStages;
         const uint32_t parity = (g_cons / C::kStages) & 1u;
@@ -452,12 +472,46 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
             m_ref[0] = mn0;
             m_ref[1] = mn1;
         }
-        const float mu0 = m_ref[0] == -CUDART_INF_F ? 0.f : -m_ref[0] * xs;
-        const float mu1 = m_ref[1] == -CUDART_INF_F ? 0.f : -m_ref[1] * xs;
+        const float mu0 = m_ref[0] == -CUDART_INF_F ? 0.f : kWeightLog2 - m_ref[0] * xs;
+        const float mu1 = m_ref[1] == -CUDART_INF_F ? 0.f : kWeightLog2 - m_ref[1] * xs;
+
+        // V's scales of tokens 2 u and 2 u + 1 (u: the lane), in fp16; one of 2 or more has bit 14 set
+        uint32_t sv[G], large = 0;
+        lds_words<G>(vp + lane % (kTok / 2) / (BS / 2) * kHeadBytes + BS * (D / 2) + lane % (BS / 2) * (4 * G), sv);
+#pragma unroll
+        for (int g = 0; g < G; ++g) large |= sv[g];
+        const bool shifted = __any_sync(0xffffffffu, (large | *shift_word) & 0x40004000u);
+        uint32_t shifts = 0;
+        if (shifted) {
+            shifts = *shift_word;
+            // each group's j for the largest scale of its present tokens so far, 2^j <= s < 2^(j + 1)
+            const int u = lane % (kTok / 2);
+            const uint32_t here = (u < 16 ? vm[0] : vm[C::kMasks - 1]) >> (2 * (u % 16));
+            uint32_t next = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t lo = here & 1u ? sv[g] & 0x7fffu : 0u, hi = here & 2u ? (sv[g] >> 16) & 0x7fffu : 0u;
+                const int e = (int)(__reduce_max_sync(0xffffffffu, max(lo, hi)) >> 10) - 15;
+                const int was = (shifts >> (8 * g)) & 0x1fu, j = max(was, e);
+                if (j > was) {
+                    const float down = pow2(was - j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * g][k] *= down;
+                        o[2 * g + 1][k] *= down;
+                    }
+                }
+                next |= (uint32_t)j << (8 * g);
+            }
+            shifts = next;
+            __syncwarp();
+            if (lane == 0) *shift_word = next != 0 ? next | 0x40000000u : 0u;
+            __syncwarp();
+        }
 
         // ---- O^T += V^T . P^T, tile by tile
-        auto product = [&](auto whole) {
-            constexpr bool kWhole = decltype(whole)::value;
+        auto product = [&](auto whole, auto shift) {
+            constexpr bool kWhole = decltype(whole)::value, kShift = decltype(shift)::value;
 #pragma unroll
             for (int kt = 0; kt < kMT; ++kt) {
                 const float p0 = weight<kWhole>(x[kt][0], xs, mu0), p1 = weight<kWhole>(x[kt][1], xs, mu1);
@@ -492,7 +546,13 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
                 mma16816<true>(zo, z0, 0u, z1, 0u, pb0, pb1);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const uint32_t b0 = hmul2u(pb0, s0[g]), b1 = hmul2u(pb1, s1[g]);
+                    uint32_t q0 = pb0, q1 = pb1;
+                    if constexpr (kShift) {
+                        const float down = pow2(-(int)((shifts >> (8 * g)) & 0x1fu));
+                        q0 = hmul2u(q0, pack2<true>(down, down));
+                        q1 = hmul2u(q1, pack2<true>(down, down));
+                    }
+                    const uint32_t b0 = hmul2u(q0, s0[g]), b1 = hmul2u(q1, s1[g]);
                     mma16816<true>(o[2 * g], w0[g] & kLo, w0[g] & kHi, w1[g] & kLo, w1[g] & kHi, b0, b1);
                     // the upper byte's two codes as one number n + 16 n', and n alone: one instruction
                     // less than taking them apart; the rows are parted when the unit is finished
@@ -501,8 +561,9 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
                 }
             }
         };
-        if (full) product(std::true_type{});
-        else product(std::false_type{});
+        if (shifted) product(std::false_type{}, std::true_type{});
+        else if (full) product(std::true_type{}, std::false_type{});
+        else product(std::false_type{}, std::false_type{});
 
         // the slot is free again: let the issue side refill it
         __syncwarp();
@@ -513,6 +574,7 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
 
         if (c_stage == c_nst) {
             // ---- finish the unit
+            const uint32_t shifts = *shift_word;
             const uint64_t keep = l2_policy_evict_last();   // partials: held in L2 until the merge reads them
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -520,14 +582,16 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
                 const bool wr = h < cu.nh;
                 const size_t row = (size_t)cu.s * p.Hq + cu.h0 + h, u = row * p.Pmax + cu.part;
                 const float l = __shfl_sync(0xffffffffu, zo[j], 4 * G + c);
-                const float f = cu.np > 1 ? 1.f : (l > 0.f ? p.out_scale / l : 0.f);
+                const float f = cu.np > 1 ? kWeightInv : (l > 0.f ? p.out_scale / l : 0.f);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float zg = __shfl_sync(0xffffffffu, zo[j], 4 * g + c);
+                    const int up = (shifts >> (8 * g)) & 0x1fu;
+                    const float c0 = pow2(24 + up), c1 = pow2(20 + up);
                     // values 32 g + 4 r .. + 3 of head h; the last pair's second row holds both
-                    const float v[4] = {fmaf(o[2 * g][j], 16777216.f, zg) * f, fmaf(o[2 * g][j + 2], 1048576.f, zg) * f,
-                                        fmaf(o[2 * g + 1][j], 16777216.f, zg) * f,
-                                        fmaf(o[2 * g + 1][j + 2] - o[2 * g + 1][j], 1048576.f, zg) * f};
+                    const float v[4] = {fmaf(o[2 * g][j], c0, zg) * f, fmaf(o[2 * g][j + 2], c1, zg) * f,
+                                        fmaf(o[2 * g + 1][j], c0, zg) * f,
+                                        fmaf(o[2 * g + 1][j + 2] - o[2 * g + 1][j], c1, zg) * f};
                     if (!wr) continue;
                     if (cu.np == 1) {
                         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 32 * g + 4 * r) =
@@ -541,7 +605,7 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
                 }
                 if (wr && cu.np > 1 && r == 0) {
                     st_l2_hint(p.part_ml + 2 * u, m_ref[j] == -CUDART_INF_F ? m_ref[j] : m_ref[j] * xs, keep);
-                    st_l2_hint(p.part_ml + 2 * u + 1, l, keep);
+                    st_l2_hint(p.part_ml + 2 * u + 1, l * kWeightInv, keep);
                 }
             }
             have_unit = false;
