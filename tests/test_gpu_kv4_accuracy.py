@@ -1,5 +1,7 @@
 """The 4-bit decode against 64 bits with bounds made of the actual weights,
-scales and codes: values of every size, alone and next to each other."""
+scales and codes: values of every size, long sequences, few and many heavy
+tokens.  The bound of a case is tight enough to refuse an output of zeros and
+one that leaves out a stage or a partition (planted in the 64-bit form)."""
 import pytest
 import torch
 
@@ -9,6 +11,9 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import paged_kv_cache_44_gb300 as pkv
+
+STAGE = 64             # tokens of a stage
+
 
 def _weights(q, k, scale, seen):
     x = (k.double() @ q.double()) * scale
@@ -101,3 +106,33 @@ def test_groups_and_tokens_of_different_sizes(window, sinks, part, d, bs):
     seen = P64.window_seen(n, n - 1, window, sinks)
     ref, bound = reference(q, ks, vs, seen, d ** -0.5, 0.25, n)
     P64.assert_within(out, ref, bound)
+
+
+@pytest.mark.parametrize("n,part,drop", [(2049, 0, STAGE), (4096, 128, STAGE), (40000, 0, 1024)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_heavy_token_per_stage(n, part, drop, d):
+    """Every stage (of the longest: every 1,024 tokens) holds one token with most of its weight: the bound holds, and
+    refuses zeros and each output that leaves one such piece out."""
+    u = _normal(1, 2, d)
+    k, v = 0.1 * _normal(2, n, 2, d), _normal(3, n, 2, d)
+    heavy = torch.arange(0, n, drop, device="cuda")
+    heavy = (heavy + torch.randint(0, drop, heavy.shape, device="cuda",
+                                   generator=torch.Generator(device="cuda").manual_seed(4))).clamp(max=n - 1)
+    k[heavy] += u
+    # the logit of a heavy token: 12 above the others'
+    q = (12 * d ** 0.5 * u / (u * u).sum(-1, keepdim=True)).repeat_interleave(4, 0)
+    q = (q + 0.05 * _normal(5, 8, d)).bfloat16()
+    out, ks, vs = decode(q, k, v, 16, d ** -0.5, part=part)
+    seen = torch.ones(n, dtype=torch.bool, device="cuda")
+    ref, bound = reference(q, ks, vs, seen, d ** -0.5, 1.0, 1024)
+    P64.assert_within(out, ref, bound)
+    # the planted mistakes, in 64 bits on the host
+    ref, bound, q, ks, vs, seen = (x.cpu() for x in (ref, bound, q, ks, vs, seen))
+    assert ((ref.abs() > bound).double().mean(-1) > 0.7).all()
+    for lo in range(0, n, max(drop, n // 16 // drop * drop)):
+        less = seen.clone()
+        less[lo:lo + drop] = False
+        for h in range(0, 8, 3):
+            w = _weights(q[h], ks[:, h // 4], d ** -0.5, less)
+            wrong = (w[:, None] * vs[:, h // 4].double()).sum(0)
+            assert ((wrong - ref[h]).abs() > bound[h]).double().mean() > 0.5, (lo, h)
