@@ -597,9 +597,11 @@ PKV_API pkv_status pkv_paged_kv4_read(void* key, void* value, pkv_dtype out_dtyp
  * paged_attention_decode_kv4 -- pkv_paged_attention_decode over a 4-bit
  * cache, under a sliding window when window > 0 (0: every token).  bf16
  * query and output (anything else returns PKV_ERR_UNSUPPORTED).  The query
- * and its sums over 32 values go through fp16 for the products: |query| must
- * stay below 2047.  Workspace: pkv_decode_window_workspace_size(...) with the
- * same window and sinks.
+ * goes through fp16 for the products, after a power of two that brings the
+ * largest finite value of up to 8 heads of a K/V head below 1024: finite
+ * values up to 2^100 are fine, and a head keeps its bf16 precision down to
+ * 2^-16 times the largest of those heads.  Workspace:
+ * pkv_decode_window_workspace_size(...) with the same window and sinks.
  */
 PKV_API pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtype q_dtype,
                                                   const void* key_cache, const void* value_cache,
