@@ -498,6 +498,17 @@ PKV_API pkv_status pkv_vtoken_plan(const int32_t* token_slots, int MT, const int
  * no window) for pkv_paged_attention_decode_kv4; 0 for invalid arguments.
  * It is used as pkv_decode_workspace_size describes, and holds partial
  * results for the tokens a window leaves visible only.
+ *
+ * The size does not grow with S or max_context_len alone: few sequences are
+ * split further than many.  A loop may give every call the workspace of its
+ * largest one: with partition_size 0 a call whose own choice wants more takes
+ * fewer, longer partitions that fit, down to none (any workspace of 256 bytes
+ * serves).  A workspace of the largest size over all shapes of the loop keeps
+ * every call at its fastest.  An explicit partition_size is never replaced:
+ * short of its size, the call returns PKV_ERR_WORKSPACE, as it does without a
+ * workspace where it would split.  The same holds for the workspaces of
+ * pkv_paged_attention_prefill_window (for which the number of queries counts
+ * too) and, above the logits' part, pkv_token_attention_decode_scored.
  */
 PKV_API size_t pkv_decode_window_workspace_size(int S, int Hq, int Hkv, int d, int bs, int max_context_len, int window,
                                                 int num_sinks, int partition_size);

@@ -518,7 +518,10 @@ def decode_window_workspace_size(S: int, Hq: int, Hkv: int, d: int, bs: int, max
 def make_window_workspace(S: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, window: int,
                           num_sinks: int = 0, partition_size: int = 0, device=None) -> torch.Tensor:
     """A zero-filled workspace for paged_attention_decode_window and
-    paged_attention_decode_kv4 (window 0: no window)."""
+    paged_attention_decode_kv4 (window 0: no window).  One made for a loop's
+    largest call serves its smaller ones, some of them with fewer partitions
+    than they would choose; the largest size over the loop's shapes keeps all
+    of them at their fastest."""
     n = decode_window_workspace_size(S, Hq, Hkv, d, bs, max_context_len, window, num_sinks, partition_size)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
@@ -560,7 +563,8 @@ def prefill_window_workspace_size(S: int, num_query_tokens: int, max_query_len: 
 def make_prefill_window_workspace(S: int, num_query_tokens: int, max_query_len: int, Hq: int, Hkv: int, d: int,
                                   bs: int, max_context_len: int, window: int, num_sinks: int = 0,
                                   partition_size: int = 0, device=None) -> torch.Tensor:
-    """A zero-filled workspace for paged_attention_prefill_window."""
+    """A zero-filled workspace for paged_attention_prefill_window (reused as
+    make_window_workspace says: a few queries may want more than many)."""
     n = prefill_window_workspace_size(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs, max_context_len, window,
                                       num_sinks, partition_size)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
@@ -701,7 +705,8 @@ def scored_workspace_size(S: int, Hq: int, Hkv: int, d: int, bs: int, max_tokens
 
 def make_scored_workspace(S: int, Hq: int, Hkv: int, d: int, bs: int, max_tokens: int, partition_size: int = 0,
                           device=None) -> torch.Tensor:
-    """A workspace for token_attention_decode_scored, its header zero."""
+    """A workspace for token_attention_decode_scored, its header zero (reused
+    as make_window_workspace says)."""
     n = scored_workspace_size(S, Hq, Hkv, d, bs, max_tokens, partition_size)
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
     ws[:256] = 0

@@ -205,6 +205,27 @@ void set_partitions(DecodeParams& p, const DecodePlan& pl, int Pl, int no_split_
     p.Pmax = hold ? pl.Pmax : pl.Pmax_plain;
 }
 
+// The bytes of a workspace that a call may lay its partial results out in.
+// One that holds no header is none: then the size is the caller's mistake.
+size_t workspace_room(const void* workspace, size_t workspace_bytes) {
+    return workspace && workspace_bytes >= kWorkspaceHeaderBytes ? workspace_bytes : SIZE_MAX;
+}
+
+// The library's partition P where `room` bytes hold its plan, else the next
+// larger one of which they do (0: no split).  The plan's size does not grow
+// with the lengths, sequences or queries alone (few of them are split
+// further), so a workspace made for the largest call of a loop may be short
+// of a smaller one's choice by a few partitions.  bytes(P): the plan's size.
+template <typename Bytes>
+int fit_partition(int P, int keys, int req, size_t room, Bytes bytes) {
+    if (req != 0) return P;
+    while (P > 0 && bytes(P) > room) {
+        const long long next = (P + (P / 8 > 32 ? P / 8 : 32) + 31LL) / 32 * 32;
+        P = next < keys ? (int)next : 0;
+    }
+    return P;
+}
+
 // A window or sinks beyond the longest sequence are as good as its length
 // (kept small so that the kernels' sums of them stay in 32 bits).
 void clamp_window(int max_ctx, int& window, int& sinks) {
@@ -614,50 +635,6 @@ int resolve_prefill_partition(int S, int max_q_len, int Hq, int Hkv, int d, int 
     return P >= keys ? 0 : P;
 }
 
-// The same under a window, whose keys are few and a little more than a power
-// of two: the number of equal partitions (of whole 128-key stages) with the
-// least estimated time, in tenths of a microsecond.  A unit is a tile of 256
-// rows (128 in the one-tile kernel); its time was fitted to 16 shapes, a
-// stage 1.8 us (1.0), the rest 7.4 (6), and 6.6 (2) more to store a partial
-// result; the merge takes 3 and reads 512 bytes per row and partition.  512
-// queries, 64 / 8 heads, window 1,024: 26.8 us in one partition, 68 in the
-// three that the plain rule takes; 4 x 512 queries, 28 / 4 heads, window
-// 4,096: 136 and 170 (two); 128 queries: 69.8 in one, 25.2 in the nine of 512.
-int resolve_prefill_window_partition(int S, int T, int max_q_len, int Hq, int Hkv, int d, int bs, int max_ctx, int keys,
-                                     int req) {
-    const int P = resolve_prefill_partition(S, max_q_len, Hq, Hkv, d, bs, max_ctx, keys, req);
-    if (P < 0 || req != 0 || T < 1 || S < 1 || max_q_len < 1) return P;
-    const int g = Hq / Hkv;
-    const bool two = prefill_two_tiles(S, T, g);
-    const long long rows = two ? 2 * kPrefillTileRows : kPrefillTileRows;
-    const long long dense = S * (((long long)max_q_len * g + rows - 1) / rows), ragged = (long long)T * g / rows + S;
-    const long long tiles = (dense < ragged ? dense : ragged) * Hkv;
-    long long best = 0;
-    int best_P = 0;
-    for (int np = 1; np <= 16; ++np) {
-        const int part = ((keys + np - 1) / np + 127) / 128 * 128;
-        if (part >= keys && np > 1) break;
-        const int n = np > 1 ? (keys + part - 1) / part : 1;
-        const long long stages = ((n > 1 ? part : keys) + 127) / 128;
-        const long long unit = stages * (two ? 18 : 10) + (two ? 74 : 60) + (n > 1 ? (two ? 66 : 20) : 0);
-        const long long cost =
-            (tiles * n + 151) / 152 * unit + (n > 1 ? 30 + (long long)T * Hq * n * 512 / 650000 : 0);
-        if (np == 1 || cost < best) {
-            best = cost;
-            best_P = n > 1 ? part : 0;
-        }
-    }
-    return best_P;
-}
-
-// Keys of the longest tile under a window: a tile of either kernel (up to
-// 256 rows) holds at most 255 / g + 2 queries.
-int prefill_keys(int max_q_len, int Hq, int Hkv, int bs, int max_ctx, int window, int sinks) {
-    if (window <= 0) return max_ctx;
-    const int queries = (2 * kPrefillTileRows - 1) / (Hq / Hkv) + 2;
-    return window_bound(max_ctx, window, sinks, bs, max_q_len < queries ? max_q_len : queries);
-}
-
 struct PrefillPlan {
     int P, Pmax;
     bool split;
@@ -677,6 +654,52 @@ PrefillPlan plan_prefill(int T, int Hq, int d, int max_ctx, int P) {
     pl.acc_offset = up(pl.ml_offset + units * 2 * sizeof(float));
     pl.bytes = up(pl.acc_offset + units * d * sizeof(float));
     return pl;
+}
+
+// The same under a window, whose keys are few and a little more than a power
+// of two: the number of equal partitions (of whole 128-key stages) with the
+// least estimated time, in tenths of a microsecond.  A unit is a tile of 256
+// rows (128 in the one-tile kernel); its time was fitted to 16 shapes, a
+// stage 1.8 us (1.0), the rest 7.4 (6), and 6.6 (2) more to store a partial
+// result; the merge takes 3 and reads 512 bytes per row and partition.  512
+// queries, 64 / 8 heads, window 1,024: 26.8 us in one partition, 68 in the
+// three that the plain rule takes; 4 x 512 queries, 28 / 4 heads, window
+// 4,096: 136 and 170 (two); 128 queries: 69.8 in one, 25.2 in the nine of 512.
+// Only partitions whose partial results `room` bytes hold are considered.
+int resolve_prefill_window_partition(int S, int T, int max_q_len, int Hq, int Hkv, int d, int bs, int max_ctx, int keys,
+                                     int req, size_t room) {
+    const int P = resolve_prefill_partition(S, max_q_len, Hq, Hkv, d, bs, max_ctx, keys, req);
+    if (P < 0 || req != 0 || T < 1 || S < 1 || max_q_len < 1) return P;
+    const int g = Hq / Hkv;
+    const bool two = prefill_two_tiles(S, T, g);
+    const long long rows = two ? 2 * kPrefillTileRows : kPrefillTileRows;
+    const long long dense = S * (((long long)max_q_len * g + rows - 1) / rows), ragged = (long long)T * g / rows + S;
+    const long long tiles = (dense < ragged ? dense : ragged) * Hkv;
+    long long best = 0;
+    int best_P = 0;
+    for (int np = 1; np <= 16; ++np) {
+        const int part = ((keys + np - 1) / np + 127) / 128 * 128;
+        if (part >= keys && np > 1) break;
+        const int n = np > 1 ? (keys + part - 1) / part : 1;
+        if (n > 1 && plan_prefill(T, Hq, d, keys, part).bytes > room) break;
+        const long long stages = ((n > 1 ? part : keys) + 127) / 128;
+        const long long unit = stages * (two ? 18 : 10) + (two ? 74 : 60) + (n > 1 ? (two ? 66 : 20) : 0);
+        const long long cost =
+            (tiles * n + 151) / 152 * unit + (n > 1 ? 30 + (long long)T * Hq * n * 512 / 650000 : 0);
+        if (np == 1 || cost < best) {
+            best = cost;
+            best_P = n > 1 ? part : 0;
+        }
+    }
+    return best_P;
+}
+
+// Keys of the longest tile under a window: a tile of either kernel (up to
+// 256 rows) holds at most 255 / g + 2 queries.
+int prefill_keys(int max_q_len, int Hq, int Hkv, int bs, int max_ctx, int window, int sinks) {
+    if (window <= 0) return max_ctx;
+    const int queries = (2 * kPrefillTileRows - 1) / (Hq / Hkv) + 2;
+    return window_bound(max_ctx, window, sinks, bs, max_q_len < queries ? max_q_len : queries);
 }
 
 }  // namespace
@@ -713,7 +736,8 @@ pkv_status prefill_call(void* out, const void* query, pkv_dtype q_dtype, const v
     clamp_window(max_context_len, window, sinks);
     const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, sinks);
     const int P = window > 0 ? resolve_prefill_window_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs,
-                                                                max_context_len, keys, partition_size)
+                                                                max_context_len, keys, partition_size,
+                                                                workspace_room(workspace, workspace_bytes))
                              : resolve_prefill_partition(S, max_query_len, Hq, Hkv, d, bs, max_context_len, keys,
                                                          partition_size);
     if (P < 0) return PKV_ERR_INVALID_ARG;
@@ -772,7 +796,7 @@ size_t pkv_prefill_window_workspace_size(int S, int num_query_tokens, int max_qu
     clamp_window(max_context_len, window, num_sinks);
     const int keys = prefill_keys(max_query_len, Hq, Hkv, bs, max_context_len, window, num_sinks);
     const int P = resolve_prefill_window_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, bs, max_context_len,
-                                                   keys, partition_size);
+                                                   keys, partition_size, SIZE_MAX);
     if (P < 0) return 0;
     return plan_prefill(num_query_tokens, Hq, d, keys, P).bytes;
 }
@@ -871,7 +895,9 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
     const bool use_tc = kernel != PKV_DECODE_CUDA_CORES && decode_tc_supports(q_dtype, cache_dtype, d, bs, NB);
     const bool use_f32 = kernel == PKV_DECODE_AUTO && decode_f32_supports(cache_dtype, bs, NB);
     const SplitRule rule = use_f32 ? kSplitF32 : cache_dtype == PKV_FP8_E4M3 ? kSplitE4m3 : kSplitBf16;
-    const int P = resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, rule);
+    const int P = fit_partition(resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, rule), keys,
+                                partition_size, workspace_room(workspace, workspace_bytes),
+                                [&](int n) { return make_plan(S, Hq, d, keys, n).bytes; });
     const bool e4m3 = cache_dtype == PKV_FP8_E4M3;
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
@@ -954,7 +980,9 @@ pkv_status pkv_paged_attention_decode_kv4(void* out, const void* query, pkv_dtyp
     if (chk != PKV_OK || S == 0) return chk;
     if (window > 0) clamp_window(max_context_len, window, num_sinks);
     const int keys = decode_keys(bs, max_context_len, window, num_sinks);
-    const int P = resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, kSplitKv4);
+    const int P = fit_partition(resolve_split(S, Hq, Hkv, d, bs, max_context_len, keys, partition_size, kSplitKv4), keys,
+                                partition_size, workspace_room(workspace, workspace_bytes),
+                                [&](int n) { return make_plan(S, Hq, d, keys, n).bytes; });
     const DecodePlan pl = make_plan(S, Hq, d, keys, P);
     if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
     if (pl.split && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
@@ -1001,8 +1029,10 @@ pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_d
                                              v_scale, partition_size, PKV_DECODE_TENSOR_CORES);
     if (chk != PKV_OK || S == 0) return chk;
     if (!scores || (reinterpret_cast<uintptr_t>(scores) & 3u)) return PKV_ERR_INVALID_ARG;
-    const int P = resolve_split(S, Hq, Hkv, d, bs, max_tokens, max_tokens, partition_size,
-                                cache_dtype == PKV_FP8_E4M3 ? kSplitE4m3 : kSplitBf16);
+    const int P = fit_partition(resolve_split(S, Hq, Hkv, d, bs, max_tokens, max_tokens, partition_size,
+                                              cache_dtype == PKV_FP8_E4M3 ? kSplitE4m3 : kSplitBf16),
+                                max_tokens, partition_size, workspace_room(workspace, workspace_bytes),
+                                [&](int n) { return make_scored_plan(S, Hq, Hkv, d, max_tokens, n).bytes; });
     const ScoredPlan sp = make_scored_plan(S, Hq, Hkv, d, max_tokens, P);
     if (!workspace || workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
