@@ -1052,7 +1052,7 @@ pkv_status pkv_token_attention_decode_scored(void* out, const void* query, pkv_d
     p.logits = reinterpret_cast<float*>(ws + sp.logits_offset);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_decode_tc(p, q_dtype, cache_dtype, num_sms_current(), st, DecodeMode::kScored);
-    if (e == cudaSuccess) e = launch_score(p, q_dtype, sp.pl.split, scores, MT, st);
+    if (e == cudaSuccess) e = launch_score(p, q_dtype, sp.pl.split, scores, MT, num_sms_current(), st);
     return from_cuda(e);
 }
 
@@ -1083,7 +1083,7 @@ pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* scores, con
     p.token_slots = token_slots; p.scores = scores; p.num_tokens = num_tokens;
     p.new_slots = new_slots; p.new_scores = new_scores; p.new_num = new_num; p.evicted = evicted; p.err = err_word;
     p.S = S; p.MT = MT; p.budget = budget; p.first = num_first; p.recent = num_recent;
-    return from_cuda(launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_evict(p, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

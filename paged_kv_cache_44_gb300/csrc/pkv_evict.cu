@@ -6,6 +6,8 @@
 // tokens a sequence drops; the token table then lists the survivors.
 #include <cooperative_groups.h>
 
+#include <mutex>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_merge.cuh"
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kScoreThreads, ONE ? 2 : 3)
 
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictHeld = 16384;                    // keys per CTA, in shared memory
-constexpr int kBins = 2048, kMaxRanks = 16;
+constexpr int kBins = 2048, kMaxRanks = 16, kPortableRanks = 8;
 static_assert(kBins == 4 * kEvictThreads && kBins == 64 * 32, "four bins per thread, 64 sums of 32 bins");
 
 // Sum of the values of the lanes above this one.
@@ -404,25 +406,65 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     if (ranks > 1 && need > 0) cluster.barrier_wait();
 }
 
+// Whether the device can place a cluster of kMaxRanks CTAs, more than the 8
+// that every device can: a context with few SMs per GPC cannot.  Asked once
+// per device and context.
+class WideClusters {
+  public:
+    bool fit(const void* kernel, size_t smem) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        CUcontext ctx = current_context();
+        std::lock_guard<std::mutex> lock(mu_);
+        const bool cached = dev >= 0 && dev < kDevices && ctx != nullptr;
+        if (cached && known_[dev] == ctx) return fits_[dev];
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxRanks);
+        cfg.blockDim = dim3(kEvictThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxRanks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+        if (!ok) (void)cudaGetLastError();     // answered: no launch has failed
+        if (cached) {
+            known_[dev] = ctx;
+            fits_[dev] = ok;
+        }
+        return ok;
+    }
+
+  private:
+    static constexpr int kDevices = 64;
+    CUcontext known_[kDevices] = {};
+    bool fits_[kDevices] = {};
+    std::mutex mu_;
+};
+
 // CTAs per sequence: a cluster of up to 16, doubled while a share is above
 // 2,048 tokens and the grid still fits the GPU's two CTAs per SM.  Shares of
 // 1,024 / 2,048 / 4,096: one sequence of 16,384 tokens 10.5 / 9.0 / 11.6 us,
 // of 4,096 9.7 / 8.4 / 7.7, eight of 8,192 8.7 / 10.1 / 10.1.
-int evict_cluster(int S, int MT) {
+int evict_cluster(int S, int MT, int num_sms, int most) {
     int c = 1;
-    while (c < kMaxRanks && (MT + c - 1) / c > 2048 && (long long)S * c * 2 <= 2LL * 152) c *= 2;
+    while (c < most && (MT + c - 1) / c > 2048 && (long long)S * c * 2 <= 2LL * num_sms) c *= 2;
     return c;
 }
 
 }  // namespace
 
 template <int D, typename QF>
-static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scores, int MT, cudaStream_t st) {
+static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scores, int MT, int num_sms, cudaStream_t st) {
     const int merge_blocks = merge ? (int)(((long long)p.S * p.Hq + kScoreWarps - 1) / kScoreWarps) : 0;
     // tokens per thread: as many as leave every SM a few blocks, so that the rows' (M, L) serve more (64 bf16
     // sequences of 512..4,096: two 39.5 us, four 41.0; 32 E4M3 ones of 256..16,384: 82.3 and 81.1)
     const long long small = (long long)p.S * ((p.max_ctx + kScoreThreads - 1) / kScoreThreads);
-    const int chunk = kScoreThreads * (small <= 4 * 152 ? 1 : small <= 8 * 152 ? 2 : 4);
+    const int chunk = kScoreThreads * (small <= 4 * num_sms ? 1 : small <= 8 * num_sms ? 2 : 4);
     const int chunks = (p.max_ctx + chunk - 1) / chunk;
     const long long blocks = merge_blocks + (long long)p.S * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -430,7 +472,7 @@ static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scor
     auto launch = [&](auto kernel) {
         return launch_pdl(kernel, grid, block, 0, st, p, scores, MT, merge_blocks, chunks, chunk);
     };
-    const bool one = blocks <= 2 * 152;
+    const bool one = blocks <= 2 * num_sms;
     switch (score_width(p.g)) {
         case 2: return one ? launch(score_kernel<2, D, QF, true>) : launch(score_kernel<2, D, QF, false>);
         case 4: return one ? launch(score_kernel<4, D, QF, true>) : launch(score_kernel<4, D, QF, false>);
@@ -439,23 +481,38 @@ static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scor
     }
 }
 
-cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st) {
+cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, int num_sms,
+                         cudaStream_t st) {
     if (p.S == 0 || p.max_ctx == 0) return cudaSuccess;
     if (p.d == 64)
-        return q_dt == PKV_F32 ? launch_score_d<64, F32>(p, merge, scores, MT, st) : launch_score_d<64, BF16>(p, merge, scores, MT, st);
-    return q_dt == PKV_F32 ? launch_score_d<128, F32>(p, merge, scores, MT, st) : launch_score_d<128, BF16>(p, merge, scores, MT, st);
+        return q_dt == PKV_F32 ? launch_score_d<64, F32>(p, merge, scores, MT, num_sms, st)
+                               : launch_score_d<64, BF16>(p, merge, scores, MT, num_sms, st);
+    return q_dt == PKV_F32 ? launch_score_d<128, F32>(p, merge, scores, MT, num_sms, st)
+                           : launch_score_d<128, BF16>(p, merge, scores, MT, num_sms, st);
 }
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
-    const int c = evict_cluster(p.S, p.MT);
-    const int share = ((p.MT + c - 1) / c + kEvictThreads - 1) / kEvictThreads * kEvictThreads;
-    const bool held = share <= kEvictHeld;
+    auto share_of = [&](int c) { return ((p.MT + c - 1) / c + kEvictThreads - 1) / kEvictThreads * kEvictThreads; };
+    int c = evict_cluster(p.S, p.MT, num_sms, kMaxRanks);
+    int share = share_of(c);
+    bool held = share <= kEvictHeld;
     auto kern = held ? evict_kernel<true> : evict_kernel<false>;
     static SmemOptIn optin;
-    if (held) {
-        const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kEvictHeld * sizeof(uint32_t));
-        if (e != cudaSuccess) return e;
+    auto opt_in = [&] {
+        return held ? optin.ensure(reinterpret_cast<const void*>(kern), kEvictHeld * sizeof(uint32_t)) : cudaSuccess;
+    };
+    cudaError_t e = opt_in();
+    if (e != cudaSuccess) return e;
+    if (c > kPortableRanks) {
+        static WideClusters wide[2];
+        if (!wide[held].fit(reinterpret_cast<const void*>(kern), held ? kEvictHeld * sizeof(uint32_t) : 0)) {
+            c = evict_cluster(p.S, p.MT, num_sms, kPortableRanks);
+            share = share_of(c);
+            held = share <= kEvictHeld;
+            kern = held ? evict_kernel<true> : evict_kernel<false>;
+            if ((e = opt_in()) != cudaSuccess) return e;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.S * c));
@@ -470,11 +527,6 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (c > 8) {       // more than the portable cluster size, allowed per kernel and context
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 

@@ -166,7 +166,7 @@ struct EvictParams {
     int32_t* err;
     int S, MT, budget, first, recent;
 };
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t st);
 
 // Resolved layout of the decode workspace.
 struct DecodePlan {
@@ -210,7 +210,8 @@ cudaError_t launch_decode_tc_window(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c
 cudaError_t launch_decode_tc_scored(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
 // after a scored decode: scores[s][t] += the attention weights (rows of MT scores) and, when split, the merge
-cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, cudaStream_t st);
+cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, int num_sms,
+                         cudaStream_t st);
 bool decode_tc_supports(pkv_dtype q_dt, pkv_dtype c_dt, int d, int bs, int NB);
 cudaError_t launch_prefill_tc(const DecodeParams& p, const int32_t* query_start, int T, int max_q_len, int num_sms,
                               bool merge, cudaStream_t st);
