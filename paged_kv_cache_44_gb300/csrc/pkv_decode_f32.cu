@@ -384,6 +384,8 @@ __global__ void __launch_bounds__(FCfg<D>::kWarps * 32, 1)
         }
     }
 
+    wait_stages(bar, kStages, g_cons, g_issue, kWaitLimitCycles);      // none, unless it gave up
+
     if (p.local) merge_set<D, QF>(p, nsets, C::kWarps);
 
     // ---- leave the scheduling counters at zero for the next launch

@@ -632,6 +632,8 @@ __global__ void __launch_bounds__(KCfg<D>::kWarps * 32, 1)
         }
     }
 
+    wait_stages(bar, C::kStages, g_cons, g_issue, kWaitLimitCycles);   // none, unless it gave up
+
     if (p.local) merge_set<D, BF16>(p, nsets, C::kWarps);
 
     // ---- leave the scheduling counters at zero for the next launch

@@ -786,8 +786,9 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
         }
     }
 
-    // copies of this lane still in flight land before the warp leaves
+    // copies still in flight land before the warp leaves: this lane's, and (none, unless it gave up) the stages'
     if constexpr (TT) asm volatile("cp.async.wait_all;" ::: "memory");
+    wait_stages(bar, C::kStages, g_cons, g_issue, kWaitLimitCycles);
 
     if constexpr (WIN)
         if (p.local) merge_set<D, QF>(p, nsets, kWarps);

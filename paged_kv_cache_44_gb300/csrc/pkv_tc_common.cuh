@@ -54,6 +54,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Waits for a ring's stages [from, to), stage i on bar(i % n): what a worker
+// that gives up does before it leaves, so that no copy lands in shared memory
+// that is no longer its own.  Each wait ends after `limit` cycles.
+template <typename Bar>
+__device__ __forceinline__ void wait_stages(Bar bar, unsigned n, unsigned from, unsigned to, long long limit) {
+    for (; from != to; ++from) {
+        const long long start = clock64();
+        while (!mbar_try_wait(bar(from % n), (from / n) & 1u) && clock64() - start < limit) {
+        }
+    }
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
