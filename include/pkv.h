@@ -489,8 +489,10 @@ PKV_API pkv_status pkv_vtoken_plan(const int32_t* token_slots, int MT, const int
  * `window` tokens, its own among them.  window >= 1, num_sinks >= 0; a
  * window or sinks beyond a sequence's length hide nothing.  Blocks none of
  * whose tokens a call's queries see are not read, and neither are their
- * entries of the block table: they may have been freed or reused.  Tokens of
- * a read block that no query sees may hold anything, NaN included.
+ * entries of the block table: a caller that manages its own blocks may have
+ * reused them (the host block manager, pkv_pool_*, frees a sequence's blocks
+ * all at once).  Tokens of a read block that no query sees may hold anything,
+ * NaN included.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -137,8 +137,9 @@ int tail_hold(pkv_dtype cache_dtype, bool tensor_cores) {
 
 // The 4-bit decode: partitions held back where the launch has fewer than
 // three units per worker (152 SMs x 11), so that its last round is made of
-// chunks.  128 sequences under a window of 2,048: 53.3 us held, 56.6 not; 64
-// of 512..4,096 tokens: 26.8 and 27.9; with five rounds (256 sequences of
+// chunks.  128 sequences (28 / 4 heads of 128) under a window of 2,048 and 4
+// sinks: 53.3 us held, 56.6 not (floor 24.0); 64 (12 / 2 heads) of 512..4,096
+// tokens: 26.8 and 27.9; with five rounds (256 sequences, 28 / 4 heads, of
 // 1..4,096) the small units cost more than they even out: 86.5 and 81.9.
 int kv4_hold(int S, int Hq, int Hkv, int keys, int P) {
     const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);

@@ -45,12 +45,14 @@
 // in every stage.  The query goes to fp16 after a power of two per unit (256 x
 // 1..4,096 tokens: 80.3 us without and 80.7 with it, others the same).
 //
-// 32 sequences of 32,768 tokens (64 / 8 heads of 128, 1.34 GB): 226 us, 5.95
-// TB/s, 88% of the measured copy rate; the same tokens take 388 us from an
-// E4M3 cache and 645 from a bf16 one.  A 16-token tile is 268 instructions of
-// those 436 slots.  Warps x tokens per stage (two stages each, what shared
-// memory holds): 11 x 64 226 us, 10 x 64 226, 8 x 64 254, 16 x 32 270, 14 x 32
-// 284.  The whole launch is one kernel and the partitions' merge.
+// 32 sequences of 32,768 tokens (64 / 8 heads of 128, 1.34 GB): 221 us a call
+// in a loop, 228 where every call has other inputs, 5.9-6.1 TB/s, 87-90% of the
+// measured copy rate; the same tokens take 378 us from an E4M3 cache and 630
+// from a bf16 one (in a loop).  A 16-token tile is 268 instructions of those
+// 436 slots.  Warps x tokens per stage (two stages each, what shared memory
+// holds; measured before the weights carried 2^12): 11 x 64 226 us, 10 x 64
+// 226, 8 x 64 254, 16 x 32 270, 14 x 32 284.  The whole launch is one kernel
+// and the partitions' merge.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 

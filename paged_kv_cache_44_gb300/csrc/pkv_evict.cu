@@ -24,16 +24,18 @@ namespace {
 // its partitions.  One thread owns a token and adds its heads in order, so
 // the sum is the same in every launch (no atomics).  The bound is the read
 // of the logits, 4 bytes per token and head: a head set's row of a token is
-// 32 consecutive bytes (two 16-byte loads), and a thread requests its next
-// step's rows before it merges or uses the ones it has.  The decode's merge
-// needs the same inputs and nothing of this, so the grid's first blocks do it:
-// one launch instead of two (one sequence of 4,096 tokens: 22.7 -> 20.7 us;
-// long launches the same).  With the same partitions it costs 2 us of 64 bf16
-// sequences of 512..4,096 tokens (33.4 us without scores, 35.0 with) and 8 us
-// of 32 E4M3 ones of 256..16,384 (69.8 and 77.9; 67.2 with the partitions the
-// scored decode takes), 34 MB of logits, a third of HBM's rate.  Four head sets per step with two blocks per SM are faster
-// where that is one wave (one sequence of 4,096: 13.2 us, 14.1 with three
-// blocks and two sets), slower in a large launch (79.2 and 77.9).
+// 4 * score_width(g) consecutive bytes (8 to 32, in 16-byte loads, in 8-byte
+// ones where the width is 2 or 6), and a thread requests its next step's rows
+// before it merges or uses the ones it has.  The decode's merge needs the same
+// inputs and nothing of this, so the grid's first blocks do it: one launch
+// instead of two (one sequence of 4,096 tokens: 22.7 -> 20.7 us; long launches
+// the same).  Calls in a loop: 64 bf16 sequences of 512..4,096 tokens 31.4 us
+// without scores and 34.8 with; 32 E4M3 ones of 256..16,384 67.7 and, with the
+// same partitions (512), 79.0, with the scored decode's (800) 67.9; 34 MB of
+// logits are read at a third of HBM's rate.  Four head sets per step with two
+// blocks per SM are faster where that is one wave (one sequence of 4,096: 13.2
+// us, 14.1 with three blocks and two sets), slower in a large launch by 1.3 us
+// (32 E4M3 sequences in partitions of 512).
 
 constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
 constexpr int kScoreRows = 512;          // (set, head) rows whose (M, 1 / L) are staged at a time
@@ -461,8 +463,9 @@ int evict_cluster(int S, int MT, int num_sms, int most) {
 template <int D, typename QF>
 static cudaError_t launch_score_d(const DecodeParams& p, bool merge, float* scores, int MT, int num_sms, cudaStream_t st) {
     const int merge_blocks = merge ? (int)(((long long)p.S * p.Hq + kScoreWarps - 1) / kScoreWarps) : 0;
-    // tokens per thread: as many as leave every SM a few blocks, so that the rows' (M, L) serve more (64 bf16
-    // sequences of 512..4,096: two 39.5 us, four 41.0; 32 E4M3 ones of 256..16,384: 82.3 and 81.1)
+    // tokens per thread: as many as leave every SM a few blocks, so that the rows' (M, L) serve more (one / two / four,
+    // calls in a replayed graph: 64 bf16 sequences of 512..4,096 40.0 / 38.5 / 40.3 us, 32 E4M3 ones of 256..16,384
+    // 72.1 / 70.4 / 69.8, one of 4,096 16.5 / 16.6 / 18.6)
     const long long small = (long long)p.S * ((p.max_ctx + kScoreThreads - 1) / kScoreThreads);
     const int chunk = kScoreThreads * (small <= 4 * num_sms ? 1 : small <= 8 * num_sms ? 2 : 4);
     const int chunks = (p.max_ctx + chunk - 1) / chunk;

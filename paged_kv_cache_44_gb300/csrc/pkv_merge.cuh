@@ -41,7 +41,10 @@ __device__ __forceinline__ void merge_load_row(const float* src, float (&a)[E], 
 // ml: the (m, l) pairs of the row's partitions [np][2]; acc: their rows
 // [np][D].  Lane i ends with o = elements [i*E, i*E+E) of sum 2^(m_p - M)
 // acc_p; returns L (the same on every lane).  The data were written by
-// another kernel: loads go through L2 (ld.global.cg).
+// another kernel, which has completed (pdl_wait), or by warps of this CTA,
+// which have passed __threadfence and __syncthreads since (merge_set): either
+// way they are in L2, and the loads go there (ld.global.cg), not to a line
+// that L1 may hold.
 template <int D>
 __device__ __forceinline__ float merge_partitions(const float* __restrict__ ml, const float* __restrict__ acc,
                                                   int np, int lane, float (&o)[D / 32]) {
