@@ -75,8 +75,9 @@ enum {
     PKV_DEVERR_TIMEOUT = 5,       /* a staged copy did not land within ~2 s; the kernel gave up */
     PKV_DEVERR_QUERY_LEN = 6,     /* prefill: a sequence's queries are < 0, more than its length or
                                      than max_query_len, or outside [0, T) (the sequence is skipped) */
-    PKV_DEVERR_MOVE = 7           /* repack: a move out of range, or whose source is not the slot the
+    PKV_DEVERR_MOVE = 7,          /* repack: a move out of range, or whose source is not the slot the
                                      token table holds (the move is skipped) */
+    PKV_DEVERR_POSITION = 8       /* rotary: a position past the table (the token is skipped) */
 };
 
 /*
@@ -681,7 +682,90 @@ PKV_API pkv_status pkv_evict_tokens(const int32_t* token_slots, const float* sco
                                     int32_t* err_word, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * The calls of the three sections above with their arguments in one array,
+ * A prompt's way into the cache.
+ *
+ * Source: "LLM推論の基礎とvLLMの内部", section 4 (a token's K/V goes to a
+ * slot as it arrives) and section 6 (a step computes prompts next to decodes).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * rotary_kv_write -- rotary position embedding of Q and K, and
+ * pkv_paged_kv_write of the rotated K and of V, in one pass.
+ *
+ * query [T, Hq, d], key / value [T, Hkv, d] of in_dtype (F32 or BF16), their
+ * heads contiguous, their tokens *_stride elements apart (Hq * d or Hkv * d for
+ * arrays of their own, the row length where one projection left all three
+ * side by side).  Token i at position p = positions[i]: the first rotary_dim
+ * values of every head of Q and K are pairs j (values j and rotary_dim/2 + j;
+ * interleaved != 0: values 2j and 2j + 1), and a pair (a, b) becomes
+ *   (a c - b s, b c + a s),  c = cos_sin[p][j], s = cos_sin[p][rotary_dim/2 + j]
+ * (fp32 [max_position, rotary_dim]), each product and sum rounded to fp32.
+ * The other values, and V, stay.  The results are rounded once per output:
+ *   q_out [T, Hq, d], k_out [T, Hkv, d] (in_dtype; tokens *_out_stride apart;
+ *         k_out or NULL), and
+ *   the slot slot_mapping[i] of key_cache / value_cache (F32, BF16 or E4M3:
+ *         e4m3(x / scale) as pkv_paged_kv_write), negative: not written.
+ * A token with a negative position is padding: nothing of it is read or
+ * written.  One past the table is skipped too and reported
+ * (PKV_DEVERR_POSITION); a slot outside the pool is not written and reported.
+ * NULL query and q_out (Hq 0): only K and V.  NULL caches, value and
+ * slot_mapping: nothing is stored in a cache; with NULL key and k_out too
+ * only Q is rotated.  q_out may be query and k_out key (same stride); outputs
+ * must not overlap anything else.  Supported: d a multiple of 16, at most
+ * 512; rotary_dim a multiple of 16, at most d; strides that are multiples of
+ * 16 bytes.  T == 0 is a no-op.
+ */
+PKV_API pkv_status pkv_rotary_kv_write(const void* query, const void* key, const void* value, pkv_dtype in_dtype,
+                                       int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                       const int64_t* positions, const float* cos_sin, int max_position,
+                                       int rotary_dim, int interleaved,
+                                       void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                       void* key_cache, void* value_cache, pkv_dtype cache_dtype,
+                                       const int64_t* slot_mapping, int T, int NB, int bs, int Hq, int Hkv, int d,
+                                       float k_scale, float v_scale, int32_t* err_word, pkv_stream_t stream);
+
+/*
+ * prompt_attention -- attention over whole packed prompts whose K and V lie
+ * side by side, before or without a cache (pkv_paged_attention_prefill reads a
+ * cache through block tables).
+ *
+ * query [Tq, Hq, d] packs S sequences: rows query_start[s] .. query_start[s+1]
+ * (int32 [S+1], device, rising) are sequence s's, and rows key_start[s] ..
+ * key_start[s+1] of key / value [Tk, Hkv, d] its keys; the two may be one
+ * array.  Heads are contiguous, tokens *_stride elements apart (Hq * d or
+ * Hkv * d for arrays of their own).  With q_len queries and k_len keys, query i
+ * sits at position p = k_len - q_len + i; it sees
+ *   causal == 0: every key of its sequence;
+ *   causal != 0: keys t <= p, and with a window (window > 0; causal only) of
+ *                these t < num_sinks or t > p - window.
+ * out[i][h] = softmax(scale <q, k_t>) v_t over the keys it sees ([Tq, Hq, d],
+ * contiguous), zeros where there is none.  Rows of out that are no sequence's
+ * are left as they were.  max_query_len and max_key_len (host) bound the
+ * lengths; a sequence that breaks a bound, or whose rows leave [0, Tq) or
+ * [0, Tk), is skipped and reported (PKV_DEVERR_QUERY_LEN).  A V value that is
+ * not finite may reach queries of the same sequence that do not see it, by
+ * way of others that do (their weight 0 times it); K values do not.
+ *
+ * Few rows over many keys are split: partition_size 0 = library choice, -1 =
+ * never, > 0 = that many keys (a multiple of 128); then `workspace` must hold
+ * pkv_prompt_workspace_size(...) bytes, its first 256 zero before first use
+ * (a smaller one: fewer partitions, as pkv_decode_window_workspace_size
+ * says).  Supported: bf16 (sums in fp32, weights rounded to bf16), d in {64,
+ * 128}, strides that are multiples of 8 elements.  out must not overlap the
+ * inputs.
+ */
+PKV_API size_t pkv_prompt_workspace_size(int S, int num_query_tokens, int max_query_len, int max_key_len, int Hq,
+                                         int Hkv, int d, int window, int num_sinks, int partition_size);
+PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, const void* value,
+                                        pkv_dtype dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                        const int32_t* query_start, const int32_t* key_start, int S,
+                                        int num_query_tokens, int num_key_tokens, int max_query_len, int max_key_len,
+                                        int Hq, int Hkv, int d, float scale, int causal, int window, int num_sinks,
+                                        int partition_size, void* workspace, size_t workspace_bytes,
+                                        int32_t* err_word, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The calls of the four sections above with their arguments in one array,
  * for callers whose foreign-function interface pays per argument (the Python
  * binding's converts 27 arguments in 2.4 us and one in 0.3).  words[i] is the
  * call's argument i as 64 bits: pointers and sizes as they are, integers and
@@ -696,7 +780,9 @@ typedef enum {
     PKV_CALL_KV4_READ = 3,         /* pkv_paged_kv4_read */
     PKV_CALL_DECODE_KV4 = 4,       /* pkv_paged_attention_decode_kv4 */
     PKV_CALL_DECODE_SCORED = 5,    /* pkv_token_attention_decode_scored */
-    PKV_CALL_EVICT = 6             /* pkv_evict_tokens */
+    PKV_CALL_EVICT = 6,            /* pkv_evict_tokens */
+    PKV_CALL_ROTARY_WRITE = 7,     /* pkv_rotary_kv_write */
+    PKV_CALL_PROMPT = 8            /* pkv_prompt_attention */
 } pkv_call;
 PKV_API pkv_status pkv_invoke(int call, const void* words);
 

@@ -59,7 +59,7 @@ EXPORTED = ("pkv_paged_kv_write", "pkv_decode_workspace_size", "pkv_decode_parti
             "pkv_prefill_window_workspace_size", "pkv_paged_attention_prefill_window", "pkv_kv4_block_bytes",
             "pkv_paged_kv4_write", "pkv_paged_kv4_read", "pkv_paged_attention_decode_kv4",
             "pkv_token_attention_scored_workspace_size", "pkv_token_attention_decode_scored", "pkv_evict_tokens",
-            "pkv_invoke")
+            "pkv_rotary_kv_write", "pkv_prompt_workspace_size", "pkv_prompt_attention", "pkv_invoke")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -162,6 +162,14 @@ def _load() -> ctypes.CDLL:
     lib.pkv_token_attention_decode_scored.restype = i32
     lib.pkv_evict_tokens.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     lib.pkv_evict_tokens.restype = i32
+    lib.pkv_rotary_kv_write.argtypes = [vp, vp, vp, i32, i64, i64, i64, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp, vp,
+                                        i32, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp]
+    lib.pkv_rotary_kv_write.restype = i32
+    lib.pkv_prompt_workspace_size.argtypes = [i32] * 10
+    lib.pkv_prompt_workspace_size.restype = sz
+    lib.pkv_prompt_attention.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, vp, vp] + [i32] * 8 + \
+        [f32, i32, i32, i32, i32, vp, sz, vp, vp]
+    lib.pkv_prompt_attention.restype = i32
     lib.pkv_invoke.argtypes = [i32, ctypes.c_char_p]
     lib.pkv_invoke.restype = i32
     lib.pkv_status_string.argtypes = [i32]
@@ -226,7 +234,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _packed(number: int, symbol: str):
     """A call of the library through pkv_invoke: one conversion of all arguments instead of one each."""
-    kinds = {ctypes.c_void_p: "Q", ctypes.c_int: "q", ctypes.c_float: "d", ctypes.c_size_t: "Q"}
+    kinds = {ctypes.c_void_p: "Q", ctypes.c_int: "q", ctypes.c_int64: "q", ctypes.c_float: "d", ctypes.c_size_t: "Q"}
     pack, invoke = struct.Struct("=" + "".join(kinds[t] for t in getattr(lib, symbol).argtypes)).pack, lib.pkv_invoke
 
     def call(*args) -> None:
@@ -478,19 +486,20 @@ def repack_tokens(key_caches: Sequence[torch.Tensor], value_caches: Sequence[tor
                                                   token_bytes, _ptr(err_word), _stream(stream)))
 
 
-def _pointers(stream, *tensors: Optional[torch.Tensor]) -> list:
+def _pointers(stream, *tensors: Optional[torch.Tensor], rows: int = 0) -> list:
     """The tensors' addresses (0 for None), then the stream's handle; the last
     tensor is the error word.  The launch goes to the current device: tensors
-    of another one are refused, and so are strided ones."""
+    of another one are refused, and so are strided ones, but for the first
+    `rows` (_row_stride has looked at those)."""
     if tensors[-1] is not None and tensors[-1].dtype != torch.int32:
         raise ValueError("the error word must be int32")
     dev, out = _current_device(), []
-    for t in tensors:
+    for i, t in enumerate(tensors):
         if t is None:
             out.append(0)
         elif t.get_device() != dev:
             raise ValueError(f"pkv calls take tensors of the current CUDA device ({dev}), got one on {t.device}")
-        elif not t.is_contiguous():
+        elif i >= rows and not t.is_contiguous():
             raise ValueError("pkv calls take contiguous tensors")
         else:
             out.append(t.data_ptr())
@@ -505,6 +514,8 @@ _kv4_read = _packed(3, "pkv_paged_kv4_read")
 _decode_kv4 = _packed(4, "pkv_paged_attention_decode_kv4")
 _decode_scored = _packed(5, "pkv_token_attention_decode_scored")
 _evict = _packed(6, "pkv_evict_tokens")
+_rotary_write = _packed(7, "pkv_rotary_kv_write")
+_prompt = _packed(8, "pkv_prompt_attention")
 
 
 # ---- sliding window with sinks
@@ -761,6 +772,120 @@ def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: to
     _evict(
         p_ts, p_sc, p_nt, S, MT, budget, num_first, num_recent, p_ns, p_nsc, p_nn, p_ev, p_err,
         p_st)
+
+
+# ---- a prompt's way into the cache
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from one token of a [T, H, d] tensor to the next; the heads of a token are contiguous."""
+    T, H, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and H > 1):
+        raise ValueError("the heads of a token must be contiguous")
+    return s0 if T > 1 else H * d
+
+
+def rotary_kv_write(query: Optional[torch.Tensor], key: Optional[torch.Tensor], value: Optional[torch.Tensor],
+                    positions: torch.Tensor, cos_sin: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+                    k_out: Optional[torch.Tensor] = None, key_cache: Optional[torch.Tensor] = None,
+                    value_cache: Optional[torch.Tensor] = None, slot_mapping: Optional[torch.Tensor] = None,
+                    interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                    err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotary embedding of query [T, Hq, d] into q_out and of key [T, Hkv, d]
+    into k_out (or None) and the cache, with value, at slot_mapping int64 [T]
+    (negative = skip).  positions int64 [T] (negative = padding, nothing is
+    done); cos_sin fp32 [max_position, rotary_dim]: cosines, then sines.
+    Inputs and outputs may be slices of wider rows (one projection's Q, K and
+    V side by side); q_out may be query, and k_out key.  Without query and
+    q_out only K and V are taken, without caches only Q and K rotated."""
+    any_in = query if query is not None else key
+    if any_in is None or any_in.dim() != 3:
+        raise ValueError("rotary_kv_write takes query and/or key of three dimensions")
+    (T, _, d), dt = any_in.shape, any_in.dtype
+    Hq, Hkv = 0 if query is None else query.shape[1], 0 if key is None else key.shape[1]
+    if (query is None) != (q_out is None):
+        raise ValueError("query and q_out go together")
+    if (key_cache is None) != (value_cache is None) or (key_cache is None) != (slot_mapping is None) or \
+            (key_cache is None) != (value is None):
+        raise ValueError("value, the two caches and slot_mapping go together")
+    if (key is None) != (k_out is None and key_cache is None):
+        raise ValueError("key needs k_out or the caches, and they need key")
+    for t, H in ((query, Hq), (q_out, Hq), (key, Hkv), (value, Hkv), (k_out, Hkv)):
+        if t is not None and (t.shape != (T, H, d) or t.dtype != dt):
+            raise ValueError("query, key, value and the outputs must agree in tokens, heads, d and dtype")
+    if positions.dtype != torch.int64 or positions.shape != (T,):
+        raise ValueError("positions must be int64 [T]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
+    NB, bs, c_code = 1, 1, BF16
+    if key_cache is not None:
+        NB, bs = key_cache.shape[:2]
+        if key_cache.shape != (NB, bs, Hkv, d) or value_cache.shape != key_cache.shape or \
+                value_cache.dtype != key_cache.dtype:
+            raise ValueError("shape mismatch between tokens and caches")
+        if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+            raise ValueError("slot_mapping must be int64 [T]")
+        c_code = dtype_code(key_cache.dtype)
+    strides = [0 if t is None else _row_stride(t) for t in (query, key, value, q_out, k_out)]
+    p_q, p_k, p_v, p_qo, p_ko, p_pos, p_cs, p_kc, p_vc, p_sm, p_err, p_st = _pointers(
+        stream, query, key, value, q_out, k_out, positions, cos_sin, key_cache, value_cache, slot_mapping, err_word,
+        rows=5)
+    _rotary_write(
+        p_q, p_k, p_v, dtype_code(dt), strides[0], strides[1], strides[2], p_pos, p_cs, cos_sin.shape[0],
+        cos_sin.shape[1], int(interleaved), p_qo, strides[3], p_ko, strides[4], p_kc, p_vc, c_code, p_sm, T, NB, bs,
+        Hq, Hkv, d, k_scale, v_scale, p_err, p_st)
+
+
+def prompt_workspace_size(S: int, num_query_tokens: int, max_query_len: int, max_key_len: int, Hq: int, Hkv: int, d: int,
+                          window: int = 0, num_sinks: int = 0, partition_size: int = 0) -> int:
+    return int(lib.pkv_prompt_workspace_size(S, num_query_tokens, max_query_len, max_key_len, Hq, Hkv, d, window,
+                                             num_sinks, partition_size))
+
+
+def make_prompt_workspace(S: int, num_query_tokens: int, max_query_len: int, max_key_len: int, Hq: int, Hkv: int, d: int,
+                          window: int = 0, num_sinks: int = 0, partition_size: int = 0, device=None) -> torch.Tensor:
+    """A workspace for prompt_attention, its header zero (reused as
+    make_window_workspace says)."""
+    n = prompt_workspace_size(S, num_query_tokens, max_query_len, max_key_len, Hq, Hkv, d, window, num_sinks,
+                              partition_size)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    ws[:256] = 0
+    return ws
+
+
+def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                     query_start: torch.Tensor, max_query_len: int, scale: float,
+                     key_start: Optional[torch.Tensor] = None, max_key_len: Optional[int] = None, causal: bool = True,
+                     window: int = 0, num_sinks: int = 0, partition_size: int = 0,
+                     workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention over whole packed prompts: bf16 query/out [Tq, Hq, d], key and
+    value [Tk, Hkv, d] (slices of wider rows will do), query_start and
+    key_start int32 [S+1] (device; key_start None: the queries').  A sequence's
+    last query sits at its last key.  causal False: every key is seen; window
+    > 0: the first num_sinks keys and the last `window` up to the query."""
+    Tq, Hq, d = shape = query.shape
+    Tk, Hkv, d2 = key.shape
+    dt, S = query.dtype, query_start.numel() - 1
+    if d2 != d or out.shape != shape or value.shape != key.shape or \
+            not (out.dtype == dt == key.dtype == value.dtype):
+        raise ValueError("shape or dtype mismatch")
+    if key_start is None:
+        key_start = query_start
+    if max_key_len is None:
+        max_key_len = max_query_len
+    if query_start.dtype != torch.int32 or key_start.dtype != torch.int32 or key_start.numel() != S + 1 or S < 0:
+        raise ValueError("query_start and key_start must be int32 [S + 1]")
+    if workspace is None:
+        workspace = _own_workspace(stream, make_prompt_workspace, S, Tq, max_query_len, max_key_len, Hq, Hkv, d, window,
+                                   num_sinks, partition_size, device=query.device)
+    p_q, p_k, p_v, p_o, p_qs, p_ks, p_ws, p_err, p_st = _pointers(
+        stream, query, key, value, out, query_start, key_start, workspace, err_word, rows=3)
+    _prompt(
+        p_o, p_q, p_k, p_v, dtype_code(dt), _row_stride(query), _row_stride(key), _row_stride(value), p_qs, p_ks, S, Tq,
+        Tk, max_query_len, max_key_len, Hq, Hkv, d, scale, int(causal), window, num_sinks, partition_size, p_ws,
+        workspace.nbytes, p_err, p_st)
+    return out
 
 
 def vtoken_plan(token_slots: np.ndarray, num_tokens: np.ndarray, block_size: int, num_blocks: int):

@@ -924,6 +924,206 @@ pkv_status pkv_paged_attention_decode_window(void* out, const void* query, pkv_d
 
 // ---- 4-bit cache
 
+}  // extern "C"
+
+namespace pkv {
+namespace {
+
+// Key stages of the longest tile of a prompt: those of the sinks and of what
+// the windows of one group of query blocks span.
+int prompt_stages(int max_k, int g, int window, int sinks) {
+    const int all = (max_k + kPromptStage - 1) / kPromptStage;
+    if (window <= 0) return all;
+    const long long span = (long long)window - 1 + prompt_group(g) * kPromptStage + kPromptStage - 1;
+    const long long n = (span + kPromptStage - 1) / kPromptStage + (sinks + kPromptStage - 1) / kPromptStage;
+    return n < all ? (int)n : all;
+}
+
+PrefillPlan plan_prompt(int Tq, int Hq, int d, int stages, int P) {
+    PrefillPlan pl = plan_prefill(Tq, Hq, d, stages * kPromptStage, P * kPromptStage);
+    pl.P = P;
+    return pl;
+}
+
+bool prompt_shape_ok(int S, int Tq, int max_q, int max_k, int Hq, int Hkv, int d, int req) {
+    return S >= 0 && S <= 65535 && Tq >= 0 && max_q >= 0 && max_k >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
+           (d == 64 || d == 128) && req >= -1 && (req <= 0 || req % kPromptStage == 0);
+}
+
+// Stages per partition (0: no split).  Units that fill the SMs are not split.
+int resolve_prompt_partition(int S, int Tq, int max_q, int Hq, int Hkv, int d, int stages, int req, size_t room) {
+    if (req != 0) return req > 0 ? req / kPromptStage : 0;
+    const int g = Hq / Hkv, group = prompt_group(g);
+    const long long rows = (long long)group * kPromptStage;
+    const long long dense = S * ((max_q + rows - 1) / rows), ragged = Tq / rows + S;
+    const long long units = (dense < ragged ? dense : ragged) * Hkv * ((g * group + 1) / 2);
+    if (units == 0 || units >= 152) return 0;
+    const long long parts = 152 / units;
+    int P = (int)((stages + parts - 1) / parts);
+    if (P < 4) P = 4;
+    while (P < stages && plan_prompt(Tq, Hq, d, stages, P).bytes > room) P += P / 8 > 1 ? P / 8 : 1;
+    return P < stages ? P : 0;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+// ---- a prompt's way into the cache
+
+size_t pkv_prompt_workspace_size(int S, int num_query_tokens, int max_query_len, int max_key_len, int Hq, int Hkv, int d,
+                                 int window, int num_sinks, int partition_size) {
+    if (!prompt_shape_ok(S, num_query_tokens, max_query_len, max_key_len, Hq, Hkv, d, partition_size) || window < 0 ||
+        num_sinks < 0)
+        return 0;
+    clamp_window(max_key_len, window, num_sinks);
+    const int stages = prompt_stages(max_key_len, Hq / Hkv, window, num_sinks);
+    const int P = resolve_prompt_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, stages, partition_size, SIZE_MAX);
+    return plan_prompt(num_query_tokens, Hq, d, stages, P).bytes;
+}
+
+pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, const void* value, pkv_dtype dtype,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* query_start,
+                                const int32_t* key_start, int S, int num_query_tokens, int num_key_tokens,
+                                int max_query_len, int max_key_len, int Hq, int Hkv, int d, float scale, int causal,
+                                int window, int num_sinks, int partition_size, void* workspace,
+                                size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream) {
+    if (S < 0 || Hkv < 1 || Hq < 1 || num_query_tokens < 0 || num_key_tokens < 0 || max_query_len < 0 || max_key_len < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0) return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_BF16 || !(d == 64 || d == 128) || S > 65535) return PKV_ERR_UNSUPPORTED;
+    if ((long long)Hq * d > (1 << 24)) return PKV_ERR_UNSUPPORTED;
+    if (!isfinite(scale) || window < 0 || num_sinks < 0 || (window > 0 && !causal)) return PKV_ERR_INVALID_ARG;
+    if (partition_size < -1 || (partition_size > 0 && partition_size % kPromptStage != 0)) return PKV_ERR_INVALID_ARG;
+    if (S == 0 || num_query_tokens == 0) return PKV_OK;
+    if (!out || !query || !query_start || !key_start || (num_key_tokens > 0 && (!key || !value))) return PKV_ERR_INVALID_ARG;
+    struct Rows {
+        const void* at;
+        int64_t stride;
+        int heads, n;
+    };
+    const size_t out_bytes = (size_t)num_query_tokens * Hq * d * 2;
+    for (const Rows& r : {Rows{query, q_stride, Hq, num_query_tokens}, Rows{key, k_stride, Hkv, num_key_tokens},
+                          Rows{value, v_stride, Hkv, num_key_tokens}}) {
+        if (r.n == 0) continue;
+        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride >= (1LL << 38) || r.stride % 8 != 0)
+            return PKV_ERR_INVALID_ARG;
+        if (overlap(out, r.at, out_bytes, (size_t)((r.n - 1) * r.stride + (int64_t)r.heads * d) * 2)) return PKV_ERR_INVALID_ARG;
+    }
+    if (!aligned16(out) || (reinterpret_cast<uintptr_t>(query_start) & 3u) || (reinterpret_cast<uintptr_t>(key_start) & 3u))
+        return PKV_ERR_INVALID_ARG;
+    clamp_window(max_key_len, window, num_sinks);
+    const int stages = prompt_stages(max_key_len, Hq / Hkv, window, num_sinks);
+    const int P = resolve_prompt_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, stages, partition_size,
+                                           workspace_room(workspace, workspace_bytes));
+    const PrefillPlan pl = plan_prompt(num_query_tokens, Hq, d, stages, P);
+    if (pl.split && (!workspace || workspace_bytes < pl.bytes)) return PKV_ERR_WORKSPACE;
+    if (workspace && !aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    PromptParams p{};
+    p.out = out; p.q = query; p.k = key; p.v = value; p.query_start = query_start; p.key_start = key_start;
+    p.err = err_word; p.q_stride = q_stride; p.k_stride = num_key_tokens > 0 ? k_stride : (int64_t)Hkv * d;
+    p.v_stride = num_key_tokens > 0 ? v_stride : (int64_t)Hkv * d;
+    p.S = S; p.Tq = num_query_tokens; p.Tk = num_key_tokens; p.max_q = max_query_len; p.max_k = max_key_len;
+    p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.group = prompt_group(p.g);
+    p.causal = causal != 0; p.window = window; p.sinks = num_sinks;
+    p.P = pl.split ? P : 0;
+    p.Pmax = pl.Pmax;
+    p.scale_log2 = scale * kLog2e;
+    if (workspace && workspace_bytes >= kWorkspaceHeaderBytes) p.sched = reinterpret_cast<unsigned*>(workspace);
+    if (pl.split) {
+        char* ws = static_cast<char*>(workspace);
+        p.part_ml = reinterpret_cast<float*>(ws + pl.ml_offset);
+        p.part_acc = reinterpret_cast<float*>(ws + pl.acc_offset);
+    }
+    return from_cuda(launch_prompt(p, d, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_rotary_kv_write(const void* query, const void* key, const void* value, pkv_dtype in_dtype,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                               const float* cos_sin, int max_position, int rotary_dim, int interleaved, void* q_out,
+                               int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* key_cache,
+                               void* value_cache, pkv_dtype cache_dtype, const int64_t* slot_mapping, int T, int NB,
+                               int bs, int Hq, int Hkv, int d, float k_scale, float v_scale, int32_t* err_word,
+                               pkv_stream_t stream) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || d < 1 || max_position < 1 || rotary_dim < 0) return PKV_ERR_INVALID_ARG;
+    if (in_dtype != PKV_F32 && in_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if (d % 16 != 0 || d > 512 || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (rotary_dim > d) return PKV_ERR_INVALID_ARG;
+    if (Hq > 65535 || Hkv > 65535) return PKV_ERR_UNSUPPORTED;
+    const bool cached = key_cache != nullptr;
+    if (cached != (value_cache != nullptr) || cached != (slot_mapping != nullptr)) return PKV_ERR_INVALID_ARG;
+    if (cached) {
+        if (cache_dtype != PKV_F32 && cache_dtype != PKV_BF16 && cache_dtype != PKV_FP8_E4M3)
+            return PKV_ERR_UNSUPPORTED;
+        if (NB < 1 || bs < 1 || (long long)NB * bs > (1LL << 40)) return PKV_ERR_INVALID_ARG;
+        if (cache_dtype == PKV_FP8_E4M3 && (!finite_pos(k_scale) || !finite_pos(v_scale))) return PKV_ERR_INVALID_ARG;
+    } else {
+        cache_dtype = PKV_BF16;
+    }
+    if (T == 0) return PKV_OK;
+    // which of Q, K and V there are; what comes in has to go out
+    const bool has_q = query != nullptr, has_k = key != nullptr;
+    if (has_q != (q_out != nullptr) || has_q != (Hq > 0)) return PKV_ERR_INVALID_ARG;
+    if ((has_k || cached) != (Hkv > 0) || has_k != (cached || k_out != nullptr) || cached != (value != nullptr))
+        return PKV_ERR_INVALID_ARG;
+    if (!has_q && !has_k) return PKV_ERR_INVALID_ARG;
+    if (!positions || (!cos_sin && rotary_dim > 0)) return PKV_ERR_INVALID_ARG;
+    const int eb = in_dtype == PKV_F32 ? 4 : 2;
+    struct Rows {
+        const void* at;
+        int64_t stride;
+        int heads;
+    };
+    const Rows rows[5] = {{query, q_stride, Hq}, {key, k_stride, Hkv}, {value, v_stride, Hkv},
+                          {q_out, q_out_stride, Hq}, {k_out, k_out_stride, Hkv}};
+    for (const Rows& r : rows) {
+        if (r.at == nullptr) continue;
+        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride > (1LL << 40) || r.stride * eb % 16 != 0)
+            return PKV_ERR_INVALID_ARG;
+    }
+    // an output lies on its own input, row for row, or on nothing that is read or written here
+    auto apart = [&](const Rows& a, const Rows& b) {
+        const int64_t wa = (int64_t)a.heads * d * eb, wb = (int64_t)b.heads * d * eb;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+        if (!overlap(a.at, b.at, (size_t)(T - 1) * a.stride * eb + wa, (size_t)(T - 1) * b.stride * eb + wb)) return true;
+        if (a.stride != b.stride) return false;
+        const int64_t s = a.stride * eb, off = (int64_t)((x > y ? x - y : y - x) % (uintptr_t)s);
+        const int64_t ab = x > y ? (s - off) % s : off;          // from a row of a to the next row of b
+        return ab >= wa && s - ab >= wb;
+    };
+    for (int o = 3; o < 5; ++o) {
+        if (rows[o].at == nullptr) continue;
+        for (int i = 0; i < o; ++i) {
+            if (rows[i].at == nullptr) continue;
+            if (i == o - 3 && rows[i].at == rows[o].at && (rows[i].stride == rows[o].stride || T == 1)) continue;
+            if (!apart(rows[o], rows[i])) return PKV_ERR_INVALID_ARG;
+        }
+    }
+    if (cached) {
+        const size_t pool = (size_t)NB * bs * Hkv * d *
+                            (cache_dtype == PKV_F32 ? 4 : (cache_dtype == PKV_BF16 ? 2 : 1));
+        if (overlap(key_cache, value_cache, pool, pool)) return PKV_ERR_INVALID_ARG;
+        for (const Rows& r : rows)
+            for (const void* c : {(const void*)key_cache, (const void*)value_cache})
+                if (r.at && overlap(r.at, c, (size_t)((T - 1) * r.stride + (int64_t)r.heads * d) * eb, pool))
+                    return PKV_ERR_INVALID_ARG;
+    }
+    if (!aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(positions) & 7u) ||
+        (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || !aligned16(key_cache) || !aligned16(value_cache))
+        return PKV_ERR_INVALID_ARG;
+    RotaryParams p{};
+    p.q = query; p.k = key; p.v = value; p.q_out = q_out; p.k_out = k_out;
+    p.positions = positions; p.cos_sin = cos_sin; p.key_cache = key_cache; p.value_cache = value_cache;
+    p.slot_mapping = slot_mapping; p.err = err_word;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;
+    p.T = T; p.Hq = has_q ? Hq : 0; p.Hk = has_k ? Hkv : 0; p.Hv = cached ? Hkv : 0; p.Hkv = Hkv;
+    p.d = d; p.rot = rotary_dim; p.max_position = max_position; p.interleaved = interleaved != 0;
+    p.NB = NB; p.bs = bs; p.k_scale = k_scale; p.v_scale = v_scale;
+    return from_cuda(launch_rotary(p, in_dtype, cache_dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t pkv_kv4_block_bytes(int bs, int Hkv, int d) {
     if (!(d == 64 || d == 128) || !(bs == 16 || bs == 32) || Hkv < 1) return 0;
     return (size_t)Hkv * kv4_head_bytes(bs, d);

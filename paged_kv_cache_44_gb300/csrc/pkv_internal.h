@@ -96,6 +96,49 @@ struct Kv4Params {
 // the write, or the read of the same slots (dt: the dtype of the tokens outside the cache)
 cudaError_t launch_kv4(const Kv4Params& p, pkv_dtype dt, bool read, cudaStream_t st);
 
+struct RotaryParams {
+    const void* q;            // [T] rows of Hq heads, q_stride elements apart; the same for k and v
+    const void* k;
+    const void* v;
+    void* q_out;
+    void* k_out;              // or null
+    const int64_t* positions; // [T]
+    const float* cos_sin;     // [max_position][rot]: cosines, then sines, of rot / 2 pairs
+    void* key_cache;          // [NB * bs][Hkv][d], or null
+    void* value_cache;
+    const int64_t* slot_mapping;
+    int32_t* err;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    int T, Hq, Hk, Hv, Hkv;   // rows of q, k and v that there are (0: none), heads of the cache
+    int d, rot, max_position, interleaved, NB, bs;
+    float k_scale, v_scale;
+};
+cudaError_t launch_rotary(const RotaryParams& p, pkv_dtype in_dt, pkv_dtype cache_dt, cudaStream_t st);
+
+constexpr int kPromptStage = 128;        // keys per stage, and queries per tile, of the prompt attention
+
+struct PromptParams {
+    void* out;                // [Tq][Hq][d]
+    const void* q;            // [Tq] rows of Hq heads, q_stride elements apart; k and v [Tk] of Hkv
+    const void* k;
+    const void* v;
+    const int32_t* query_start;   // [S + 1]
+    const int32_t* key_start;     // [S + 1]
+    float* part_ml;           // [Tq][Hq][Pmax][2]: running max (log2 units) and sum
+    float* part_acc;          // [Tq][Hq][Pmax][d]
+    unsigned* sched;          // scheduling counters in the workspace header (or null)
+    int32_t* err;
+    long long q_stride, k_stride, v_stride;
+    int S, Tq, Tk, max_q, max_k, Hq, Hkv, g;
+    int group;                // query blocks whose tiles are paired (prompt_group)
+    int causal, window, sinks;
+    int P, Pmax;              // stages per partition (0: no split), partial results per row
+    float scale_log2;
+};
+// an odd number of heads per K/V head pairs the tiles of two query blocks
+inline int prompt_group(int g) { return g % 2 ? 2 : 1; }
+cudaError_t launch_prompt(const PromptParams& p, int d, int num_sms, cudaStream_t st);
+
 struct CopyParams {
     const int64_t* mapping;
     int32_t* err;
@@ -225,6 +268,10 @@ cudaError_t launch_prefill_merge(const DecodeParams& p, const int32_t* query_sta
 // 2-D tensor map over a bf16 K or V cache [NB * bs tokens, Hkv * d]: boxes of
 // 64 values by min(bs, 32) tokens, 128-byte swizzle
 bool prefill_encode_kv_map(CUtensorMap* map, const void* base, const DecodeParams& p);
+
+// 2-D tensor map over bf16 rows of `values` values, `stride` elements apart:
+// boxes of 64 values by box_rows rows, 128-byte swizzle
+bool encode_rows_map(CUtensorMap* map, const void* base, long long rows, int values, long long stride, int box_rows);
 
 // 3-D tensor map over the query [T, Hq, d]: boxes of 64 values by the g heads
 // of one K/V head by tile_queries queries, 128-byte swizzle

@@ -20,7 +20,7 @@ bool take(const unsigned char* at, T& v) {
         double w;
         std::memcpy(&w, at, 8);
         v = static_cast<T>(w);
-    } else if constexpr (std::is_unsigned_v<T> && sizeof(T) == 8) {
+    } else if constexpr (std::is_integral_v<T> && sizeof(T) == 8) {
         std::memcpy(&v, at, 8);
     } else {                                  // int and enumerations
         int64_t w;
@@ -55,6 +55,8 @@ extern "C" pkv_status pkv_invoke(int call, const void* words) {
         case PKV_CALL_DECODE_KV4: return run(pkv_paged_attention_decode_kv4, words);
         case PKV_CALL_DECODE_SCORED: return run(pkv_token_attention_decode_scored, words);
         case PKV_CALL_EVICT: return run(pkv_evict_tokens, words);
+        case PKV_CALL_ROTARY_WRITE: return run(pkv_rotary_kv_write, words);
+        case PKV_CALL_PROMPT: return run(pkv_prompt_attention, words);
     }
     return PKV_ERR_INVALID_ARG;
 }

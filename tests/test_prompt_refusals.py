@@ -1,0 +1,86 @@
+"""Arguments that the rotary write, the prompt attention and the shared decode
+refuse, on the host: no GPU is needed, and a call that got past its checks
+would answer 4 here."""
+import pytest
+import torch
+
+import paged_kv_cache_44_gb300 as pkv
+
+A = 1 << 30            # an aligned address nothing reads
+
+
+def _rotary(q=A, k=2 * A, v=3 * A, dt=1, qs=1024, ks=256, vs=256, pos=4 * A, cs=5 * A, mp=100, rot=128, inter=0, qo=6 * A,
+            qos=1024, ko=7 * A, kos=256, kc=8 * A, vc=9 * A, cdt=1, slots=10 * A, T=5, NB=10, bs=16, Hq=8, Hkv=2, d=128,
+            k_scale=1.0, v_scale=1.0):
+    return pkv.lib.pkv_rotary_kv_write(q, k, v, dt, qs, ks, vs, pos, cs, mp, rot, inter, qo, qos, ko, kos, kc, vc, cdt,
+                                       slots, T, NB, bs, Hq, Hkv, d, k_scale, v_scale, None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(T=0), 0), (dict(dt=2), 2), (dict(cdt=5), 2), (dict(d=120, rot=96), 2), (dict(d=528, qs=1 << 14, qos=1 << 14, ks=1 << 12, vs=1 << 12, kos=1 << 12), 2),
+    (dict(rot=8), 2), (dict(rot=144), 1), (dict(rot=-16), 1), (dict(mp=0), 1), (dict(Hq=-1), 1), (dict(Hq=0), 1),
+    (dict(q=None), 1), (dict(qo=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(kc=None), 1), (dict(vc=None), 1),
+    (dict(slots=None), 1), (dict(pos=None), 1), (dict(cs=None), 1), (dict(q=A + 8), 1), (dict(qs=1023), 1), (dict(qs=1028), 1),
+    (dict(ks=255), 1), (dict(kos=128), 1), (dict(cs=5 * A + 4), 1), (dict(pos=4 * A + 4), 1), (dict(NB=0), 1),
+    (dict(cdt=2, k_scale=0.0), 1), (dict(cdt=2, v_scale=float("nan")), 1), (dict(kc=8 * A + 2), 1),
+    # outputs over something else that is read or written
+    (dict(qo=2 * A), 1), (dict(qo=A + 16), 1), (dict(qo=A, qos=2048), 1), (dict(ko=3 * A), 1), (dict(ko=6 * A + 256), 1),
+    (dict(qo=8 * A + 4096), 1), (dict(kc=9 * A), 1), (dict(qs=1536, q=A, k=A + 2048, ks=1536, qo=A + 1024, qos=1536), 1)])
+def test_rotary(kw, status):
+    assert _rotary(**kw) == status
+
+
+def test_rotary_without_anything_to_do():
+    none = dict(kc=None, vc=None, slots=None, v=None)
+    assert _rotary(q=None, qo=None, Hq=0, k=None, ko=None, Hkv=0, **none) == 1
+    assert _rotary(k=None, ko=None, Hkv=0, T=0, **none) == 0
+
+
+def test_rotary_binding():
+    x = torch.zeros(4, 2, 64)
+    pos, cs = torch.zeros(4, dtype=torch.int64), torch.zeros(10, 64)
+    for args, kw in [((x, None, None, pos, cs), {}), ((None, None, None, pos, cs), {}), ((x, x, None, pos, cs, x), {}),
+                     ((x, None, None, pos.int(), cs, x), {}), ((x, None, None, pos, cs.double(), x), {}),
+                     ((x, None, None, pos, cs, x.double()), {}), ((x, None, None, pos, cs, x[:3]), {}),
+                     ((x, x, x, pos, cs, x, x), {}), ((x.transpose(1, 2), None, None, pos, cs, x.transpose(1, 2)), {})]:
+        with pytest.raises((ValueError, TypeError)):
+            pkv.rotary_kv_write(*args, **kw)
+
+
+def _prompt(out=A, q=2 * A, k=3 * A, v=4 * A, dt=1, qs=1024, ks=256, vs=256, q_start=5 * A, k_start=6 * A, S=2, Tq=100,
+            Tk=100, mq=60, mk=60, Hq=8, Hkv=2, d=128, scale=0.1, causal=1, window=0, sinks=0, part=0, ws=7 * A, wsb=1 << 40):
+    return pkv.lib.pkv_prompt_attention(out, q, k, v, dt, qs, ks, vs, q_start, k_start, S, Tq, Tk, mq, mk, Hq, Hkv, d, scale,
+                                        causal, window, sinks, part, ws, wsb, None, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=-1), 1), (dict(S=0), 0), (dict(S=65536), 2), (dict(Tq=0), 0), (dict(Tq=-1), 1), (dict(Tk=-1), 1), (dict(mq=-1), 1),
+    (dict(mk=-1), 1), (dict(dt=0), 2), (dict(dt=2), 2), (dict(d=96), 2), (dict(Hq=7), 1), (dict(Hkv=0), 1),
+    (dict(scale=float("inf")), 1), (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(window=5, causal=0), 1), (dict(part=-2), 1),
+    (dict(part=100), 1), (dict(out=None), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(q_start=None), 1),
+    (dict(k_start=None), 1), (dict(q=2 * A + 8), 1), (dict(qs=1020), 1), (dict(qs=1028), 1), (dict(ks=255), 1),
+    (dict(vs=1 << 38), 1), (dict(out=A + 4), 1), (dict(q_start=5 * A + 2), 1), (dict(out=2 * A), 1), (dict(out=3 * A - 16), 1),
+    (dict(out=4 * A + 2048), 1), (dict(part=128, mk=1000, ws=None, wsb=0), 3), (dict(part=128, mk=1000, wsb=1000), 3),
+    (dict(part=128, mk=1000, ws=7 * A + 8), 1)])
+def test_prompt(kw, status):
+    assert _prompt(**kw) == status
+
+
+def test_prompt_workspace():
+    f = pkv.prompt_workspace_size
+    assert f(2, 100, 60, 60, 8, 2, 128) == 256                           # a few stages are not split
+    units = 9 * 12 * 8                                                   # 9 queries, 12 heads, 1,000 keys in 128s
+    assert 256 + units * 130 * 4 <= f(2, 9, 5, 1000, 12, 2, 128, partition_size=128) < 256 + units * 130 * 4 + 1024
+    assert f(2, 9, 5, 32768, 12, 2, 128) > 256                           # few rows over many keys
+    assert f(2, 9, 5, 32768, 12, 2, 128, window=100, num_sinks=2) == 256
+    assert f(2, 9, 5, 32768, 12, 2, 96) == 0 and f(2, 9, 5, 32768, 12, 5, 128) == 0 and f(2, 9, 5, 100, 12, 2, 128, -1) == 0
+    assert f(2, 9, 5, 1000, 12, 2, 128, partition_size=64) == 0
+
+
+def test_prompt_binding():
+    q, k = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    qs = torch.tensor([0, 4], dtype=torch.int32)
+    for args, kw in [((q, q, k, k.float(), qs, 4, 1.0), {}), ((q, q, k, k[:3], qs, 4, 1.0), {}), ((q[:2], q, k, k, qs, 4, 1.0), {}),
+                     ((q, q, k, k, qs.long(), 4, 1.0), {}), ((q, q, k, k, qs, 4, 1.0), dict(key_start=qs[:1]))]:
+        with pytest.raises(ValueError):
+            pkv.prompt_attention(*args, workspace=q, **kw)
