@@ -15,16 +15,15 @@
 // queries of one head each (two heads of a K/V head, or two query blocks of
 // one) over the same keys, so each K/V stage is read once for both; one
 // persistent block per SM.  Roles:
-//   warps 0-15  softmax: 8 warps a tile, two threads per row (TMEM lane), each
-//               64 of a stage's 128 columns.  P = 2^(x - m) in bf16 goes over
-//               the first half of the thread's own columns of S.  The two
-//               threads of a row exchange their maxima through shared memory.
-//   warp 16     claims units, K tiles by TMA into a ring
-//   warp 17     one thread issues the products:
+//   warps 0-3   softmax of tile 0, warps 4-7 of tile 1, one thread per row (TMEM
+//               lane): P = 2^(x - m) in bf16 goes over the first half of S's
+//               columns
+//   warp 8      claims units, K tiles by TMA into a ring
+//   warp 9      one thread issues the products:
 //                 S_t = Q_t . K_j^T       M 128, N 128, K d
 //                 O_t (+)= P_t . V_j      M 128, N d, K 128 (P_t in TMEM)
-//   warp 18     Q tiles by TMA
-//   warp 19     V tiles by TMA; zeroes the rows of a sequence's last tile that
+//   warp 10     Q tiles by TMA
+//   warp 11     V tiles by TMA; zeroes the rows of a sequence's last tile that
 //               are other sequences' (0 times what they hold may be NaN)
 // A row's reference maximum m moves only when a stage's maximum exceeds it by
 // more than 2^8; O is then rescaled in TMEM.  Every exponent stays <= 2^8 and O
@@ -55,8 +54,8 @@ using namespace tc;
 
 constexpr int kTok = kPromptStage;    // key tokens per stage
 constexpr int kRows = kPromptStage;   // queries per tile
-constexpr int kSoftWarps = 16, kThreads = 640;
-constexpr int kKWarp = 16, kMmaWarp = 17, kQWarp = 18, kVWarp = 19;
+constexpr int kSoftWarps = 8, kThreads = 384;
+constexpr int kKWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 11;
 constexpr float kRescaleLog2 = 8.f;
 constexpr long long kWaitLimit = 4000000000LL;    // ~2 s: a barrier that never completes
 constexpr uint32_t kTmemCols = 512;               // O_0, O_1, S_0, S_1
@@ -64,7 +63,7 @@ __host__ __device__ constexpr uint32_t tmem_o(int t) { return 128u * t; }
 __host__ __device__ constexpr uint32_t tmem_s(int t) { return 256u + 128u * t; }
 // Registers: launched with kThreads x kLaunchRegs; the softmax warps raise
 // theirs, the others lower theirs, within the launch's total.
-constexpr int kLaunchRegs = 96, kSoftRegs = 104, kOtherRegs = 64;
+constexpr int kLaunchRegs = 168, kSoftRegs = 200, kOtherRegs = 104;
 static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 
 // control block, in front of the tiles (byte offsets)
@@ -73,7 +72,7 @@ constexpr uint32_t kKEmpty = 32;       // [4]
 constexpr uint32_t kVFull = 64;        // [4]
 constexpr uint32_t kVEmpty = 96;       // [4]
 constexpr uint32_t kSFull = 128;       // [2 tiles]: S_t of the tile's stage done
-constexpr uint32_t kPFull = 144;       // [2 tiles]: P_t written (8 warps)
+constexpr uint32_t kPFull = 144;       // [2 tiles]: P_t written (4 warps)
 constexpr uint32_t kPVDone = 160;      // [2 tiles]: P_t . V done
 constexpr uint32_t kQFull = 176;       // [2 tiles]
 constexpr uint32_t kQEmpty = 192;      // [2 tiles]
@@ -81,9 +80,9 @@ constexpr uint32_t kUFull = 208;       // [2]: unit records
 constexpr uint32_t kUEmpty = 224;      // [2]
 constexpr uint32_t kTail = 240;        // the V tile whose rows are to be zeroed has landed
 constexpr uint32_t kFin = 248;
-constexpr uint32_t kPair = 256;        // [8]: the two warps of 32 rows
-constexpr uint32_t kTmemSlot = 320, kAbort = 324, kRing = 336 /* [2][4] int4 */, kExch = 512 /* [2][2][128] floats */;
-constexpr uint32_t kCtlBytes = kExch + 2048;
+constexpr uint32_t kPFull2 = 256;      // [2 tiles]: ... of the second half of the keys
+constexpr uint32_t kTmemSlot = 272, kAbort = 276, kRing = 288 /* [2][4] int4 */;
+constexpr uint32_t kCtlBytes = kRing + 128;
 
 template <int D>
 struct Cfg {
@@ -98,6 +97,29 @@ struct Cfg {
     static constexpr int kSmemBytes = ((int)kCtlBytes + 1023) / 1024 * 1024 + kTileBytes;
     static_assert(kSmemBytes <= 232448, "shared memory per block");
 };
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// true in one thread of the (converged) warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+    return is != 0;
+}
 
 // D[tmem] (+)= A[tmem] . B[smem]
 __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -171,7 +193,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + kAbort);
     int4* ring = reinterpret_cast<int4*>(smem_raw + kRing);              // [2 units][4]
-    float* exch = reinterpret_cast<float*>(smem_raw + kExch);            // [tile][half][row]
     auto ktile = [&](uint32_t j) { return base + (j % NK) * C::kItemBytes; };
     auto vtile = [&](uint32_t j) { return base + C::kVOff + (j % NV) * C::kItemBytes; };
     auto qbuf = [&](int t) { return base + C::kQOff + t * C::kItemBytes; };
@@ -188,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(kSFull, t), 1);
             mbar_init(bar(kPFull, t), kSoftWarps / 2);
+            mbar_init(bar(kPFull2, t), kSoftWarps / 2);
             mbar_init(bar(kPVDone, t), 1);
             mbar_init(bar(kQFull, t), 1);
             mbar_init(bar(kQEmpty, t), 1);
@@ -196,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(bar(kTail, 0), 1);
         mbar_init(bar(kFin, 0), 1);
-        for (int i = 0; i < 8; ++i) mbar_init(bar(kPair, i), 2);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -436,108 +457,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         // ----------------------------------------------------------- products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (lane == 0) {
-            constexpr uint32_t idS = umma::idesc_bf16_f32(kRows, kTok, false);
-            constexpr uint32_t idPV = umma::idesc_bf16_f32(kRows, D, true);
-            uint32_t g = 0, un = 0, gt[2] = {0u, 0u}, qu[2] = {0u, 0u};
-            bool ok = true;
-            auto issue_s = [&](int t, uint32_t gs) {
-                const uint32_t kb = ktile(gs);
+        // The whole warp walks the loop and one elected thread issues: the
+        // operands are then uniform, and a product takes its 64 clocks.  Issued
+        // by `if (lane == 0)` every operand goes through a vector register, and
+        // a product took 123-147 clocks to issue.
+        constexpr uint32_t idS = umma::idesc_bf16_f32(kRows, kTok, false);
+        constexpr uint32_t idPV = umma::idesc_bf16_f32(kRows, D, true);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // descriptors of the first K step of slot 0; a slot or K step on adds to the address, in 16 bytes
+        const uint64_t q_desc = umma::desc_sw128(qbuf(0), 16, 1024), k_desc = umma::desc_sw128(base, 16, 1024);
+        const uint64_t v_desc = umma::desc_sw128(base + C::kVOff, kTok * 128, 1024);
+        uint32_t g = 0, un = 0, gt[2] = {0u, 0u}, qu[2] = {0u, 0u};
+        bool ok = true;
+        // waits of the whole warp
+        auto all = [&](uint32_t b, uint32_t parity) -> bool { return !__any_sync(0xffffffffu, !wait(b, parity, true)); };
+        auto issue_s = [&](int t, uint32_t gs, bool last) {
+            const uint64_t kd = k_desc + (gs % NK) * (C::kItemBytes / 16), qd = q_desc + t * (C::kItemBytes / 16);
+            umma::fence_after_sync();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
-                    umma::mma_bf16(tmem + tmem_s(t), umma::desc_sw128(qbuf(t) + off, 16, 1024),
-                                   umma::desc_sw128(kb + off, 16, 1024), idS, kk > 0);
+                    const uint32_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) / 16;
+                    umma::mma_bf16(tm + tmem_s(t), qd + off, kd + off, idS, kk > 0);
                 }
                 umma::commit(bar(kSFull, t));
-            };
-            auto issue_pv = [&](int t, uint32_t gs, bool first) {
-                const uint32_t vb = vtile(gs);
+                if (last) umma::commit(bar(kQEmpty, t));
+            }
+            __syncwarp();
+        };
+        // half of a stage's keys
+        auto issue_pv = [&](int t, uint32_t gs, int half, bool first) {
+            const uint64_t vd = v_desc + (gs % NV) * (C::kItemBytes / 16) + half * (kTok / 2 * 128 / 16);
+            umma::fence_after_sync();
+            if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kTok / 16; ++kk)
-                    mma_ts(tmem + tmem_o(t), tmem + tmem_s(t) + (kk >> 2) * 64 + (kk & 3) * 8,
-                           umma::desc_sw128(vb + kk * 2048, kTok * 128, 1024), idPV, !(first && kk == 0));
-                umma::commit(bar(kPVDone, t));
-            };
-            for (;;) {
-                const int slot = un & 1;
-                if (!wait(bar(kUFull, slot), (un >> 1) & 1, true)) break;
-                const int4 e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
-                umma::mbar_arrive(bar(kUEmpty, slot));
-                if (e1.x < 0) break;
-                const int c[2] = {e2.z, e2.w}, n = max(c[0], c[1]);
-                if (n > 0) {
-                    ok = wait(bar(kKFull, g % NK), (g / NK) & 1, true);
+                for (int kk = 0; kk < kTok / 32; ++kk)
+                    mma_ts(tm + tmem_o(t), tm + tmem_s(t) + half * (kTok / 4) + kk * 8, vd + kk * (2048 / 16), idPV,
+                           !(first && kk == 0));
+                if (half) umma::commit(bar(kPVDone, t));
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t b) {                  // a slot, once what was issued before has read it
+            if (elect_one()) umma::commit(b);
+            __syncwarp();
+        };
+        for (;;) {
+            const int slot = un & 1;
+            if (!all(bar(kUFull, slot), (un >> 1) & 1)) break;
+            const int kvh = __shfl_sync(0xffffffffu, ring[4 * slot + 1].x, 0);
+            const int c[2] = {__shfl_sync(0xffffffffu, ring[4 * slot + 2].z, 0),
+                              __shfl_sync(0xffffffffu, ring[4 * slot + 2].w, 0)};
+            const int n = max(c[0], c[1]);
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (kvh < 0) break;
+            if (n > 0) {
+                ok = all(bar(kKFull, g % NK), (g / NK) & 1);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (c[t] == 0 || !ok) continue;
-                        ok = wait(bar(kQFull, t), qu[t] & 1, true);
-                        // the tile's last P . V has read the buffer
-                        if (ok && gt[t] > 0) ok = wait(bar(kPVDone, t), (gt[t] - 1) & 1, true);
-                        if (!ok) break;
-                        umma::fence_after_sync();
-                        issue_s(t, g);
-                        if (c[t] == 1) umma::commit(bar(kQEmpty, t));
-                    }
-                    if (!ok) break;
-                    umma::commit(bar(kKEmpty, g % NK));
-                }
-                for (int j = 0; j < n && ok; ++j, ++g) {
-                    ok = wait(bar(kVFull, g % NV), (g / NV) & 1, true);
-                    bool next_k = false;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (j >= c[t] || !ok) continue;
-                        ok = wait(bar(kPFull, t), gt[t] & 1, true);
-                        if (!ok) break;
-                        umma::fence_after_sync();
-                        issue_pv(t, g, j == 0);
-                        if (j + 1 < c[t]) {
-                            // the next S_t overwrites P_t: only after P_t . V_j is done
-                            if (!next_k) ok = wait(bar(kKFull, (g + 1) % NK), ((g + 1) / NK) & 1, true);
-                            next_k = true;
-                            ok = ok && wait(bar(kPVDone, t), gt[t] & 1, true);
-                            if (!ok) break;
-                            umma::fence_after_sync();
-                            issue_s(t, g + 1);
-                            if (j + 2 == c[t]) umma::commit(bar(kQEmpty, t));
-                        }
-                        ++gt[t];
-                    }
-                    if (!ok) break;
-                    umma::commit(bar(kVEmpty, g % NV));
-                    if (j + 1 < n) umma::commit(bar(kKEmpty, (g + 1) % NK));
+                for (int t = 0; t < 2; ++t) {
+                    if (c[t] == 0 || !ok) continue;
+                    ok = all(bar(kQFull, t), qu[t] & 1);
+                    // the tile's last P . V has read the buffer
+                    if (ok && gt[t] > 0) ok = all(bar(kPVDone, t), (gt[t] - 1) & 1);
+                    if (ok) issue_s(t, g, c[t] == 1);
                 }
                 if (!ok) break;
-                for (int t = 0; t < 2; ++t) qu[t] += c[t] > 0;
-                ++un;
+                release(bar(kKEmpty, g % NK));
             }
-            // every product issued here completes before the block releases TMEM
-            umma::commit(bar(kFin, 0));
-            wait(bar(kFin, 0), 0, false);
+            for (int j = 0; j < n && ok; ++j, ++g) {
+                ok = all(bar(kVFull, g % NV), (g / NV) & 1);
+                bool next_k = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= c[t] || !ok) continue;
+                    ok = all(bar(kPFull, t), gt[t] & 1);
+                    if (!ok) break;
+                    issue_pv(t, g, 0, j == 0);
+                    ok = all(bar(kPFull2, t), gt[t] & 1);
+                    if (!ok) break;
+                    issue_pv(t, g, 1, false);
+                    if (j + 1 < c[t]) {
+                        // the next S_t overwrites P_t: only after P_t . V_j is done
+                        if (!next_k) ok = all(bar(kKFull, (g + 1) % NK), ((g + 1) / NK) & 1);
+                        next_k = true;
+                        ok = ok && all(bar(kPVDone, t), gt[t] & 1);
+                        if (!ok) break;
+                        issue_s(t, g + 1, j + 2 == c[t]);
+                    }
+                    ++gt[t];
+                }
+                if (!ok) break;
+                release(bar(kVEmpty, g % NV));
+                if (j + 1 < n) release(bar(kKEmpty, (g + 1) % NK));
+            }
+            if (!ok) break;
+            for (int t = 0; t < 2; ++t) qu[t] += c[t] > 0;
+            ++un;
         }
+        // every product issued here completes before the block releases TMEM
+        release(bar(kFin, 0));
+        wait(bar(kFin, 0), 0, false);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int t = warp >> 3, half = (warp >> 2) & 1;     // tile, half of the columns
+        const int t = warp >> 2;                              // tile
         const int i = (warp & 3) * 32 + lane;                // row of the tile, TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_col = tmem + lane_base + tmem_s(t) + 64 * half;
-        const uint32_t o_col = tmem + lane_base + tmem_o(t) + D / 2 * half;
-        const uint32_t pair = bar(kPair, t * 4 + (warp & 3));
-        float* here = exch + (t * 2 + half) * kRows + i;
-        const float* there = exch + (t * 2 + (half ^ 1)) * kRows + i;
-        uint32_t gt = 0, un = 0, met = 0;
+        const uint32_t s_col = tmem + lane_base + tmem_s(t);
+        const uint32_t o_col = tmem + lane_base + tmem_o(t);
+        uint32_t gt = 0, un = 0;
         bool ok = true, bad = false;
-        // both warps of 32 rows are here; what each wrote before is visible to the other
-        auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(pair);
-            const bool all = wait(pair, met & 1, true);
-            ++met;
-            return !__any_sync(0xffffffffu, !all);
-        };
         for (;;) {
             const int slot = un & 1;
             ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
@@ -565,24 +596,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 umma::fence_after_sync();
-                uint32_t sr[2][32];
-                umma::tmem_ld32(s_col, sr[0]);
-                umma::tmem_ld32(s_col + 32, sr[1]);
+                uint32_t sr[kTok / 32][32];
+#pragma unroll
+                for (int w = 0; w < kTok / 32; ++w) umma::tmem_ld32(s_col + 32 * w, sr[w]);
                 umma::tmem_wait_ld();
                 const int key = stage_key(e1.w + j, e2.x, e2.y);
                 const bool whole = key + kTok - 1 <= min(first, kl - 1) &&
                                    (p.window == 0 || key + kTok <= p.sinks || key > far - p.window);
                 if (flip) {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w)
+                    for (int w = 0; w < kTok / 32; ++w)
 #pragma unroll
                         for (int b = 0; b < 32; ++b) sr[w][b] = __float_as_uint(__uint_as_float(sr[w][b]) * p.scale_log2);
                 }
                 if (!whole) {
                     // -inf where this row does not see the key
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const int v0 = key + 64 * half + 32 * w;
+                    for (int w = 0; w < kTok / 32; ++w) {
+                        const int v0 = key + 32 * w;
                         uint32_t seen = bits_below(min(pos, kl - 1) + 1 - v0);
                         if (p.window > 0) seen &= ~bits_between(v0, p.sinks, pos - p.window + 1);
                         if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
@@ -596,15 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(sr[0][k]);
 #pragma unroll
-                for (int b = 8; b < 64; ++b) mx8[b & 7] = fmaxf(mx8[b & 7], __uint_as_float(sr[b >> 5][b & 31]));
-                const float own = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                        fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scl;
-                *here = own;
-                if (!meet()) {
-                    bad = true;
-                    break;
-                }
-                const float mx = fmaxf(own, *there);
+                for (int b = 8; b < kTok; ++b) mx8[b & 7] = fmaxf(mx8[b & 7], __uint_as_float(sr[b >> 5][b & 31]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scl;
                 float alpha = 1.f;
                 bool resc = false;
                 if (j == 0) {
@@ -620,38 +645,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mb = m_ref == -CUDART_INF_F ? 0.f : m_ref;
                 const uint64_t xs2 = umma::f2_pack(scl, scl), nmb2 = umma::f2_pack(-mb, -mb);
                 uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-                uint32_t pw[32];
+                if (__any_sync(0xffffffffu, resc)) {
+                    // O_t holds the products up to the previous stage
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_col + c0, ov);
+                        umma::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const uint64_t s01 = umma::f2_pack(__uint_as_float(sr[k >> 4][(2 * k) & 31]),
-                                                       __uint_as_float(sr[k >> 4][(2 * k + 1) & 31]));
-                    float x0, x1;
-                    umma::f2_unpack(umma::f2_fma(s01, xs2, nmb2), x0, x1);
-                    const float a0 = fast_exp2(x0), a1 = fast_exp2(x1);
-                    ls2[k & 3] = umma::f2_add(ls2[k & 3], umma::f2_pack(a0, a1));
-                    pw[k] = pack2<false>(a0, a1);
+                        for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                        tmem_st16(o_col + c0, ov);
+                    }
                 }
-                umma::tmem_st32(s_col, pw);
+                // P in two halves: the product with the first 64 keys runs while the others are weighed
+#pragma unroll
+                for (int w = 0; w < kTok / 32; ++w) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint64_t s01 = umma::f2_pack(__uint_as_float(sr[w][2 * k]), __uint_as_float(sr[w][2 * k + 1]));
+                        float x0, x1;
+                        umma::f2_unpack(umma::f2_fma(s01, xs2, nmb2), x0, x1);
+                        const float a0 = fast_exp2(x0), a1 = fast_exp2(x1);
+                        ls2[k & 3] = umma::f2_add(ls2[k & 3], umma::f2_pack(a0, a1));
+                        pw[k] = pack2<false>(a0, a1);
+                    }
+                    tmem_st16(s_col + 16 * w, pw);
+                    if (w & 1) {
+                        umma::tmem_wait_st();
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(bar(w == 1 ? kPFull : kPFull2, t));
+                    }
+                }
                 float ls[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) umma::f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
                 l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-                if (__any_sync(0xffffffffu, resc)) {
-                    // O_t holds the products up to the previous stage; each of a row's threads scales its half
-#pragma unroll
-                    for (int c0 = 0; c0 < D / 64; ++c0) {
-                        uint32_t ov[32];
-                        umma::tmem_ld32(o_col + 32 * c0, ov);
-                        umma::tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-                        umma::tmem_st32(o_col + 32 * c0, ov);
-                    }
-                }
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) umma::mbar_arrive(bar(kPFull, t));
             }
             if (bad) break;
 
@@ -660,17 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait(bar(kPVDone, t), (gt - 1) & 1, true);
                 if (__any_sync(0xffffffffu, !ok)) break;
                 umma::fence_after_sync();
-                // the row's sum is its two threads'; the partner has read the last maximum (it wrote P since)
-                *here = l;
-                if (!meet()) break;
-                l += *there;
-                if (!meet()) break;                              // before the next unit's maxima overwrite the sums
             }
             const int np = e1.y;
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + head;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
-            for (int c0 = 0; c0 < D / 64; ++c0) {
+            for (int c0 = 0; c0 < D / 32; ++c0) {
                 uint32_t ov[32];
                 if (n > 0) {
                     umma::tmem_ld32(o_col + 32 * c0, ov);
@@ -681,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 32; ++k) ov[k] = 0u;
                 }
                 if (!rv) continue;
-                const int col = D / 2 * half + 32 * c0;
+                const int col = 32 * c0;
                 if (np == 1) {
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + hrow * D + col;
                     store_row32(dst, ov, f, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0);
@@ -690,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
                 }
             }
-            if (rv && np > 1 && half == 0) {
+            if (rv && np > 1) {
                 const size_t u = hrow * p.Pmax + e1.z;
                 p.part_ml[2 * u] = m_ref;
                 p.part_ml[2 * u + 1] = l;
