@@ -764,6 +764,46 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void
                                         int partition_size, void* workspace, size_t workspace_bytes,
                                         int32_t* err_word, pkv_stream_t stream);
 
+/*
+ * paged_attention_decode_shared -- pkv_paged_attention_decode of sequences in
+ * groups whose first blocks are the same physical blocks (one system prompt,
+ * several samples of a prompt, questions about one document).  The shared
+ * blocks are read once per group and not once per sequence; the result is the
+ * decode's, up to the order of its sums.
+ *
+ * Source: "vLLM 内部構造 (2) — PagedAttention", section "共有": many requests
+ * point at one set of physical blocks.
+ *
+ * Group i (of G) is the sequences group_start[i] .. group_start[i+1] (int32
+ * [G+1], device, rising); the first shared_lens[i] tokens (int32 [G], device;
+ * counted in whole blocks, the rest is each sequence's own) of all of them are
+ * read through the table of the first.  Sequences in no group, and groups
+ * that share 0 tokens, are decoded as they are.  max_shared_len (host) bounds
+ * every shared_lens[i], max_group_size the sequences of every group that
+ * shares a block; a group that breaks a bound is reported
+ * (PKV_DEVERR_QUERY_LEN) and decoded without sharing.  Groups that overlap
+ * give unspecified results.  A sequence shorter than its group's shared tokens
+ * sees its own length.  A block id outside [0, NB) is reported and its tokens
+ * are absent, as in the decode.
+ *
+ * partition_size: as in the decode, for the shared tokens (rounded up to 128)
+ * and the others alike.  `workspace` must hold
+ * pkv_decode_shared_workspace_size(...) bytes, its first 256 zero before first
+ * use (a smaller one: fewer partitions, as pkv_decode_window_workspace_size
+ * says).  Supported: bf16 query and cache; anything else returns
+ * PKV_ERR_UNSUPPORTED.
+ */
+PKV_API size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, int bs, int max_context_len,
+                                                int max_shared_len, int max_group_size, int partition_size);
+PKV_API pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_dtype q_dtype,
+                                                     const void* key_cache, const void* value_cache,
+                                                     pkv_dtype cache_dtype, const int32_t* block_tables, int MB,
+                                                     const int32_t* context_lens, const int32_t* group_start,
+                                                     const int32_t* shared_lens, int S, int G, int max_context_len,
+                                                     int max_shared_len, int max_group_size, int Hq, int Hkv, int d,
+                                                     int bs, int NB, float scale, int partition_size, void* workspace,
+                                                     size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * The calls of the four sections above with their arguments in one array,
  * for callers whose foreign-function interface pays per argument (the Python
@@ -782,7 +822,8 @@ typedef enum {
     PKV_CALL_DECODE_SCORED = 5,    /* pkv_token_attention_decode_scored */
     PKV_CALL_EVICT = 6,            /* pkv_evict_tokens */
     PKV_CALL_ROTARY_WRITE = 7,     /* pkv_rotary_kv_write */
-    PKV_CALL_PROMPT = 8            /* pkv_prompt_attention */
+    PKV_CALL_PROMPT = 8,           /* pkv_prompt_attention */
+    PKV_CALL_DECODE_SHARED = 9     /* pkv_paged_attention_decode_shared */
 } pkv_call;
 PKV_API pkv_status pkv_invoke(int call, const void* words);
 

@@ -59,7 +59,8 @@ EXPORTED = ("pkv_paged_kv_write", "pkv_decode_workspace_size", "pkv_decode_parti
             "pkv_prefill_window_workspace_size", "pkv_paged_attention_prefill_window", "pkv_kv4_block_bytes",
             "pkv_paged_kv4_write", "pkv_paged_kv4_read", "pkv_paged_attention_decode_kv4",
             "pkv_token_attention_scored_workspace_size", "pkv_token_attention_decode_scored", "pkv_evict_tokens",
-            "pkv_rotary_kv_write", "pkv_prompt_workspace_size", "pkv_prompt_attention", "pkv_invoke")
+            "pkv_rotary_kv_write", "pkv_prompt_workspace_size", "pkv_prompt_attention",
+            "pkv_decode_shared_workspace_size", "pkv_paged_attention_decode_shared", "pkv_invoke")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -170,6 +171,11 @@ def _load() -> ctypes.CDLL:
     lib.pkv_prompt_attention.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, vp, vp] + [i32] * 8 + \
         [f32, i32, i32, i32, i32, vp, sz, vp, vp]
     lib.pkv_prompt_attention.restype = i32
+    lib.pkv_decode_shared_workspace_size.argtypes = [i32] * 10
+    lib.pkv_decode_shared_workspace_size.restype = sz
+    lib.pkv_paged_attention_decode_shared.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, vp, vp, vp] + [i32] * 10 + \
+        [f32, i32, vp, sz, vp, vp]
+    lib.pkv_paged_attention_decode_shared.restype = i32
     lib.pkv_invoke.argtypes = [i32, ctypes.c_char_p]
     lib.pkv_invoke.restype = i32
     lib.pkv_status_string.argtypes = [i32]
@@ -516,6 +522,7 @@ _decode_scored = _packed(5, "pkv_token_attention_decode_scored")
 _evict = _packed(6, "pkv_evict_tokens")
 _rotary_write = _packed(7, "pkv_rotary_kv_write")
 _prompt = _packed(8, "pkv_prompt_attention")
+_decode_shared = _packed(9, "pkv_paged_attention_decode_shared")
 
 
 # ---- sliding window with sinks
@@ -885,6 +892,55 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
         p_o, p_q, p_k, p_v, dtype_code(dt), _row_stride(query), _row_stride(key), _row_stride(value), p_qs, p_ks, S, Tq,
         Tk, max_query_len, max_key_len, Hq, Hkv, d, scale, int(causal), window, num_sinks, partition_size, p_ws,
         workspace.nbytes, p_err, p_st)
+    return out
+
+
+# ---- decode of sequences that share blocks
+
+def shared_workspace_size(S: int, G: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, max_shared_len: int,
+                          max_group_size: int, partition_size: int = 0) -> int:
+    return int(lib.pkv_decode_shared_workspace_size(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len,
+                                                    max_group_size, partition_size))
+
+
+def make_shared_workspace(S: int, G: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, max_shared_len: int,
+                          max_group_size: int, partition_size: int = 0, device=None) -> torch.Tensor:
+    """A workspace for paged_attention_decode_shared, its header zero (reused
+    as make_window_workspace says)."""
+    n = shared_workspace_size(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    ws[:256] = 0
+    return ws
+
+
+def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                  value_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  group_start: torch.Tensor, shared_lens: torch.Tensor, max_context_len: int,
+                                  max_shared_len: int, max_group_size: int, scale: float, partition_size: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
+                                  stream=None) -> torch.Tensor:
+    """paged_attention_decode (bf16) of sequences in groups whose first blocks
+    are the same: group i is the sequences group_start[i] .. group_start[i+1]
+    (int32 [G+1]), and their first shared_lens[i] tokens (int32 [G], whole
+    blocks) are read once, through the first one's table.  max_shared_len and
+    max_group_size (host) bound them."""
+    S, Hq, d = shape = query.shape
+    NB, bs, Hkv, d2 = pool = key_cache.shape
+    q_dt, c_dt, G = query.dtype, key_cache.dtype, shared_lens.numel()
+    if d2 != d or out.shape != shape or out.dtype != q_dt or value_cache.shape != pool or value_cache.dtype != c_dt:
+        raise ValueError("shape or dtype mismatch")
+    MB = _check_tables(block_tables, context_lens, S)
+    if group_start.dtype != torch.int32 or shared_lens.dtype != torch.int32 or group_start.numel() != G + 1:
+        raise ValueError("group_start must be int32 [G + 1] and shared_lens int32 [G]")
+    if workspace is None:
+        workspace = _own_workspace(stream, make_shared_workspace, S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len,
+                                   max_group_size, partition_size, device=query.device)
+    p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_gs, p_sl, p_ws, p_err, p_st = _pointers(
+        stream, out, query, key_cache, value_cache, block_tables, context_lens, group_start, shared_lens, workspace,
+        err_word)
+    _decode_shared(
+        p_o, p_q, dtype_code(q_dt), p_kc, p_vc, dtype_code(c_dt), p_bt, MB, p_cl, p_gs, p_sl, S, G, max_context_len,
+        max_shared_len, max_group_size, Hq, Hkv, d, bs, NB, scale, partition_size, p_ws, workspace.nbytes, p_err, p_st)
     return out
 
 

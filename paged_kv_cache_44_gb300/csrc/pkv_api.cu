@@ -1039,6 +1039,161 @@ pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, c
     return from_cuda(launch_prompt(p, d, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace pkv {
+namespace {
+
+// Partitions of a shared decode: of the shared tokens Pre (stages of 128; 0:
+// not split), of a sequence's own tokens P, and where each row's partial
+// results and the sequences' shared lengths lie.
+struct SharedPlan {
+    int pre, first_own;                   // partial results of the shared tokens come first
+    DecodePlan own;
+    int Pmax;
+    size_t ml_offset, acc_offset, begin_offset, bytes;
+};
+SharedPlan plan_shared(int S, int Hq, int d, int max_ctx, int max_shared, int pre, int P) {
+    SharedPlan sp{};
+    const int stages = (max_shared + kPromptStage - 1) / kPromptStage;
+    sp.pre = pre;
+    sp.first_own = pre > 0 ? (stages + pre - 1) / pre : 1;
+    sp.own = make_plan(S, Hq, d, max_ctx, P);
+    sp.Pmax = sp.first_own + sp.own.Pmax_plain;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t units = (size_t)S * Hq * sp.Pmax;
+    sp.ml_offset = kWorkspaceHeaderBytes;
+    sp.acc_offset = up(sp.ml_offset + units * 2 * sizeof(float));
+    sp.begin_offset = up(sp.acc_offset + units * d * sizeof(float));
+    sp.bytes = up(sp.begin_offset + (size_t)S * sizeof(int32_t));
+    return sp;
+}
+
+// Stages per partition of the shared tokens: the number of equal partitions
+// with the least rounds of units, a unit's fixed cost counted as 3 stages.
+int resolve_shared_prefix(int G, int max_group, int g, int Hkv, int max_shared, int req) {
+    const int stages = (max_shared + kPromptStage - 1) / kPromptStage;
+    if (req == -1) return 0;
+    if (req > 0) {
+        const int p = (req + kPromptStage - 1) / kPromptStage;
+        return p < stages ? p : 0;
+    }
+    const long long tiles = ((long long)max_group * g + kPromptStage - 1) / kPromptStage, units = G * Hkv * ((tiles + 1) / 2);
+    long long best = 0;
+    int best_p = 0;
+    for (int np = 1; np <= 64 && np <= stages; ++np) {
+        const int p = (stages + np - 1) / np, n = (stages + p - 1) / p;
+        const long long cost = (units * n + 151) / 152 * (p + 3) * 16 + n;
+        if (np == 1 || cost < best) {
+            best = cost;
+            best_p = n > 1 ? p : 0;
+        }
+    }
+    return best_p;
+}
+
+bool shared_shape_ok(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, int max_shared, int max_group, int req) {
+    return decode_shape_ok(S, Hq, Hkv, d, bs, max_ctx) && G >= 0 && max_shared >= 0 && max_shared <= max_ctx && max_group >= 0 &&
+           max_group <= 65535 && req >= -1 && (req <= 0 || req % bs == 0);
+}
+
+// Whether the shared tokens are worth a launch of their own.
+bool shares_enough(int G, int max_shared, int max_group, int bs) { return G > 0 && max_shared >= bs && max_group > 1; }
+
+SharedPlan choose_shared(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, int max_shared, int max_group, int req,
+                         size_t room) {
+    int P = resolve_partition(S, Hq, Hkv, d, bs, max_ctx, req);
+    int pre = resolve_shared_prefix(G, max_group, Hq / Hkv, Hkv, max_shared, req);
+    SharedPlan sp = plan_shared(S, Hq, d, max_ctx, max_shared, pre, P);
+    // a smaller workspace: fewer partitions
+    while (req == 0 && sp.bytes > room && (P > 0 || pre > 0)) {
+        P = P > 0 && 2 * P < max_ctx ? 2 * P : 0;
+        pre = pre > 0 && 2 * pre * kPromptStage < max_shared ? 2 * pre : 0;
+        sp = plan_shared(S, Hq, d, max_ctx, max_shared, pre, P);
+    }
+    return sp;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, int bs, int max_context_len,
+                                        int max_shared_len, int max_group_size, int partition_size) {
+    if (!shared_shape_ok(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size)) return 0;
+    const size_t plain = make_plan(S, Hq, d, max_context_len, resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size)).bytes;
+    if (!shares_enough(G, max_shared_len, max_group_size, bs)) return plain;
+    return max(plain, choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size,
+                                    SIZE_MAX).bytes);
+}
+
+pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_dtype q_dtype, const void* key_cache,
+                                             const void* value_cache, pkv_dtype cache_dtype, const int32_t* block_tables,
+                                             int MB, const int32_t* context_lens, const int32_t* group_start,
+                                             const int32_t* shared_lens, int S, int G, int max_context_len,
+                                             int max_shared_len, int max_group_size, int Hq, int Hkv, int d, int bs,
+                                             int NB, float scale, int partition_size, void* workspace,
+                                             size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream) {
+    if (G < 0 || max_shared_len < 0 || max_shared_len > max_context_len || max_group_size < 0) return PKV_ERR_INVALID_ARG;
+    if (q_dtype != PKV_BF16 || cache_dtype != PKV_BF16 || max_group_size > 65535 || G > 65535) return PKV_ERR_UNSUPPORTED;
+    const pkv_status chk = check_decode_args(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,
+                                             context_lens, S, max_context_len, Hq, Hkv, d, bs, NB, scale, 1.f, 1.f,
+                                             partition_size, PKV_DECODE_TENSOR_CORES);
+    if (chk != PKV_OK || S == 0) return chk;
+    if (G > 0 && (!group_start || !shared_lens)) return PKV_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(group_start) & 3u) || (reinterpret_cast<uintptr_t>(shared_lens) & 3u))
+        return PKV_ERR_INVALID_ARG;
+    const size_t room = workspace_room(workspace, workspace_bytes);
+    const bool shares = shares_enough(G, max_shared_len, max_group_size, bs);
+    SharedPlan sp{};
+    if (shares)
+        sp = choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size, room);
+    if (!shares || (partition_size == 0 && sp.bytes > room)) {
+        // nothing to share, or no room to: every sequence on its own
+        int P = resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size);
+        P = fit_partition(P, max_context_len, partition_size, room, [&](int n) { return make_plan(S, Hq, d, max_context_len, n).bytes; });
+        return pkv_paged_attention_decode_ex(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,
+                                             context_lens, S, max_context_len, Hq, Hkv, d, bs, NB, scale, 1.f, 1.f,
+                                             P > 0 ? P : -1, workspace, workspace_bytes, err_word, stream,
+                                             PKV_DECODE_TENSOR_CORES);
+    }
+    if (!workspace || workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    DecodeParams d_p{};
+    d_p.out = out; d_p.q = query; d_p.kc = key_cache; d_p.vc = value_cache;
+    d_p.block_tables = block_tables; d_p.context_lens = context_lens; d_p.err = err_word;
+    d_p.S = S; d_p.MB = MB; d_p.Hq = Hq; d_p.Hkv = Hkv; d_p.g = Hq / Hkv; d_p.d = d; d_p.bs = bs; d_p.NB = NB;
+    set_partitions(d_p, sp.own, sp.own.P, MB * bs, 0);
+    d_p.Pmax = sp.Pmax;
+    d_p.max_ctx = max_context_len;
+    d_p.logit_scale_log2 = scale * kLog2e;
+    d_p.out_scale = 1.f;
+    d_p.sched = reinterpret_cast<unsigned*>(ws);
+    // a row's own partial results lie behind those of its shared tokens
+    float* ml = reinterpret_cast<float*>(ws + sp.ml_offset);
+    float* acc = reinterpret_cast<float*>(ws + sp.acc_offset);
+    d_p.part_ml = ml + 2 * sp.first_own;
+    d_p.part_acc = acc + (size_t)sp.first_own * d;
+    d_p.begin = reinterpret_cast<int32_t*>(ws + sp.begin_offset);
+    PromptParams p{};
+    p.out = out; p.q = query; p.k = key_cache; p.v = value_cache;
+    p.query_start = group_start; p.key_start = shared_lens; p.part_ml = ml; p.part_acc = acc;
+    p.sched = d_p.sched; p.err = err_word;
+    p.S = G; p.Tq = S; p.max_q = max_group_size; p.max_k = max_shared_len; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv;
+    p.group = 1; p.P = sp.pre; p.Pmax = sp.Pmax;
+    p.scale_log2 = scale * kLog2e;
+    p.tables = block_tables; p.lens = context_lens; p.begin = reinterpret_cast<int32_t*>(ws + sp.begin_offset);
+    p.MB = MB; p.bs = bs; p.NB = NB;
+    const SharedParts parts{sp.first_own, d_p.P, d_p.Q, max_context_len};
+    auto st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_shared_prefix(p, d_p, num_sms_current(), st);
+    if (e == cudaSuccess) e = launch_decode_tc_suffix(d_p, q_dtype, cache_dtype, num_sms_current(), st);
+    if (e == cudaSuccess) e = launch_shared_merge(p, parts, d, st);
+    return from_cuda(e);
+}
+
 pkv_status pkv_rotary_kv_write(const void* query, const void* key, const void* value, pkv_dtype in_dtype,
                                int64_t q_stride, int64_t k_stride, int64_t v_stride, const int64_t* positions,
                                const float* cos_sin, int max_position, int rotary_dim, int interleaved, void* q_out,

@@ -1,0 +1,911 @@
+// Attention of many query rows over the same keys on the fifth-generation
+// tensor cores: whole packed prompts with K and V contiguous (pkv_prompt.cu),
+// and the shared blocks of a group of decoding sequences, read through a block
+// table (SHARED; pkv_shared.cu).
+//
+// "LLM推論の基礎とvLLMの内部", section 6: a step computes prompts next to
+// decodes; section 2: GQA lets several query heads share one K/V head.
+// Sequence s has queries query_start[s] .. query_start[s + 1] of q and keys
+// key_start[s] .. key_start[s + 1] of k and v; its last query sits at its last
+// key.  out = softmax(scale q k^T) v over the keys a query sees: all of them,
+// those up to its own position, or of these the first `sinks` and the last
+// `window`.
+//
+// Two products of 128 x 128 x d per 128 queries, 128 keys and head, and 16,384
+// exponentials between them: bound by the tensor cores, if the softmax of one
+// tile hides behind the products of another.  A work unit is two tiles of 128
+// queries of one head each (two heads of a K/V head, or two query blocks of
+// one) over the same keys, so each K/V stage is read once for both; one
+// persistent block per SM.  Roles:
+//   warps 0-3   softmax of tile 0, warps 4-7 of tile 1, one thread per row (TMEM
+//               lane): P = 2^(x - m) in bf16 goes over the first half of S's
+//               columns
+//   warp 8      claims units, K tiles by TMA into a ring
+//   warp 9      one thread issues the products:
+//                 S_t = Q_t . K_j^T       M 128, N 128, K d
+//                 O_t (+)= P_t . V_j      M 128, N d, K 128 (P_t in TMEM)
+//   warp 10     Q tiles by TMA
+//   warp 11     V tiles by TMA; zeroes the rows of a sequence's last tile that
+//               are other sequences' (0 times what they hold may be NaN)
+// A row's reference maximum m moves only when a stage's maximum exceeds it by
+// more than 2^8; O is then rescaled in TMEM.  Every exponent stays <= 2^8 and O
+// / l is the same softmax whatever m was.  P is rounded to bf16 (2^-9 of each
+// weight): the tensor cores take 16-bit operands; sums stay in fp32.
+//
+// Units are numbered longest first: query blocks from the last to the first
+// over all sequences, so the end of a launch is made of short ones.  A block
+// takes tickets from a counter and walks (block, 32 sequences at a time) to
+// the unit of its ticket, so ragged lengths cost no empty tickets.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include <mutex>
+
+#include "pkv_common.cuh"
+#include "pkv_internal.h"
+#include "pkv_qtile.cuh"
+#include "pkv_tc_common.cuh"
+#include "pkv_umma.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace tc;
+
+constexpr int kTok = kPromptStage;    // key tokens per stage
+constexpr int kRows = kPromptStage;   // queries per tile
+constexpr int kSoftWarps = 8, kThreads = 384;
+constexpr int kKWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 11;
+constexpr float kRescaleLog2 = 8.f;
+constexpr long long kWaitLimit = 4000000000LL;    // ~2 s: a barrier that never completes
+constexpr uint32_t kTmemCols = 512;               // O_0, O_1, S_0, S_1
+__host__ __device__ constexpr uint32_t tmem_o(int t) { return 128u * t; }
+__host__ __device__ constexpr uint32_t tmem_s(int t) { return 256u + 128u * t; }
+// Registers: launched with kThreads x kLaunchRegs; the softmax warps raise
+// theirs, the others lower theirs, within the launch's total.
+constexpr int kLaunchRegs = 168, kSoftRegs = 200, kOtherRegs = 104;
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+
+// control block, in front of the tiles (byte offsets)
+constexpr uint32_t kKFull = 0;         // [4]
+constexpr uint32_t kKEmpty = 32;       // [4]
+constexpr uint32_t kVFull = 64;        // [4]
+constexpr uint32_t kVEmpty = 96;       // [4]
+constexpr uint32_t kSFull = 128;       // [2 tiles]: S_t of the tile's stage done
+constexpr uint32_t kPFull = 144;       // [2 tiles]: P_t written (4 warps)
+constexpr uint32_t kPVDone = 160;      // [2 tiles]: P_t . V done
+constexpr uint32_t kQFull = 176;       // [2 tiles]
+constexpr uint32_t kQEmpty = 192;      // [2 tiles]
+constexpr uint32_t kUFull = 208;       // [2]: unit records
+constexpr uint32_t kUEmpty = 224;      // [2]
+constexpr uint32_t kTail = 240;        // the V tile whose rows are to be zeroed has landed
+constexpr uint32_t kFin = 248;
+constexpr uint32_t kPFull2 = 256;      // [2 tiles]: ... of the second half of the keys
+constexpr uint32_t kTmemSlot = 272, kAbort = 276, kRing = 288 /* [2][4] int4 */;
+constexpr uint32_t kMasks = kRing + 128 /* [8 stages][4 words] */, kCtlBytes = kMasks + 128;
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;                 // 128-byte halves of a row
+    static constexpr int kItemBytes = kTok * 2 * D;        // a K, V or Q tile
+    static constexpr int kKItems = D == 128 ? 3 : 4, kVItems = D == 128 ? 2 : 4;
+    static constexpr int kVOff = kKItems * kItemBytes;
+    static constexpr int kQOff = (kKItems + kVItems) * kItemBytes;
+    static constexpr int kTileBytes = kQOff + 2 * kItemBytes;
+    // the control block, up to the next 1,024 bytes (the dynamic shared memory starts on such a boundary;
+    // the kernel checks it)
+    static constexpr int kSmemBytes = ((int)kCtlBytes + 1023) / 1024 * 1024 + kTileBytes;
+    static_assert(kSmemBytes <= 232448, "shared memory per block");
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// true in one thread of the (converged) warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(is));
+    return is != 0;
+}
+
+// D[tmem] (+)= A[tmem] . B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
+}
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A sequence's rows; false when a bound is broken (it is skipped then).
+// SHARED: a group of sequences, its members q0 .. q0 + ql, whose first kl
+// tokens (whole blocks) are read through the table of the first of them.
+struct Seq {
+    int q0, ql, k0, kl;
+};
+template <bool SHARED>
+__device__ __forceinline__ bool sequence(const PromptParams& p, int s, Seq& x) {
+    if constexpr (SHARED) {
+        x.q0 = __ldg(p.query_start + s);
+        const long long members = (long long)__ldg(p.query_start + s + 1) - x.q0;
+        const int shared = __ldg(p.key_start + s);
+        x.ql = (int)members;
+        x.k0 = 0;
+        x.kl = shared / p.bs * p.bs;
+        const bool ok = x.q0 >= 0 && members >= 0 && x.q0 + members <= p.Tq && shared >= 0 && shared <= p.max_k &&
+                        (x.kl == 0 || members <= p.max_q);
+        if (!ok) x.kl = 0;
+        return ok;
+    }
+    x.q0 = __ldg(p.query_start + s);
+    x.k0 = __ldg(p.key_start + s);
+    const long long ql = (long long)__ldg(p.query_start + s + 1) - x.q0, kl = (long long)__ldg(p.key_start + s + 1) - x.k0;
+    x.ql = (int)ql;
+    x.kl = (int)kl;
+    return x.q0 >= 0 && x.k0 >= 0 && ql >= 0 && kl >= 0 && ql <= p.max_q && kl <= p.max_k && x.q0 + ql <= p.Tq &&
+           x.k0 + kl <= p.Tk;
+}
+
+// Query blocks come in groups of p.group (two where the heads per K/V head are
+// odd, so that tiles pair up).  The keys of a group's stages: the blocks of
+// 128 that hold sinks, then those from the first query's window on.
+struct Group {
+    int blocks, units, sinks, low, np;      // query blocks here; units per K/V head; key blocks; partitions
+};
+__device__ __forceinline__ int key_end(const PromptParams& p, const Seq& x, int block) {   // keys the block's queries see
+    if (!p.causal) return x.kl;
+    const int last = min(x.ql, (block + 1) * kRows);
+    return max(x.kl - x.ql + last, 0);
+}
+__device__ __forceinline__ int stages_to(const Group& g, int end) {
+    const int blocks = ceil_div(end, kTok);
+    return min(g.sinks, blocks) + max(0, blocks - max(g.low, g.sinks));
+}
+template <bool SHARED>
+__device__ __forceinline__ bool group_of(const PromptParams& p, const Seq& x, int level, Group& g) {
+    if constexpr (SHARED) {
+        // tiles of 128 (member, head) rows of a K/V head; one level holds them all
+        g.blocks = (int)(((long long)x.ql * p.g + kRows - 1) / kRows);
+        g.units = (g.blocks + 1) / 2;
+        g.sinks = g.low = 0;
+        const int n = ceil_div(x.kl, kTok);
+        g.np = p.P > 0 && n > p.P ? ceil_div(n, p.P) : 1;
+        return x.kl > 0 && g.blocks > 0;
+    }
+    const int nqb = ceil_div(x.ql, kRows);
+    g.blocks = min(p.group, nqb - level * p.group);
+    if (g.blocks <= 0) return false;
+    g.units = (p.g * g.blocks + 1) / 2;
+    g.sinks = 0;
+    g.low = 0;
+    if (p.window > 0) {
+        g.low = max(0, x.kl - x.ql + level * p.group * kRows - p.window + 1) / kTok;
+        g.sinks = min(ceil_div(p.sinks, kTok), g.low);
+    }
+    const int n = stages_to(g, key_end(p, x, level * p.group + g.blocks - 1));
+    g.np = p.P > 0 && n > p.P ? ceil_div(n, p.P) : 1;
+    return true;
+}
+
+// Tokens that sequence s shares with its group, by the bounds that attend_kernel keeps (0 for a group it skips).
+__device__ __forceinline__ int shared_tokens(const PromptParams& p, int s) {
+    int lo = 0, hi = p.S;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(p.query_start + mid) <= s) lo = mid; else hi = mid;
+    }
+    Seq x;
+    return p.S > 0 && sequence<true>(p, lo, x) && s >= x.q0 && s < x.q0 + x.ql ? x.kl : 0;
+}
+
+// A group's block ids, stage by stage: 32 entries of the table at a time, one
+// per lane, the next 32 on their way.
+struct BlockIds {
+    const int32_t* row;
+    int blocks, next, tab, tab_next;      // blocks of the group; the next stage's first
+    __device__ __forceinline__ int load(int at) const {
+        const int b = at + (int)(threadIdx.x & 31);
+        return b < blocks ? __ldg(row + b) : 0;
+    }
+    __device__ __forceinline__ void start(const PromptParams& p, int member, int n, int stage) {
+        row = p.tables + (size_t)member * p.MB;
+        blocks = n;
+        next = stage * (kTok / p.bs);
+        tab = load(next & ~31);
+        tab_next = load((next & ~31) + 32);
+    }
+    // lane i: block i of the stage's 8 or 4; -1 past the group's last, -2 out of the pool
+    __device__ __forceinline__ int stage(const PromptParams& p) {
+        const int n = kTok / p.bs, i = threadIdx.x & 31;
+        int pb = __shfl_sync(0xffffffffu, tab, (next + i) & 31);
+        if (i >= n || next + i >= blocks) pb = -1;
+        else if (pb < 0 || pb >= p.NB) pb = -2;
+        next += n;
+        if ((next & 31) == 0) {
+            tab = tab_next;
+            tab_next = load(next + 32);
+        }
+        return pb;
+    }
+};
+
+// The blocks of a stage into a tile: a box per block and 64 values, one lane each.
+template <int D>
+__device__ __forceinline__ void load_blocks(const PromptParams& p, const CUtensorMap* map, uint32_t tile, int kvh, int pb,
+                                            uint32_t there, uint32_t full) {
+    constexpr int H = D / 64;
+    const int lane = threadIdx.x & 31, b = lane / H, h = lane % H;
+    const int id = __shfl_sync(0xffffffffu, pb, b);
+    if (lane == 0) mbar_arrive_expect_tx(full, __popc(there) * (uint32_t)p.bs * 2 * D);
+    __syncwarp();
+    if (b < kTok / p.bs && id >= 0) tensor_load_2d(tile + h * (kTok * 128) + b * p.bs * 128, map, kvh * D + h * 64, id * p.bs, full);
+}
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<D>;
+    constexpr int NK = C::kKItems, NV = C::kVItems;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t ctl = smem_addr(smem_raw);
+    const uint32_t base = (ctl + kCtlBytes + 1023u) & ~1023u;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (base + C::kTileBytes > ctl + C::kSmemBytes) {        // not on the boundary the layout counts on
+        pdl_wait();
+        if (tid == 0) report(p.err, PKV_DEVERR_TIMEOUT);
+        return;
+    }
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + kAbort);
+    int4* ring = reinterpret_cast<int4*>(smem_raw + kRing);              // [2 units][4]
+    uint32_t* masks = reinterpret_cast<uint32_t*>(smem_raw + kMasks);    // SHARED: tokens there are, stage g in slot g % 8
+    auto ktile = [&](uint32_t j) { return base + (j % NK) * C::kItemBytes; };
+    auto vtile = [&](uint32_t j) { return base + C::kVOff + (j % NV) * C::kItemBytes; };
+    auto qbuf = [&](int t) { return base + C::kQOff + t * C::kItemBytes; };
+    auto bar = [&](uint32_t off, int i) { return ctl + off + 8 * i; };
+    pdl_trigger();
+
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(kKFull, i), 1);
+            mbar_init(bar(kKEmpty, i), 1);
+            mbar_init(bar(kVFull, i), 1);
+            mbar_init(bar(kVEmpty, i), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(kSFull, t), 1);
+            mbar_init(bar(kPFull, t), kSoftWarps / 2);
+            mbar_init(bar(kPFull2, t), kSoftWarps / 2);
+            mbar_init(bar(kPVDone, t), 1);
+            mbar_init(bar(kQFull, t), 1);
+            mbar_init(bar(kQEmpty, t), 1);
+            mbar_init(bar(kUFull, t), 1);
+            mbar_init(bar(kUEmpty, t), kSoftWarps + 3);
+        }
+        mbar_init(bar(kTail, 0), 1);
+        mbar_init(bar(kFin, 0), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) umma::tmem_alloc(ctl + kTmemSlot, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem_raw + kTmemSlot);
+    pdl_wait();
+
+    // bounded wait; false once the limit passes or another role gave up
+    auto wait = [&](uint32_t b, uint32_t parity, bool abortable) -> bool {
+        if (mbar_try_wait(b, parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(b, parity)) {
+            if (abortable && *abort_flag) return false;
+            if (clock64() - t0 > kWaitLimit) {
+                report(p.err, PKV_DEVERR_TIMEOUT);
+                *abort_flag = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+    if constexpr (SHARED) {
+        // where each sequence's own part begins, for the kernels behind this one
+        for (int s = blockIdx.x * kThreads + tid; s < p.Tq; s += gridDim.x * kThreads) p.begin[s] = shared_tokens(p, s);
+    }
+    // the first key of stage j of a unit's list
+    auto stage_key = [](int j, int sinks, int low) { return (j < sinks ? j : j - sinks + low) * kTok; };
+    // A parity wait is exact while the barrier is within one phase of the
+    // awaited one; every wait below is by construction.  K_j and V_j sit in
+    // slots j % NK, j % NV (j counted over the block's stages); the per-tile
+    // barriers count the stages that tile took part in.
+
+    if (warp == kKWarp) {
+        // ------------------------------------------------- units and K tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        // the highest query block group of any sequence
+        int level = 0;
+        for (int s = lane; s < p.S; s += 32) {
+            Seq x;
+            if (sequence<SHARED>(p, s, x)) level = max(level, SHARED ? 1 : ceil_div(x.ql, p.group * kRows));
+            else if (blockIdx.x == 0) report(p.err, PKV_DEVERR_QUERY_LEN);
+        }
+        level = __reduce_max_sync(0xffffffffu, level) - 1;
+        // this lane's sequence of the current 32, its group at this level, and the units up to its own
+        Seq x{};
+        Group gr{};
+        int at = -32;
+        long long before = 0, mine = 0, upto = 0, total = 0;
+        auto next_batch = [&]() -> bool {
+            before += total;
+            at += 32;
+            if (at >= p.S) {
+                at = 0;
+                --level;
+            }
+            if (level < 0) return false;
+            mine = 0;
+            if (at + lane < p.S && sequence<SHARED>(p, at + lane, x) && group_of<SHARED>(p, x, level, gr))
+                mine = (long long)p.Hkv * gr.np * gr.units;
+            upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            total = __shfl_sync(0xffffffffu, upto, 31);
+            return true;
+        };
+        long long ticket = blockIdx.x;
+        uint32_t g = 0, un = 0;
+        bool ok = true, bad = false, more = level >= 0 && next_batch();
+        for (;;) {
+            while (more && ticket >= before + total) more = next_batch();
+            const int slot = un & 1;
+            if (un >= 2) ok = wait(bar(kUEmpty, slot), ((un >> 1) - 1) & 1, true);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            if (!more) {
+                if (lane == 0) {
+                    ring[4 * slot + 1] = make_int4(-1, 0, 0, 0);
+                    umma::mbar_arrive(bar(kUFull, slot));
+                }
+                break;
+            }
+            const int owner = __ffs(__ballot_sync(0xffffffffu, ticket < before + upto)) - 1;
+            int4 e0, e1, e2, e3;
+            if (lane == owner) {
+                const int rel = (int)(ticket - before - (upto - mine)), per = gr.np * gr.units;
+                const int kvh = rel / per, part = (rel - kvh * per) / gr.units, u = rel - kvh * per - part * gr.units;
+                const int j0 = gr.np > 1 ? part * p.P : 0, cap = gr.np > 1 ? p.P : 0x7fffffff;
+                int b0 = 2 * u, h0 = 0, b1 = 2 * u + 1, h1 = 2 * u + 1 < gr.blocks ? 0 : -1;
+                int n0 = ceil_div(x.kl, kTok), n1 = n0;
+                if constexpr (!SHARED) {
+                    b0 = level * p.group + 2 * u / p.g;
+                    h0 = 2 * u % p.g;
+                    b1 = level * p.group + (2 * u + 1) / p.g;
+                    h1 = 2 * u + 1 < p.g * gr.blocks ? (2 * u + 1) % p.g : -1;
+                    n0 = stages_to(gr, key_end(p, x, b0));
+                    n1 = stages_to(gr, key_end(p, x, b1));
+                }
+                e0 = make_int4(x.q0, x.k0, x.ql, x.kl);
+                e1 = make_int4(kvh, gr.np, part, j0);
+                e2 = make_int4(gr.sinks, max(gr.low, gr.sinks), min(max(n0 - j0, 0), cap), h1 < 0 ? 0 : min(max(n1 - j0, 0), cap));
+                e3 = make_int4(b0, h0, b1, h1);
+                int4* e = ring + 4 * slot;
+                e[0] = e0;
+                e[1] = e1;
+                e[2] = e2;
+                e[3] = e3;
+                umma::mbar_arrive(bar(kUFull, slot));
+            }
+            const int k0 = __shfl_sync(0xffffffffu, e0.y, owner), kvh = __shfl_sync(0xffffffffu, e1.x, owner);
+            const int j0 = __shfl_sync(0xffffffffu, e1.w, owner), sinks = __shfl_sync(0xffffffffu, e2.x, owner);
+            const int low = __shfl_sync(0xffffffffu, e2.y, owner);
+            const int n = max(__shfl_sync(0xffffffffu, e2.z, owner), __shfl_sync(0xffffffffu, e2.w, owner));
+            BlockIds ids;
+            if constexpr (SHARED)
+                ids.start(p, __shfl_sync(0xffffffffu, e0.x, owner), __shfl_sync(0xffffffffu, e0.w, owner) / p.bs, j0);
+            // the next ticket, on its way while the tiles are requested
+            if (p.sched != nullptr) {
+                long long v = 0;
+                if (lane == 0) v = (long long)atomicAdd(reinterpret_cast<unsigned long long*>(p.sched), 1ull);
+                ticket = (long long)gridDim.x + __shfl_sync(0xffffffffu, v, 0);
+            } else {
+                ticket += gridDim.x;
+            }
+            for (int j = 0; j < n; ++j, ++g) {
+                if (g >= (uint32_t)NK) ok = wait(bar(kKEmpty, g % NK), (g / NK - 1) & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    bad = true;
+                    break;
+                }
+                if constexpr (SHARED) {
+                    // which of the stage's tokens there are: a block whose id is out of the pool is absent
+                    const int pb = ids.stage(p);
+                    const uint32_t there = __ballot_sync(0xffffffffu, pb >= 0);
+                    if (pb == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
+                    if (lane < 4) {
+                        uint32_t w = (there >> lane) & 1u ? 0xffffffffu : 0u;
+                        if (p.bs == 16) w = ((there >> (2 * lane)) & 1u ? 0xffffu : 0u) | ((there >> (2 * lane)) & 2u ? 0xffff0000u : 0u);
+                        masks[4 * (g & 7) + lane] = w;
+                    }
+                    __syncwarp();
+                    load_blocks<D>(p, &kmap, ktile(g), kvh, pb, there, bar(kKFull, g % NK));
+                    continue;
+                }
+                if (lane == 0) {
+                    const uint32_t full = bar(kKFull, g % NK);
+                    mbar_arrive_expect_tx(full, C::kItemBytes);
+                    const int row = k0 + stage_key(j0 + j, sinks, low);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tensor_load_2d(ktile(g) + h * (kTok * 128), &kmap, kvh * D + h * 64, row, full);
+                }
+                __syncwarp();
+            }
+            if (bad) break;
+            ++un;
+        }
+        // copies still in flight land before the block leaves
+        for (uint32_t k = 1; k <= (uint32_t)NK && k <= g; ++k)
+            wait(bar(kKFull, (g - k) % NK), ((g - k) / NK) & 1, false);
+        if (p.sched != nullptr && lane == 0) {
+            unsigned long long* ctr = reinterpret_cast<unsigned long long*>(p.sched);
+            __threadfence();
+            if (atomicAdd(ctr + 1, 1ull) == gridDim.x - 1) {
+                atomicExch(ctr, 0ull);
+                atomicExch(ctr + 1, 0ull);
+            }
+        }
+    } else if (warp == kVWarp) {
+        // ------------------------------------------------------------ V tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        uint32_t g = 0, un = 0, tails = 0;
+        bool ok = true, bad = false;
+        for (;;) {
+            const int slot = un & 1;
+            ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (e1.x < 0) break;
+            const int n = max(e2.z, e2.w);
+            BlockIds ids;
+            if constexpr (SHARED) ids.start(p, e0.x, e0.w / p.bs, e1.w);
+            for (int j = 0; j < n; ++j, ++g) {
+                if (g >= (uint32_t)NV) ok = wait(bar(kVEmpty, g % NV), (g / NV - 1) & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    bad = true;
+                    break;
+                }
+                const int key = stage_key(e1.w + j, e2.x, e2.y);
+                // rows of the tile, in eighths (SHARED: a block or half of one) or counted, that hold something
+                const int here = e0.w - key;
+                uint32_t there = 0xffu;
+                int pb = 0;
+                if constexpr (SHARED) {
+                    pb = ids.stage(p);
+                    there = __ballot_sync(0xffffffffu, pb >= 0);
+                }
+                const bool part = SHARED ? there != (p.bs == 16 ? 0xffu : 0xfu) : here < kTok;
+                const uint32_t full = bar(kVFull, g % NV), landed = part ? bar(kTail, 0) : full;
+                if constexpr (SHARED) {
+                    load_blocks<D>(p, &vmap, vtile(g), e1.x, pb, there, landed);
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(landed, C::kItemBytes);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tensor_load_2d(vtile(g) + h * (kTok * 128), &vmap, e1.x * D + h * 64, e0.y + key, landed);
+                }
+                __syncwarp();
+                if (part) {
+                    ok = wait(landed, tails & 1, false);
+                    ++tails;
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        bad = true;
+                        break;
+                    }
+                    const uint32_t vb = vtile(g);
+                    for (int i = (SHARED ? 0 : here * 8) + lane; i < kTok * 8; i += 32) {
+                        if (SHARED && ((there >> (i / 8 / p.bs)) & 1u)) continue;
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + h * (kTok * 128) + i * 16), "r"(0u)
+                                         : "memory");
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(full);
+                }
+            }
+            if (bad) break;
+            ++un;
+        }
+        for (uint32_t k = 1; k <= (uint32_t)NV && k <= g; ++k)
+            wait(bar(kVFull, (g - k) % NV), ((g - k) / NV) & 1, false);
+    } else if (warp == kQWarp) {
+        // ------------------------------------------------------------ Q tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        uint32_t un = 0, qu[2] = {0u, 0u};
+        bool ok = true, bad = false;
+        for (;;) {
+            const int slot = un & 1;
+            ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2], e3 = ring[4 * slot + 3];
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (e1.x < 0) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if ((t == 0 ? e2.z : e2.w) == 0) continue;       // no keys, or no tile
+                if (qu[t] >= 1) ok = wait(bar(kQEmpty, t), (qu[t] - 1) & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    bad = true;
+                    break;
+                }
+                if constexpr (SHARED) {
+                    DecodeParams q{};
+                    q.q = p.q;
+                    q.Hq = p.Hq;
+                    q.g = p.g;
+                    const int r0 = (t == 0 ? e3.x : e3.z) * kRows;
+                    load_q_rows<D, kRows>(q, e0.x, e1.x, r0, 0, kRows, e0.z * p.g - r0, qbuf(t));
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(bar(kQFull, t));
+                } else if (lane == 0) {
+                    // rows past the sequence's last are other sequences' or zeros: their results are not stored
+                    mbar_arrive_expect_tx(bar(kQFull, t), C::kItemBytes);
+                    const int head = e1.x * p.g + (t == 0 ? e3.y : e3.w), row = e0.x + (t == 0 ? e3.x : e3.z) * kRows;
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tensor_load_2d(qbuf(t) + h * (kRows * 128), &qmap, head * D + h * 64, row, bar(kQFull, t));
+                }
+                __syncwarp();
+                ++qu[t];
+            }
+            if (bad) break;
+            ++un;
+        }
+        for (int t = 0; t < 2; ++t)
+            if (qu[t] > 0) wait(bar(kQFull, t), (qu[t] - 1) & 1, false);
+    } else if (warp == kMmaWarp) {
+        // ----------------------------------------------------------- products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        // The whole warp walks the loop and one elected thread issues: the
+        // operands are then uniform, and a product takes its 64 clocks.  Issued
+        // by `if (lane == 0)` every operand goes through a vector register, and
+        // a product took 123-147 clocks to issue.
+        constexpr uint32_t idS = umma::idesc_bf16_f32(kRows, kTok, false);
+        constexpr uint32_t idPV = umma::idesc_bf16_f32(kRows, D, true);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // descriptors of the first K step of slot 0; a slot or K step on adds to the address, in 16 bytes
+        const uint64_t q_desc = umma::desc_sw128(qbuf(0), 16, 1024), k_desc = umma::desc_sw128(base, 16, 1024);
+        const uint64_t v_desc = umma::desc_sw128(base + C::kVOff, kTok * 128, 1024);
+        uint32_t g = 0, un = 0, gt[2] = {0u, 0u}, qu[2] = {0u, 0u};
+        bool ok = true;
+        // waits of the whole warp
+        auto all = [&](uint32_t b, uint32_t parity) -> bool { return !__any_sync(0xffffffffu, !wait(b, parity, true)); };
+        auto issue_s = [&](int t, uint32_t gs, bool last) {
+            const uint64_t kd = k_desc + (gs % NK) * (C::kItemBytes / 16), qd = q_desc + t * (C::kItemBytes / 16);
+            umma::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) / 16;
+                    umma::mma_bf16(tm + tmem_s(t), qd + off, kd + off, idS, kk > 0);
+                }
+                umma::commit(bar(kSFull, t));
+                if (last) umma::commit(bar(kQEmpty, t));
+            }
+            __syncwarp();
+        };
+        // half of a stage's keys
+        auto issue_pv = [&](int t, uint32_t gs, int half, bool first) {
+            const uint64_t vd = v_desc + (gs % NV) * (C::kItemBytes / 16) + half * (kTok / 2 * 128 / 16);
+            umma::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kTok / 32; ++kk)
+                    mma_ts(tm + tmem_o(t), tm + tmem_s(t) + half * (kTok / 4) + kk * 8, vd + kk * (2048 / 16), idPV,
+                           !(first && kk == 0));
+                if (half) umma::commit(bar(kPVDone, t));
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t b) {                  // a slot, once what was issued before has read it
+            if (elect_one()) umma::commit(b);
+            __syncwarp();
+        };
+        for (;;) {
+            const int slot = un & 1;
+            if (!all(bar(kUFull, slot), (un >> 1) & 1)) break;
+            const int kvh = __shfl_sync(0xffffffffu, ring[4 * slot + 1].x, 0);
+            const int c[2] = {__shfl_sync(0xffffffffu, ring[4 * slot + 2].z, 0),
+                              __shfl_sync(0xffffffffu, ring[4 * slot + 2].w, 0)};
+            const int n = max(c[0], c[1]);
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (kvh < 0) break;
+            if (n > 0) {
+                ok = all(bar(kKFull, g % NK), (g / NK) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (c[t] == 0 || !ok) continue;
+                    ok = all(bar(kQFull, t), qu[t] & 1);
+                    // the tile's last P . V has read the buffer
+                    if (ok && gt[t] > 0) ok = all(bar(kPVDone, t), (gt[t] - 1) & 1);
+                    if (ok) issue_s(t, g, c[t] == 1);
+                }
+                if (!ok) break;
+                release(bar(kKEmpty, g % NK));
+            }
+            for (int j = 0; j < n && ok; ++j, ++g) {
+                ok = all(bar(kVFull, g % NV), (g / NV) & 1);
+                bool next_k = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= c[t] || !ok) continue;
+                    ok = all(bar(kPFull, t), gt[t] & 1);
+                    if (!ok) break;
+                    issue_pv(t, g, 0, j == 0);
+                    ok = all(bar(kPFull2, t), gt[t] & 1);
+                    if (!ok) break;
+                    issue_pv(t, g, 1, false);
+                    if (j + 1 < c[t]) {
+                        // the next S_t overwrites P_t: only after P_t . V_j is done
+                        if (!next_k) ok = all(bar(kKFull, (g + 1) % NK), ((g + 1) / NK) & 1);
+                        next_k = true;
+                        ok = ok && all(bar(kPVDone, t), gt[t] & 1);
+                        if (!ok) break;
+                        issue_s(t, g + 1, j + 2 == c[t]);
+                    }
+                    ++gt[t];
+                }
+                if (!ok) break;
+                release(bar(kVEmpty, g % NV));
+                if (j + 1 < n) release(bar(kKEmpty, (g + 1) % NK));
+            }
+            if (!ok) break;
+            for (int t = 0; t < 2; ++t) qu[t] += c[t] > 0;
+            ++un;
+        }
+        // every product issued here completes before the block releases TMEM
+        release(bar(kFin, 0));
+        wait(bar(kFin, 0), 0, false);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int t = warp >> 2;                              // tile
+        const int i = (warp & 3) * 32 + lane;                // row of the tile, TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_col = tmem + lane_base + tmem_s(t);
+        const uint32_t o_col = tmem + lane_base + tmem_o(t);
+        uint32_t gt = 0, un = 0, gs = 0;
+        bool ok = true, bad = false;
+        for (;;) {
+            const int slot = un & 1;
+            ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
+            if (__any_sync(0xffffffffu, !ok)) break;
+            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2], e3 = ring[4 * slot + 3];
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (e1.x < 0) break;
+            ++un;
+            const int head = t == 0 ? e3.y : e3.w, n = t == 0 ? e2.z : e2.w;
+            const uint32_t stages = gs;
+            gs += max(e2.z, e2.w);
+            if (head < 0) continue;                              // the unit has one tile
+            const int block = t == 0 ? e3.x : e3.z;
+            const int ql = e0.z, kl = e0.w;
+            int qi = block * kRows + i, hh = head;               // this row's query and head of the K/V head's
+            bool rv = qi < ql;
+            int first = p.causal ? kl - ql + block * kRows : kl - 1;             // position of the tile's first row
+            int pos = p.causal ? first + i : kl - 1;
+            const int far = p.causal ? first + kRows - 1 : kl - 1;               // and of its last
+            if constexpr (SHARED) {
+                rv = qi / p.g < ql;
+                hh = qi % p.g;
+                qi /= p.g;
+                // a member that ends inside the shared blocks sees its own tokens only
+                pos = rv ? min(__ldg(p.lens + e0.x + qi), kl) - 1 : kl - 1;
+                first = (int)__reduce_min_sync(0xffffffffu, (unsigned)max(pos + 1, 0)) - 1;
+            }
+            const bool flip = !(p.scale_log2 > 0.f);
+            const float scl = flip ? 1.f : p.scale_log2;
+            float m_ref = -CUDART_INF_F, l = 0.f;
+            uint32_t e4 = stages;                                // the stage in the block's count (SHARED's masks)
+            for (int j = 0; j < n; ++j, ++gt, ++e4) {
+                ok = wait(bar(kSFull, t), gt & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    bad = true;
+                    break;
+                }
+                umma::fence_after_sync();
+                uint32_t sr[kTok / 32][32];
+#pragma unroll
+                for (int w = 0; w < kTok / 32; ++w) umma::tmem_ld32(s_col + 32 * w, sr[w]);
+                umma::tmem_wait_ld();
+                const int key = stage_key(e1.w + j, e2.x, e2.y);
+                bool whole = key + kTok - 1 <= min(first, kl - 1) &&
+                             (p.window == 0 || key + kTok <= p.sinks || key > far - p.window);
+                if constexpr (SHARED) {
+                    const uint32_t* m = masks + 4 * (e4 & 7);
+                    whole = whole && (m[0] & m[1] & m[2] & m[3]) == 0xffffffffu;
+                }
+                if (flip) {
+#pragma unroll
+                    for (int w = 0; w < kTok / 32; ++w)
+#pragma unroll
+                        for (int b = 0; b < 32; ++b) sr[w][b] = __float_as_uint(__uint_as_float(sr[w][b]) * p.scale_log2);
+                }
+                if (!whole) {
+                    // -inf where this row does not see the key
+#pragma unroll
+                    for (int w = 0; w < kTok / 32; ++w) {
+                        const int v0 = key + 32 * w;
+                        uint32_t seen = bits_below(min(pos, kl - 1) + 1 - v0);
+                        if constexpr (SHARED) seen &= masks[4 * (e4 & 7) + w];
+                        else if (p.window > 0) seen &= ~bits_between(v0, p.sinks, pos - p.window + 1);
+                        if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+#pragma unroll
+                            for (int b = 0; b < 32; ++b)
+                                if (!((seen >> b) & 1u)) sr[w][b] = 0xff800000u;
+                        }
+                    }
+                }
+                float mx8[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(sr[0][k]);
+#pragma unroll
+                for (int b = 8; b < kTok; ++b) mx8[b & 7] = fmaxf(mx8[b & 7], __uint_as_float(sr[b >> 5][b & 31]));
+                const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scl;
+                float alpha = 1.f;
+                bool resc = false;
+                if (j == 0) {
+                    m_ref = mx;
+                } else if (mx > m_ref + kRescaleLog2) {
+                    if (m_ref != -CUDART_INF_F) {
+                        alpha = fast_exp2(m_ref - mx);
+                        resc = true;
+                    }
+                    m_ref = mx;
+                }
+                l *= alpha;
+                const float mb = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+                const uint64_t xs2 = umma::f2_pack(scl, scl), nmb2 = umma::f2_pack(-mb, -mb);
+                uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+                if (__any_sync(0xffffffffu, resc)) {
+                    // O_t holds the products up to the previous stage
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_col + c0, ov);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                        tmem_st16(o_col + c0, ov);
+                    }
+                }
+                // P in two halves: the product with the first 64 keys runs while the others are weighed
+#pragma unroll
+                for (int w = 0; w < kTok / 32; ++w) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint64_t s01 = umma::f2_pack(__uint_as_float(sr[w][2 * k]), __uint_as_float(sr[w][2 * k + 1]));
+                        float x0, x1;
+                        umma::f2_unpack(umma::f2_fma(s01, xs2, nmb2), x0, x1);
+                        const float a0 = fast_exp2(x0), a1 = fast_exp2(x1);
+                        ls2[k & 3] = umma::f2_add(ls2[k & 3], umma::f2_pack(a0, a1));
+                        pw[k] = pack2<false>(a0, a1);
+                    }
+                    tmem_st16(s_col + 16 * w, pw);
+                    if (w & 1) {
+                        umma::tmem_wait_st();
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(bar(w == 1 ? kPFull : kPFull2, t));
+                    }
+                }
+                float ls[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma::f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
+                l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+            }
+            if (bad) break;
+
+            // O / l, or the partition's (m, l, O), once the tile's last product is done
+            if (n > 0) {
+                ok = wait(bar(kPVDone, t), (gt - 1) & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) break;
+                umma::fence_after_sync();
+            }
+            const int np = e1.y;
+            const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
+            const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < D / 32; ++c0) {
+                uint32_t ov[32];
+                if (n > 0) {
+                    umma::tmem_ld32(o_col + 32 * c0, ov);
+                    umma::tmem_wait_ld();
+                }
+                if (n == 0) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) ov[k] = 0u;
+                }
+                if (!rv) continue;
+                const int col = 32 * c0;
+                if (!SHARED && np == 1) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + hrow * D + col;
+                    store_row32(dst, ov, f, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0);
+                } else {
+                    store_part32(p.part_acc + (hrow * p.Pmax + e1.z) * D + col, ov,
+                                 (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
+                }
+            }
+            if (rv && (SHARED || np > 1)) {
+                const size_t u = hrow * p.Pmax + e1.z;
+                p.part_ml[2 * u] = m_ref;
+                p.part_ml[2 * u + 1] = l;
+            }
+            umma::fence_before_sync();
+        }
+    }
+
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool SHARED>
+cudaError_t launch_attend(const PromptParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                          long long units, int num_sms, cudaStream_t st) {
+    using C = Cfg<D>;
+    auto kern = attend_kernel<D, SHARED>;
+    // the register shares must fit in what the block is launched with
+    // (setmaxnreg waits forever otherwise): checked once, on the binary
+    static std::once_flag checked;
+    static cudaError_t check = cudaSuccess;
+    std::call_once(checked, [&] {
+        cudaFuncAttributes fa;
+        check = cudaFuncGetAttributes(&fa, kern);
+        if (check == cudaSuccess &&
+            (fa.numRegs * kThreads < 32 * kSoftWarps * kSoftRegs + 128 * kOtherRegs || fa.maxThreadsPerBlock < kThreads))
+            check = cudaErrorInvalidConfiguration;
+    });
+    if (check != cudaSuccess) return check;
+    static SmemOptIn optin;
+    cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)(units < num_sms ? (units > 0 ? units : 1) : num_sms);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, st, p, qmap, kmap, vmap);
+}
+
+}  // namespace
+}  // namespace pkv

@@ -17,6 +17,7 @@ cudaError_t launch_decode_tc(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, in
     switch (mode) {
         case DecodeMode::kBlockTable: return launch_tc<DecodeMode::kBlockTable>(p, q_dt, c_dt, num_sms, st);
         case DecodeMode::kTokenTable: return launch_decode_tc_token(p, q_dt, c_dt, num_sms, st);
+        case DecodeMode::kSuffix: return launch_decode_tc_suffix(p, q_dt, c_dt, num_sms, st);
         case DecodeMode::kWindow: return launch_decode_tc_window(p, q_dt, c_dt, num_sms, st);
         case DecodeMode::kScored: return launch_decode_tc_scored(p, q_dt, c_dt, num_sms, st);
     }

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     constexpr bool TT = MODE == DecodeMode::kTokenTable || MODE == DecodeMode::kScored;
     constexpr bool WIN = MODE == DecodeMode::kWindow;
     constexpr bool SCORED = MODE == DecodeMode::kScored;
+    constexpr bool SUF = MODE == DecodeMode::kSuffix;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;     // fragment row / column-pair of this lane
@@ -265,9 +266,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
             v = __shfl_sync(0xffffffffu, v, 0);
             static_next += total_warps;
             if (v >= total_units) return false;
-            if (!unit_of<WIN>(p, v, nsets, region_a, x)) continue;
+            if (!unit_of<WIN, SUF>(p, v, nsets, region_a, x)) continue;
             if (x.t1 <= x.t0) {
-                // a sequence with no tokens: its output is zero
+                // a sequence with no tokens: its output is zero (or its shared tokens' alone)
+                if (SUF && x.np > 1) continue;
                 for (int i = lane; i < x.nh * D; i += 32)
                     store_out<QF>(p, ((size_t)x.s * p.Hq + x.h0 + i / D) * D + (i % D), 0.f);
                 continue;
@@ -281,11 +283,13 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
     int tab = 0, tab_next = 0, tab_chunk = 0, tab_blocks = 0;
     int i_n = 0;                          // with a window: the sequence's length and the tokens left out
     WindowSpan i_span{};
+    int i_begin = 0;                      // SUF: the blocks before the unit's token 0
     auto load_chunk = [&](int chunk) -> int {
         const int rb = 32 * chunk + lane;
         if (rb >= tab_blocks) return 0;
         int lb = iu.t0 / bs + rb;
         if constexpr (WIN) lb = span_token(i_span, lb * bs) / bs;
+        if constexpr (SUF) lb += i_begin;
         return __ldg(p.block_tables + (size_t)iu.s * p.MB + lb);
     };
 
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8, QF::bytes>::kWarps * 32, 1)
                 i_n = min(max(__ldg(p.context_lens + iu.s), 0), p.max_ctx);
                 i_span = window_span(i_n - p.window, p.sinks, bs);
             }
+            if constexpr (SUF) i_begin = __ldg(p.begin + iu.s) / bs;
             if (lane == 0) {
                 int4* e = reinterpret_cast<int4*>(queue + q_tail % C::kQueue);
                 e[0] = make_int4(iu.s, iu.kvh, iu.h0, iu.nh);
@@ -856,8 +861,8 @@ cudaError_t launch_one(DecodeParams& p, int num_sms, cudaStream_t st) {
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
     const unsigned long long region_a = (unsigned long long)(max_visible(p) / p.P) * per_part;   // full partitions
     const unsigned long long units = region_a + (unsigned long long)chunk_slots(p.P, p.Q, p.hold) * per_part;
-    // with a window, or scored, a small launch puts its units on as many SMs as it has
-    const bool spread = MODE == DecodeMode::kWindow || MODE == DecodeMode::kScored;
+    // with a window, scored, or behind shared tokens a small launch puts its units on as many SMs as it has
+    const bool spread = MODE == DecodeMode::kWindow || MODE == DecodeMode::kScored || MODE == DecodeMode::kSuffix;
     unsigned long long want = spread ? units : (units + C::kWarps - 1) / C::kWarps;
     int grid = (int)(want < (unsigned long long)num_sms ? want : (unsigned long long)num_sms);
     if (grid < 1) grid = 1;

@@ -134,10 +134,23 @@ struct PromptParams {
     int causal, window, sinks;
     int P, Pmax;              // stages per partition (0: no split), partial results per row
     float scale_log2;
+    // decode of sequences that share blocks: S groups, group i the sequences query_start[i] .. query_start[i + 1]
+    // of the Tq, whose first key_start[i] tokens lie in the blocks of the first one's table
+    const int32_t* tables;    // [Tq][MB]
+    const int32_t* lens;      // [Tq]
+    int32_t* begin;           // [Tq]: written: the tokens a sequence shares
+    int MB, bs, NB;
 };
 // an odd number of heads per K/V head pairs the tiles of two query blocks
 inline int prompt_group(int g) { return g % 2 ? 2 : 1; }
 cudaError_t launch_prompt(const PromptParams& p, int d, int num_sms, cudaStream_t st);
+// the partial results of the sequences' own tokens, behind first_own of a row's Pmax
+struct SharedParts {
+    int first_own, P, Q, max_ctx;
+};
+struct DecodeParams;
+cudaError_t launch_shared_prefix(const PromptParams& p, const DecodeParams& d, int num_sms, cudaStream_t st);
+cudaError_t launch_shared_merge(const PromptParams& p, const SharedParts& x, int d, cudaStream_t st);
 
 struct CopyParams {
     const int64_t* mapping;
@@ -196,6 +209,7 @@ struct DecodeParams {
     // scored token-table decode: the logits (log2 units) of each unit's
     // tokens, rows of score_width(g) heads, [S][Hkv * head sets][max_ctx]
     float* logits;
+    const int32_t* begin;     // kSuffix: [S]: tokens before the ones this call attends to, whole blocks
 };
 
 struct EvictParams {
@@ -236,7 +250,8 @@ enum class DecodeMode {
     kBlockTable,
     kTokenTable,
     kWindow,     // block table, sliding window with sinks
-    kScored      // token table; also writes the logits and every row's (max, sum)
+    kScored,     // token table; also writes the logits and every row's (max, sum)
+    kSuffix      // block table, from the token `begin` of each sequence on
 };
 
 cudaError_t launch_decode_simt(const DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, cudaStream_t st);
@@ -251,6 +266,7 @@ cudaError_t launch_decode_kv4(DecodeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_tc_token(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_tc_window(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_tc_scored(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
+cudaError_t launch_decode_tc_suffix(DecodeParams& p, pkv_dtype q_dt, pkv_dtype c_dt, int num_sms, cudaStream_t st);
 cudaError_t launch_decode_reduce(const DecodeParams& p, pkv_dtype q_dt, cudaStream_t st);
 // after a scored decode: scores[s][t] += the attention weights (rows of MT scores) and, when split, the merge
 cudaError_t launch_score(const DecodeParams& p, pkv_dtype q_dt, bool merge, float* scores, int MT, int num_sms,

@@ -57,6 +57,7 @@ extern "C" pkv_status pkv_invoke(int call, const void* words) {
         case PKV_CALL_EVICT: return run(pkv_evict_tokens, words);
         case PKV_CALL_ROTARY_WRITE: return run(pkv_rotary_kv_write, words);
         case PKV_CALL_PROMPT: return run(pkv_prompt_attention, words);
+        case PKV_CALL_DECODE_SHARED: return run(pkv_paged_attention_decode_shared, words);
     }
     return PKV_ERR_INVALID_ARG;
 }

@@ -42,8 +42,10 @@ struct __align__(16) Unit {
 // the tail of the launch is short.  Returns false for ids that name no
 // work (a partition past the sequence's full ones, a chunk past its
 // remainder, or a last chunk that does not exist).  With a window (WIN) the
-// tokens t0, t1 are those of window_span's numbering.
-template <bool WIN>
+// tokens t0, t1 are those of window_span's numbering.  SUFFIX: numbered from
+// p.begin[s]; where that is not 0 there are other partial results beside this
+// launch's, and np is never 1.
+template <bool WIN, bool SUFFIX = false>
 __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long long u, int nsets,
                                         unsigned long long region_a, Unit& x) {
     const unsigned long long per_part = (unsigned long long)p.S * p.Hkv * nsets;
@@ -63,7 +65,13 @@ __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long lon
         n = n < 0 ? 0 : p.max_ctx;
     }
     if constexpr (WIN) n -= window_span(n - p.window, p.sinks, p.bs).gap;
+    int begin = 0;
+    if constexpr (SUFFIX) {
+        begin = __ldg(p.begin + x.s);
+        n = max(n - begin, 0);
+    }
     x.np = num_partitions(n, p.P, p.Q, p.hold);
+    if (SUFFIX && begin > 0) x.np = max(x.np, 2);
     const int full = whole_partitions(n, p.P, p.Q, p.hold);
     const int tail = n - full * p.P;
     const int cfull = chunk_slots(p.P, p.Q, p.hold) - 1;   // full-size chunks of the longest remainder
