@@ -950,13 +950,23 @@ bool prompt_shape_ok(int S, int Tq, int max_q, int max_k, int Hq, int Hkv, int d
            (d == 64 || d == 128) && req >= -1 && (req <= 0 || req % kPromptStage == 0);
 }
 
+// Few queries: tiles of (query, head) rows, so that the heads of a K/V head
+// share them.  (Rows are stepped through by heads.)
+constexpr int kPackedQueries = 64;
+bool prompt_packed(int max_q, int64_t q_stride, int d) { return max_q <= kPackedQueries && q_stride % d == 0; }
+
 // Stages per partition (0: no split).  Units that fill the SMs are not split.
 int resolve_prompt_partition(int S, int Tq, int max_q, int Hq, int Hkv, int d, int stages, int req, size_t room) {
     if (req != 0) return req > 0 ? req / kPromptStage : 0;
     const int g = Hq / Hkv, group = prompt_group(g);
     const long long rows = (long long)group * kPromptStage;
     const long long dense = S * ((max_q + rows - 1) / rows), ragged = Tq / rows + S;
-    const long long units = (dense < ragged ? dense : ragged) * Hkv * ((g * group + 1) / 2);
+    long long units = (dense < ragged ? dense : ragged) * Hkv * ((g * group + 1) / 2);
+    if (max_q <= kPackedQueries) {
+        const long long tiles = ((long long)max_q * g + kPromptStage - 1) / kPromptStage;
+        units = (long long)S * Hkv * ((tiles + 1) / 2);
+        if (tiles == 1) units = (units + 1) / 2;           // paired partitions
+    }
     if (units == 0 || units >= 152) return 0;
     const long long parts = 152 / units;
     int P = (int)((stages + parts - 1) / parts);
@@ -1026,6 +1036,7 @@ pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, c
     p.v_stride = num_key_tokens > 0 ? v_stride : (int64_t)Hkv * d;
     p.S = S; p.Tq = num_query_tokens; p.Tk = num_key_tokens; p.max_q = max_query_len; p.max_k = max_key_len;
     p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv; p.group = prompt_group(p.g);
+    p.packed = prompt_packed(max_query_len, q_stride, d);
     p.causal = causal != 0; p.window = window; p.sinks = num_sinks;
     p.P = pl.split ? P : 0;
     p.Pmax = pl.Pmax;
@@ -1078,12 +1089,14 @@ int resolve_shared_prefix(int G, int max_group, int g, int Hkv, int max_shared, 
         const int p = (req + kPromptStage - 1) / kPromptStage;
         return p < stages ? p : 0;
     }
+    // a group of one tile pairs its partitions: two of them are a unit
     const long long tiles = ((long long)max_group * g + kPromptStage - 1) / kPromptStage, units = G * Hkv * ((tiles + 1) / 2);
+    const int per = tiles == 1 ? 2 : 1;
     long long best = 0;
     int best_p = 0;
     for (int np = 1; np <= 64 && np <= stages; ++np) {
         const int p = (stages + np - 1) / np, n = (stages + p - 1) / p;
-        const long long cost = (units * n + 151) / 152 * (p + 3) * 16 + n;
+        const long long cost = (units * ((n + per - 1) / per) + 151) / 152 * ((n > 1 ? per : 1) * p + 4) * 16 + n;
         if (np == 1 || cost < best) {
             best = cost;
             best_p = n > 1 ? p : 0;
@@ -1097,12 +1110,21 @@ bool shared_shape_ok(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, 
            max_group <= 65535 && req >= -1 && (req <= 0 || req % bs == 0);
 }
 
+constexpr int kMaxOwnParts = 96;
+
 // Whether the shared tokens are worth a launch of their own.
 bool shares_enough(int G, int max_shared, int max_group, int bs) { return G > 0 && max_shared >= bs && max_group > 1; }
 
 SharedPlan choose_shared(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, int max_shared, int max_group, int req,
                          size_t room) {
-    int P = resolve_partition(S, Hq, Hkv, d, bs, max_ctx, req);
+    // what a sequence has of its own: taken to be what the longest one would have beside the longest shared part
+    // (longer ones are more partitions, up to kMaxOwnParts)
+    int P = resolve_partition(S, Hq, Hkv, d, bs, max_ctx > max_shared ? max_ctx - max_shared : max_ctx, req);
+    if (req == 0) {
+        if (P == 0) P = max_ctx > max_shared ? (max_ctx - max_shared + bs - 1) / bs * bs : max_ctx;
+        P = max(P, (max_ctx / kMaxOwnParts + bs) / bs * bs);
+        if (P >= max_ctx) P = 0;
+    }
     int pre = resolve_shared_prefix(G, max_group, Hq / Hkv, Hkv, max_shared, req);
     SharedPlan sp = plan_shared(S, Hq, d, max_ctx, max_shared, pre, P);
     // a smaller workspace: fewer partitions
@@ -1177,15 +1199,17 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_d
     d_p.part_ml = ml + 2 * sp.first_own;
     d_p.part_acc = acc + (size_t)sp.first_own * d;
     d_p.begin = reinterpret_cast<int32_t*>(ws + sp.begin_offset);
+    d_p.own_max = reinterpret_cast<int*>(ws + 128);       // behind the counters, in the header
     PromptParams p{};
     p.out = out; p.q = query; p.k = key_cache; p.v = value_cache;
     p.query_start = group_start; p.key_start = shared_lens; p.part_ml = ml; p.part_acc = acc;
     p.sched = d_p.sched; p.err = err_word;
     p.S = G; p.Tq = S; p.max_q = max_group_size; p.max_k = max_shared_len; p.Hq = Hq; p.Hkv = Hkv; p.g = Hq / Hkv;
-    p.group = 1; p.P = sp.pre; p.Pmax = sp.Pmax;
+    p.group = 1; p.q_stride = (int64_t)Hq * d; p.P = sp.pre; p.Pmax = sp.Pmax;
     p.scale_log2 = scale * kLog2e;
     p.tables = block_tables; p.lens = context_lens; p.begin = reinterpret_cast<int32_t*>(ws + sp.begin_offset);
-    p.MB = MB; p.bs = bs; p.NB = NB;
+    p.own_max = reinterpret_cast<int*>(ws + 128);
+    p.MB = MB; p.bs = bs; p.NB = NB; p.max_ctx = max_context_len;
     const SharedParts parts{sp.first_own, d_p.P, d_p.Q, max_context_len};
     auto st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_shared_prefix(p, d_p, num_sms_current(), st);

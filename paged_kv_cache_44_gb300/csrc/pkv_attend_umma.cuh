@@ -134,18 +134,23 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// The rows of a tile: 128 queries of one head (kHeads: K and V of a head are
+// read for two tiles), or the (query, head) pairs of a K/V head in order, 128 at
+// a time (kPacked, kShared: few queries fill a tile between them).
+enum Mode { kHeads, kPacked, kShared };
+
 // A sequence's rows; false when a bound is broken (it is skipped then).
-// SHARED: a group of sequences, its members q0 .. q0 + ql, whose first kl
+// kShared: a group of sequences, its members q0 .. q0 + ql, whose first kl
 // tokens (whole blocks) are read through the table of the first of them.
 struct Seq {
     int q0, ql, k0, kl;
 };
-template <bool SHARED>
+template <int MODE>
 __device__ __forceinline__ bool sequence(const PromptParams& p, int s, Seq& x) {
-    if constexpr (SHARED) {
-        x.q0 = __ldg(p.query_start + s);
-        const long long members = (long long)__ldg(p.query_start + s + 1) - x.q0;
-        const int shared = __ldg(p.key_start + s);
+    if constexpr (MODE == kShared) {
+        x.q0 = load_behind_wait(p.query_start + s);
+        const long long members = (long long)load_behind_wait(p.query_start + s + 1) - x.q0;
+        const int shared = load_behind_wait(p.key_start + s);
         x.ql = (int)members;
         x.k0 = 0;
         x.kl = shared / p.bs * p.bs;
@@ -154,53 +159,60 @@ __device__ __forceinline__ bool sequence(const PromptParams& p, int s, Seq& x) {
         if (!ok) x.kl = 0;
         return ok;
     }
-    x.q0 = __ldg(p.query_start + s);
-    x.k0 = __ldg(p.key_start + s);
-    const long long ql = (long long)__ldg(p.query_start + s + 1) - x.q0, kl = (long long)__ldg(p.key_start + s + 1) - x.k0;
+    x.q0 = load_behind_wait(p.query_start + s);
+    x.k0 = load_behind_wait(p.key_start + s);
+    const long long ql = (long long)load_behind_wait(p.query_start + s + 1) - x.q0, kl = (long long)load_behind_wait(p.key_start + s + 1) - x.k0;
     x.ql = (int)ql;
     x.kl = (int)kl;
     return x.q0 >= 0 && x.k0 >= 0 && ql >= 0 && kl >= 0 && ql <= p.max_q && kl <= p.max_k && x.q0 + ql <= p.Tq &&
            x.k0 + kl <= p.Tk;
 }
 
-// Query blocks come in groups of p.group (two where the heads per K/V head are
-// odd, so that tiles pair up).  The keys of a group's stages: the blocks of
-// 128 that hold sinks, then those from the first query's window on.
+// kHeads: query blocks come in groups of p.group (two where the heads per K/V
+// head are odd, so that tiles pair up), one group a level; else a sequence's
+// tiles are one group.  The keys of a group's stages: the blocks of 128 that
+// hold sinks, then those from the first query's window on.  A sequence of one
+// packed tile and several partitions pairs the partitions instead: the unit's
+// two tiles then hold the same rows and take turns at the stages (few rows over
+// many keys: one tile alone waits for its own products, XXXX).
 struct Group {
-    int blocks, units, sinks, low, np;      // query blocks here; units per K/V head; key blocks; partitions
+    int blocks, units, sinks, low, np;      // query blocks (tiles) here; units per K/V head; key blocks; partitions
+    bool pairs;
+    __device__ __forceinline__ int per_head() const { return pairs ? (np + 1) / 2 : np * units; }
 };
-__device__ __forceinline__ int key_end(const PromptParams& p, const Seq& x, int block) {   // keys the block's queries see
-    if (!p.causal) return x.kl;
-    const int last = min(x.ql, (block + 1) * kRows);
-    return max(x.kl - x.ql + last, 0);
+// keys that the queries of a block (a packed tile) see
+template <int MODE>
+__device__ __forceinline__ int key_end(const PromptParams& p, const Seq& x, int block) {
+    if (MODE == kShared || !p.causal) return x.kl;
+    int last = (block + 1) * kRows;
+    if constexpr (MODE == kPacked) last = (last - 1) / p.g + 1;
+    return max(x.kl - x.ql + min(x.ql, last), 0);
 }
 __device__ __forceinline__ int stages_to(const Group& g, int end) {
     const int blocks = ceil_div(end, kTok);
     return min(g.sinks, blocks) + max(0, blocks - max(g.low, g.sinks));
 }
-template <bool SHARED>
+template <int MODE>
 __device__ __forceinline__ bool group_of(const PromptParams& p, const Seq& x, int level, Group& g) {
-    if constexpr (SHARED) {
-        // tiles of 128 (member, head) rows of a K/V head; one level holds them all
+    int first = 0;                          // the group's first query, and its last block
+    if constexpr (MODE == kHeads) {
+        first = level * p.group;
+        g.blocks = min(p.group, ceil_div(x.ql, kRows) - first);
+        g.units = (p.g * g.blocks + 1) / 2;
+    } else {
         g.blocks = (int)(((long long)x.ql * p.g + kRows - 1) / kRows);
         g.units = (g.blocks + 1) / 2;
-        g.sinks = g.low = 0;
-        const int n = ceil_div(x.kl, kTok);
-        g.np = p.P > 0 && n > p.P ? ceil_div(n, p.P) : 1;
-        return x.kl > 0 && g.blocks > 0;
     }
-    const int nqb = ceil_div(x.ql, kRows);
-    g.blocks = min(p.group, nqb - level * p.group);
-    if (g.blocks <= 0) return false;
-    g.units = (p.g * g.blocks + 1) / 2;
+    if (g.blocks <= 0 || (MODE == kShared && x.kl == 0)) return false;
     g.sinks = 0;
     g.low = 0;
-    if (p.window > 0) {
-        g.low = max(0, x.kl - x.ql + level * p.group * kRows - p.window + 1) / kTok;
+    if (MODE != kShared && p.window > 0) {
+        g.low = max(0, x.kl - x.ql + first * kRows - p.window + 1) / kTok;
         g.sinks = min(ceil_div(p.sinks, kTok), g.low);
     }
-    const int n = stages_to(g, key_end(p, x, level * p.group + g.blocks - 1));
+    const int n = stages_to(g, key_end<MODE>(p, x, first + g.blocks - 1));
     g.np = p.P > 0 && n > p.P ? ceil_div(n, p.P) : 1;
+    g.pairs = MODE != kHeads && g.blocks == 1 && g.np > 1;
     return true;
 }
 
@@ -209,38 +221,44 @@ __device__ __forceinline__ int shared_tokens(const PromptParams& p, int s) {
     int lo = 0, hi = p.S;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(p.query_start + mid) <= s) lo = mid; else hi = mid;
+        if (load_behind_wait(p.query_start + mid) <= s) lo = mid; else hi = mid;
     }
     Seq x;
-    return p.S > 0 && sequence<true>(p, lo, x) && s >= x.q0 && s < x.q0 + x.ql ? x.kl : 0;
+    return p.S > 0 && sequence<kShared>(p, lo, x) && s >= x.q0 && s < x.q0 + x.ql ? x.kl : 0;
 }
 
-// A group's block ids, stage by stage: 32 entries of the table at a time, one
-// per lane, the next 32 on their way.
+// A group's block ids, stage by stage, of one run of stages or two that are
+// `apart` stages apart: 32 entries of the table at a time, one per lane, the
+// next 32 on their way.
 struct BlockIds {
     const int32_t* row;
-    int blocks, next, tab, tab_next;      // blocks of the group; the next stage's first
+    int blocks, next[2], tab[2], tab_next[2];      // blocks of the group; a run's next one and its entries
     __device__ __forceinline__ int load(int at) const {
         const int b = at + (int)(threadIdx.x & 31);
         return b < blocks ? __ldg(row + b) : 0;
     }
-    __device__ __forceinline__ void start(const PromptParams& p, int member, int n, int stage) {
+    __device__ __forceinline__ void start(const PromptParams& p, int member, int n, int stage, int apart) {
         row = p.tables + (size_t)member * p.MB;
         blocks = n;
-        next = stage * (kTok / p.bs);
-        tab = load(next & ~31);
-        tab_next = load((next & ~31) + 32);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            next[r] = (stage + r * apart) * (kTok / p.bs);
+            if (r > 0 && apart == 0) break;
+            tab[r] = load(next[r] & ~31);
+            tab_next[r] = load((next[r] & ~31) + 32);
+        }
     }
-    // lane i: block i of the stage's 8 or 4; -1 past the group's last, -2 out of the pool
-    __device__ __forceinline__ int stage(const PromptParams& p) {
+    // the next stage of run r; lane i: block i of its 8 or 4; -1 past the group's last, -2 out of the pool
+    __device__ __forceinline__ int stage(const PromptParams& p, int r) { return r ? take(p, next[1], tab[1], tab_next[1]) : take(p, next[0], tab[0], tab_next[0]); }
+    __device__ __forceinline__ int take(const PromptParams& p, int& at, int& now, int& then) {
         const int n = kTok / p.bs, i = threadIdx.x & 31;
-        int pb = __shfl_sync(0xffffffffu, tab, (next + i) & 31);
-        if (i >= n || next + i >= blocks) pb = -1;
+        int pb = __shfl_sync(0xffffffffu, now, (at + i) & 31);
+        if (i >= n || at + i >= blocks) pb = -1;
         else if (pb < 0 || pb >= p.NB) pb = -2;
-        next += n;
-        if ((next & 31) == 0) {
-            tab = tab_next;
-            tab_next = load(next + 32);
+        at += n;
+        if ((at & 31) == 0) {
+            now = then;
+            then = load(at + 32);
         }
         return pb;
     }
@@ -258,11 +276,12 @@ __device__ __forceinline__ void load_blocks(const PromptParams& p, const CUtenso
     if (b < kTok / p.bs && id >= 0) tensor_load_2d(tile + h * (kTok * 128) + b * p.bs * 128, map, kvh * D + h * 64, id * p.bs, full);
 }
 
-template <int D, bool SHARED>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D>;
+    constexpr bool SHARED = MODE == kShared, PACKED = MODE != kHeads;
     constexpr int NK = C::kKItems, NV = C::kVItems;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t ctl = smem_addr(smem_raw);
@@ -326,11 +345,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
     if constexpr (SHARED) {
-        // where each sequence's own part begins, for the kernels behind this one
-        for (int s = blockIdx.x * kThreads + tid; s < p.Tq; s += gridDim.x * kThreads) p.begin[s] = shared_tokens(p, s);
+        // where each sequence's own part begins, and the longest one, for the kernels behind this one
+        int own = 0;
+        for (int s = blockIdx.x * kThreads + tid; s < p.Tq; s += gridDim.x * kThreads) {
+            const int begin = shared_tokens(p, s);
+            p.begin[s] = begin;
+            own = max(own, min(load_behind_wait(p.lens + s), p.max_ctx) - begin);
+        }
+        own = __reduce_max_sync(0xffffffffu, own);
+        if (lane == 0 && own > 0) atomicMax(p.own_max, own);
     }
     // the first key of stage j of a unit's list
     auto stage_key = [](int j, int sinks, int low) { return (j < sinks ? j : j - sinks + low) * kTok; };
+    // Stages of a unit whose tiles take c0 and c1 of them: the same ones, or
+    // (paired partitions, c0 >= c1) each its own, in turn.  order: which of the
+    // unit's stages tile t's stage j is; turn: the other way round, as the
+    // tile's stage, plus p.P in tile 1's.
+    auto count = [](bool pair, int c0, int c1) { return PACKED && pair ? c0 + c1 : max(c0, c1); };
+    auto order = [](bool pair, int c1, int t, int j) { return PACKED && pair ? (j < c1 ? 2 * j + t : c1 + j) : j; };
+    auto turn = [&](bool pair, int c1, int m) {
+        return PACKED && pair ? (m < 2 * c1 ? m / 2 + (m & 1) * p.P : m - c1) : m;
+    };
     // A parity wait is exact while the barrier is within one phase of the
     // awaited one; every wait below is by construction.  K_j and V_j sit in
     // slots j % NK, j % NV (j counted over the block's stages); the per-tile
@@ -341,15 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // the highest query block group of any sequence
         int level = 0;
-        for (int s = lane; s < p.S; s += 32) {
-            Seq x;
-            if (sequence<SHARED>(p, s, x)) level = max(level, SHARED ? 1 : ceil_div(x.ql, p.group * kRows));
-            else if (blockIdx.x == 0) report(p.err, PKV_DEVERR_QUERY_LEN);
-        }
-        level = __reduce_max_sync(0xffffffffu, level) - 1;
         // this lane's sequence of the current 32, its group at this level, and the units up to its own
         Seq x{};
         Group gr{};
+        bool there = false;
+        for (int s = lane; s < p.S; s += 32) {
+            there = sequence<MODE>(p, s, x);
+            if (there) level = max(level, PACKED ? 1 : ceil_div(x.ql, p.group * kRows));
+            else if (blockIdx.x == 0) report(p.err, PKV_DEVERR_QUERY_LEN);
+        }
+        level = __reduce_max_sync(0xffffffffu, level) - 1;
         int at = -32;
         long long before = 0, mine = 0, upto = 0, total = 0;
         auto next_batch = [&]() -> bool {
@@ -361,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (level < 0) return false;
             mine = 0;
-            if (at + lane < p.S && sequence<SHARED>(p, at + lane, x) && group_of<SHARED>(p, x, level, gr))
-                mine = (long long)p.Hkv * gr.np * gr.units;
+            if (p.S > 32) there = at + lane < p.S && sequence<MODE>(p, at + lane, x);
+            if (there && group_of<MODE>(p, x, level, gr)) mine = (long long)p.Hkv * gr.per_head();
             upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -390,22 +426,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int owner = __ffs(__ballot_sync(0xffffffffu, ticket < before + upto)) - 1;
             int4 e0, e1, e2, e3;
             if (lane == owner) {
-                const int rel = (int)(ticket - before - (upto - mine)), per = gr.np * gr.units;
-                const int kvh = rel / per, part = (rel - kvh * per) / gr.units, u = rel - kvh * per - part * gr.units;
+                const int rel = (int)(ticket - before - (upto - mine)), per = gr.per_head(), kvh = rel / per;
+                int part = gr.pairs ? 2 * (rel - kvh * per) : (rel - kvh * per) / gr.units;
+                const int u = gr.pairs ? 0 : rel - kvh * per - part * gr.units;
                 const int j0 = gr.np > 1 ? part * p.P : 0, cap = gr.np > 1 ? p.P : 0x7fffffff;
+                // the tiles' query blocks (packed: tiles) and heads; -1: no second tile; packed, 1: paired partitions
                 int b0 = 2 * u, h0 = 0, b1 = 2 * u + 1, h1 = 2 * u + 1 < gr.blocks ? 0 : -1;
-                int n0 = ceil_div(x.kl, kTok), n1 = n0;
-                if constexpr (!SHARED) {
+                if constexpr (!PACKED) {
                     b0 = level * p.group + 2 * u / p.g;
                     h0 = 2 * u % p.g;
                     b1 = level * p.group + (2 * u + 1) / p.g;
                     h1 = 2 * u + 1 < p.g * gr.blocks ? (2 * u + 1) % p.g : -1;
-                    n0 = stages_to(gr, key_end(p, x, b0));
-                    n1 = stages_to(gr, key_end(p, x, b1));
+                }
+                const int n0 = stages_to(gr, key_end<MODE>(p, x, b0)) - j0;
+                int n1 = stages_to(gr, key_end<MODE>(p, x, b1)) - j0;
+                if (gr.pairs) {
+                    b1 = 0;
+                    h1 = part + 1 < gr.np ? 1 : -1;
+                    n1 = n0 - p.P;
                 }
                 e0 = make_int4(x.q0, x.k0, x.ql, x.kl);
                 e1 = make_int4(kvh, gr.np, part, j0);
-                e2 = make_int4(gr.sinks, max(gr.low, gr.sinks), min(max(n0 - j0, 0), cap), h1 < 0 ? 0 : min(max(n1 - j0, 0), cap));
+                e2 = make_int4(gr.sinks, max(gr.low, gr.sinks), min(max(n0, 0), cap), h1 < 0 ? 0 : min(max(n1, 0), cap));
                 e3 = make_int4(b0, h0, b1, h1);
                 int4* e = ring + 4 * slot;
                 e[0] = e0;
@@ -417,18 +459,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int k0 = __shfl_sync(0xffffffffu, e0.y, owner), kvh = __shfl_sync(0xffffffffu, e1.x, owner);
             const int j0 = __shfl_sync(0xffffffffu, e1.w, owner), sinks = __shfl_sync(0xffffffffu, e2.x, owner);
             const int low = __shfl_sync(0xffffffffu, e2.y, owner);
-            const int n = max(__shfl_sync(0xffffffffu, e2.z, owner), __shfl_sync(0xffffffffu, e2.w, owner));
+            const int c1 = __shfl_sync(0xffffffffu, e2.w, owner);
+            const bool pair = PACKED && __shfl_sync(0xffffffffu, e3.w, owner) > 0;
+            const int n = count(pair, __shfl_sync(0xffffffffu, e2.z, owner), c1);
             BlockIds ids;
             if constexpr (SHARED)
-                ids.start(p, __shfl_sync(0xffffffffu, e0.x, owner), __shfl_sync(0xffffffffu, e0.w, owner) / p.bs, j0);
+                ids.start(p, __shfl_sync(0xffffffffu, e0.x, owner), __shfl_sync(0xffffffffu, e0.w, owner) / p.bs, j0,
+                          pair ? p.P : 0);
             // the next ticket, on its way while the tiles are requested
-            if (p.sched != nullptr) {
-                long long v = 0;
-                if (lane == 0) v = (long long)atomicAdd(reinterpret_cast<unsigned long long*>(p.sched), 1ull);
-                ticket = (long long)gridDim.x + __shfl_sync(0xffffffffu, v, 0);
-            } else {
-                ticket += gridDim.x;
-            }
+            long long claimed = 0;
+            if (p.sched != nullptr && lane == 0)
+                claimed = (long long)atomicAdd(reinterpret_cast<unsigned long long*>(p.sched), 1ull);
             for (int j = 0; j < n; ++j, ++g) {
                 if (g >= (uint32_t)NK) ok = wait(bar(kKEmpty, g % NK), (g / NK - 1) & 1, true);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -437,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if constexpr (SHARED) {
                     // which of the stage's tokens there are: a block whose id is out of the pool is absent
-                    const int pb = ids.stage(p);
+                    const int pb = ids.stage(p, pair && j < 2 * c1 ? j & 1 : 0);
                     const uint32_t there = __ballot_sync(0xffffffffu, pb >= 0);
                     if (pb == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
                     if (lane < 4) {
@@ -452,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     const uint32_t full = bar(kKFull, g % NK);
                     mbar_arrive_expect_tx(full, C::kItemBytes);
-                    const int row = k0 + stage_key(j0 + j, sinks, low);
+                    const int row = k0 + stage_key(j0 + turn(pair, c1, j), sinks, low);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
                         tensor_load_2d(ktile(g) + h * (kTok * 128), &kmap, kvh * D + h * 64, row, full);
@@ -460,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             if (bad) break;
+            ticket = p.sched != nullptr ? (long long)gridDim.x + __shfl_sync(0xffffffffu, claimed, 0) : ticket + gridDim.x;
             ++un;
         }
         // copies still in flight land before the block leaves
@@ -483,25 +525,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
             const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
+            const bool pair = PACKED && ring[4 * slot + 3].w > 0;
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
             if (e1.x < 0) break;
-            const int n = max(e2.z, e2.w);
+            const int n = count(pair, e2.z, e2.w);
             BlockIds ids;
-            if constexpr (SHARED) ids.start(p, e0.x, e0.w / p.bs, e1.w);
+            if constexpr (SHARED) ids.start(p, e0.x, e0.w / p.bs, e1.w, pair ? p.P : 0);
             for (int j = 0; j < n; ++j, ++g) {
                 if (g >= (uint32_t)NV) ok = wait(bar(kVEmpty, g % NV), (g / NV - 1) & 1, true);
                 if (__any_sync(0xffffffffu, !ok)) {
                     bad = true;
                     break;
                 }
-                const int key = stage_key(e1.w + j, e2.x, e2.y);
+                const int key = stage_key(e1.w + turn(pair, e2.w, j), e2.x, e2.y);
                 // rows of the tile, in eighths (SHARED: a block or half of one) or counted, that hold something
                 const int here = e0.w - key;
                 uint32_t there = 0xffu;
                 int pb = 0;
                 if constexpr (SHARED) {
-                    pb = ids.stage(p);
+                    pb = ids.stage(p, pair && j < 2 * e2.w ? j & 1 : 0);
                     there = __ballot_sync(0xffffffffu, pb >= 0);
                 }
                 const bool part = SHARED ? there != (p.bs == 16 ? 0xffu : 0xfu) : here < kTok;
@@ -561,10 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bad = true;
                     break;
                 }
-                if constexpr (SHARED) {
+                if constexpr (PACKED) {
                     DecodeParams q{};
                     q.q = p.q;
-                    q.Hq = p.Hq;
+                    q.Hq = (int)(p.q_stride / D);                // (heads from one token to the next)
                     q.g = p.g;
                     const int r0 = (t == 0 ? e3.x : e3.z) * kRows;
                     load_q_rows<D, kRows>(q, e0.x, e1.x, r0, 0, kRows, e0.z * p.g - r0, qbuf(t));
@@ -643,48 +686,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c[2] = {__shfl_sync(0xffffffffu, ring[4 * slot + 2].z, 0),
                               __shfl_sync(0xffffffffu, ring[4 * slot + 2].w, 0)};
             const int n = max(c[0], c[1]);
+            const bool pair = PACKED && __shfl_sync(0xffffffffu, ring[4 * slot + 3].w, 0) > 0;
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
             if (kvh < 0) break;
-            if (n > 0) {
-                ok = all(bar(kKFull, g % NK), (g / NK) & 1);
+            auto at = [&](int t, int j) { return g + order(pair, c[1], t, j); };
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (c[t] == 0 || !ok) continue;
-                    ok = all(bar(kQFull, t), qu[t] & 1);
-                    // the tile's last P . V has read the buffer
-                    if (ok && gt[t] > 0) ok = all(bar(kPVDone, t), (gt[t] - 1) & 1);
-                    if (ok) issue_s(t, g, c[t] == 1);
-                }
+            for (int t = 0; t < 2; ++t) {
+                if (c[t] == 0 || !ok) continue;
+                const uint32_t s0 = at(t, 0);
+                ok = all(bar(kKFull, s0 % NK), (s0 / NK) & 1) && all(bar(kQFull, t), qu[t] & 1);
+                // the tile's last P . V has read the buffer
+                if (ok && gt[t] > 0) ok = all(bar(kPVDone, t), (gt[t] - 1) & 1);
                 if (!ok) break;
-                release(bar(kKEmpty, g % NK));
+                issue_s(t, s0, c[t] == 1);
+                if (pair) release(bar(kKEmpty, s0 % NK));
             }
-            for (int j = 0; j < n && ok; ++j, ++g) {
-                ok = all(bar(kVFull, g % NV), (g / NV) & 1);
+            if (!ok) break;
+            if (n > 0 && !pair) release(bar(kKEmpty, g % NK));
+            for (int j = 0; j < n && ok; ++j) {
                 bool next_k = false;
+                if (!pair) ok = all(bar(kVFull, (g + j) % NV), ((g + j) / NV) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j >= c[t] || !ok) continue;
-                    ok = all(bar(kPFull, t), gt[t] & 1);
+                    const uint32_t s0 = at(t, j);
+                    if (pair) ok = all(bar(kVFull, s0 % NV), (s0 / NV) & 1);
+                    ok = ok && all(bar(kPFull, t), gt[t] & 1);
                     if (!ok) break;
-                    issue_pv(t, g, 0, j == 0);
+                    issue_pv(t, s0, 0, j == 0);
                     ok = all(bar(kPFull2, t), gt[t] & 1);
                     if (!ok) break;
-                    issue_pv(t, g, 1, false);
+                    issue_pv(t, s0, 1, false);
+                    if (pair) release(bar(kVEmpty, s0 % NV));
                     if (j + 1 < c[t]) {
                         // the next S_t overwrites P_t: only after P_t . V_j is done
-                        if (!next_k) ok = all(bar(kKFull, (g + 1) % NK), ((g + 1) / NK) & 1);
+                        const uint32_t s1 = at(t, j + 1);
+                        if (!next_k || pair) ok = all(bar(kKFull, s1 % NK), (s1 / NK) & 1);
                         next_k = true;
                         ok = ok && all(bar(kPVDone, t), gt[t] & 1);
                         if (!ok) break;
-                        issue_s(t, g + 1, j + 2 == c[t]);
+                        issue_s(t, s1, j + 2 == c[t]);
+                        if (pair) release(bar(kKEmpty, s1 % NK));
                     }
                     ++gt[t];
                 }
                 if (!ok) break;
-                release(bar(kVEmpty, g % NV));
-                if (j + 1 < n) release(bar(kKEmpty, (g + 1) % NK));
+                if (!pair) {
+                    release(bar(kVEmpty, (g + j) % NV));
+                    if (j + 1 < n) release(bar(kKEmpty, (g + j + 1) % NK));
+                }
             }
+            g += count(pair, c[0], c[1]);
             if (!ok) break;
             for (int t = 0; t < 2; ++t) qu[t] += c[t] > 0;
             ++un;
@@ -713,8 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e1.x < 0) break;
             ++un;
             const int head = t == 0 ? e3.y : e3.w, n = t == 0 ? e2.z : e2.w;
-            const uint32_t stages = gs;
-            gs += max(e2.z, e2.w);
+            const bool pair = PACKED && e3.w > 0;
+            const uint32_t stages = gs;                          // the unit's first in the block's count (SHARED's masks)
+            gs += count(pair, e2.z, e2.w);
             if (head < 0) continue;                              // the unit has one tile
             const int block = t == 0 ? e3.x : e3.z;
             const int ql = e0.z, kl = e0.w;
@@ -722,20 +776,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool rv = qi < ql;
             int first = p.causal ? kl - ql + block * kRows : kl - 1;             // position of the tile's first row
             int pos = p.causal ? first + i : kl - 1;
-            const int far = p.causal ? first + kRows - 1 : kl - 1;               // and of its last
-            if constexpr (SHARED) {
-                rv = qi / p.g < ql;
+            int far = p.causal ? first + kRows - 1 : kl - 1;               // and of its last
+            if constexpr (PACKED) {
                 hh = qi % p.g;
                 qi /= p.g;
+                rv = qi < ql;
+                first = p.causal ? kl - ql + block * kRows / p.g : kl - 1;
+                pos = p.causal ? kl - ql + qi : kl - 1;
+                far = p.causal ? kl - ql + (block * kRows + kRows - 1) / p.g : kl - 1;
+            }
+            if constexpr (SHARED) {
                 // a member that ends inside the shared blocks sees its own tokens only
                 pos = rv ? min(__ldg(p.lens + e0.x + qi), kl) - 1 : kl - 1;
                 first = (int)__reduce_min_sync(0xffffffffu, (unsigned)max(pos + 1, 0)) - 1;
             }
+            const int j0 = e1.w + (pair && t ? p.P : 0);         // the tile's first stage
             const bool flip = !(p.scale_log2 > 0.f);
             const float scl = flip ? 1.f : p.scale_log2;
             float m_ref = -CUDART_INF_F, l = 0.f;
-            uint32_t e4 = stages;                                // the stage in the block's count (SHARED's masks)
-            for (int j = 0; j < n; ++j, ++gt, ++e4) {
+            for (int j = 0; j < n; ++j, ++gt) {
                 ok = wait(bar(kSFull, t), gt & 1, true);
                 if (__any_sync(0xffffffffu, !ok)) {
                     bad = true;
@@ -746,12 +805,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int w = 0; w < kTok / 32; ++w) umma::tmem_ld32(s_col + 32 * w, sr[w]);
                 umma::tmem_wait_ld();
-                const int key = stage_key(e1.w + j, e2.x, e2.y);
+                const int key = stage_key(j0 + j, e2.x, e2.y);
+                const uint32_t* there = masks + 4 * ((stages + order(pair, e2.w, t, j)) & 7);
                 bool whole = key + kTok - 1 <= min(first, kl - 1) &&
                              (p.window == 0 || key + kTok <= p.sinks || key > far - p.window);
                 if constexpr (SHARED) {
-                    const uint32_t* m = masks + 4 * (e4 & 7);
-                    whole = whole && (m[0] & m[1] & m[2] & m[3]) == 0xffffffffu;
+                    whole = whole && (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
                 }
                 if (flip) {
 #pragma unroll
@@ -765,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int w = 0; w < kTok / 32; ++w) {
                         const int v0 = key + 32 * w;
                         uint32_t seen = bits_below(min(pos, kl - 1) + 1 - v0);
-                        if constexpr (SHARED) seen &= masks[4 * (e4 & 7) + w];
+                        if constexpr (SHARED) seen &= there[w];
                         else if (p.window > 0) seen &= ~bits_between(v0, p.sinks, pos - p.window + 1);
                         if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
 #pragma unroll
@@ -842,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, !ok)) break;
                 umma::fence_after_sync();
             }
-            const int np = e1.y;
+            const int np = e1.y, part = e1.z + (pair && t ? 1 : 0);
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
@@ -862,12 +921,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + hrow * D + col;
                     store_row32(dst, ov, f, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0);
                 } else {
-                    store_part32(p.part_acc + (hrow * p.Pmax + e1.z) * D + col, ov,
+                    store_part32(p.part_acc + (hrow * p.Pmax + part) * D + col, ov,
                                  (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
                 }
             }
             if (rv && (SHARED || np > 1)) {
-                const size_t u = hrow * p.Pmax + e1.z;
+                const size_t u = hrow * p.Pmax + part;
                 p.part_ml[2 * u] = m_ref;
                 p.part_ml[2 * u + 1] = l;
             }
@@ -883,11 +942,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool SHARED>
+template <int D, int MODE>
 cudaError_t launch_attend(const PromptParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           long long units, int num_sms, cudaStream_t st) {
     using C = Cfg<D>;
-    auto kern = attend_kernel<D, SHARED>;
+    auto kern = attend_kernel<D, MODE>;
     // the register shares must fit in what the block is launched with
     // (setmaxnreg waits forever otherwise): checked once, on the binary
     static std::once_flag checked;

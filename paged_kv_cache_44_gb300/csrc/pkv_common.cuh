@@ -25,6 +25,21 @@ struct E4M3 { using T = uint8_t; static constexpr int bytes = 1; };
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
 
+// Loads that stay behind pdl_wait().  __ldg promises data that nothing writes
+// while the kernel runs, so the compiler may move it up, past the wait too,
+// where the address does not depend on an earlier load: a length or a start that
+// the previous kernel of the stream writes would then be read too early.
+__device__ __forceinline__ int32_t load_behind_wait(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int64_t load_behind_wait(const int64_t* p) {
+    int64_t v;
+    asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // Record the first device-side problem; never traps.
 __device__ __forceinline__ void report(int32_t* err, int code) {
     if (err != nullptr) atomicCAS(err, 0, code);

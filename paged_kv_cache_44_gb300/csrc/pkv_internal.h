@@ -131,6 +131,7 @@ struct PromptParams {
     long long q_stride, k_stride, v_stride;
     int S, Tq, Tk, max_q, max_k, Hq, Hkv, g;
     int group;                // query blocks whose tiles are paired (prompt_group)
+    int packed;               // tiles of (query, head) rows; else of 128 queries of a head
     int causal, window, sinks;
     int P, Pmax;              // stages per partition (0: no split), partial results per row
     float scale_log2;
@@ -139,7 +140,8 @@ struct PromptParams {
     const int32_t* tables;    // [Tq][MB]
     const int32_t* lens;      // [Tq]
     int32_t* begin;           // [Tq]: written: the tokens a sequence shares
-    int MB, bs, NB;
+    int* own_max;             // raised to the most tokens a sequence has of its own (0 between calls)
+    int MB, bs, NB, max_ctx;
 };
 // an odd number of heads per K/V head pairs the tiles of two query blocks
 inline int prompt_group(int g) { return g % 2 ? 2 : 1; }
@@ -210,6 +212,7 @@ struct DecodeParams {
     // tokens, rows of score_width(g) heads, [S][Hkv * head sets][max_ctx]
     float* logits;
     const int32_t* begin;     // kSuffix: [S]: tokens before the ones this call attends to, whole blocks
+    const int* own_max;       // kSuffix: the most tokens a sequence has behind them
 };
 
 struct EvictParams {

@@ -7,7 +7,7 @@ namespace pkv {
 namespace {
 
 // The merge of a launch's partitions, one warp per (query, head).
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant__ PromptParams p) {
     constexpr int E = D / 32;
     pdl_trigger();
@@ -20,11 +20,12 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
     int lo = 0, hi = p.S;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(p.query_start + mid) <= tq) lo = mid; else hi = mid;
+        if (load_behind_wait(p.query_start + mid) <= tq) lo = mid; else hi = mid;
     }
     Seq x;
     Group g;
-    if (!sequence<false>(p, lo, x) || tq < x.q0 || tq >= x.q0 + x.ql || !group_of<false>(p, x, (tq - x.q0) / (p.group * kRows), g) || g.np <= 1)
+    if (!sequence<MODE>(p, lo, x) || tq < x.q0 || tq >= x.q0 + x.ql ||
+        !group_of<MODE>(p, x, MODE == kPacked ? 0 : (tq - x.q0) / (p.group * kRows), g) || g.np <= 1)
         return;
     float acc[E];
     const size_t u0 = (size_t)gw * p.Pmax;
@@ -38,19 +39,26 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
     else *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
-template <int D>
-cudaError_t launch_prompt_d(const PromptParams& p, int num_sms, cudaStream_t st) {
+template <int D, int MODE>
+cudaError_t launch_mode(const PromptParams& p, int num_sms, cudaStream_t st) {
     CUtensorMap qmap, kmap, vmap;
     // (no keys at all: nothing is loaded through the maps of K and V)
-    if (!encode_rows_map(&qmap, p.q, p.Tq, p.Hq * D, p.q_stride, kRows) ||
-        !encode_rows_map(&kmap, p.Tk > 0 ? p.k : p.q, p.Tk, p.Hkv * D, p.k_stride, kTok) ||
+    if (!encode_rows_map(&kmap, p.Tk > 0 ? p.k : p.q, p.Tk, p.Hkv * D, p.k_stride, kTok) ||
         !encode_rows_map(&vmap, p.Tk > 0 ? p.v : p.q, p.Tk, p.Hkv * D, p.v_stride, kTok))
         return cudaErrorInvalidValue;
-    const long long units = (long long)p.S * p.Hkv * ceil_div(p.max_q, p.group * kRows) * ((p.g * p.group + 1) / 2) * p.Pmax;
-    const cudaError_t e = launch_attend<D, false>(p, qmap, kmap, vmap, units, num_sms, st);
+    if (MODE == kPacked) qmap = kmap;
+    else if (!encode_rows_map(&qmap, p.q, p.Tq, p.Hq * D, p.q_stride, kRows)) return cudaErrorInvalidValue;
+    const long long per_head = MODE == kPacked ? (ceil_div(p.max_q * p.g, kRows) + 1) / 2
+                                               : (long long)ceil_div(p.max_q, p.group * kRows) * ((p.g * p.group + 1) / 2);
+    const cudaError_t e = launch_attend<D, MODE>(p, qmap, kmap, vmap, (long long)p.S * p.Hkv * per_head * p.Pmax, num_sms, st);
     if (e != cudaSuccess || p.Pmax <= 1) return e;
     const long long rows = (long long)p.Tq * p.Hq;
-    return launch_pdl(prompt_merge_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, p);
+    return launch_pdl(prompt_merge_kernel<D, MODE>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, p);
+}
+
+template <int D>
+cudaError_t launch_prompt_d(const PromptParams& p, int num_sms, cudaStream_t st) {
+    return p.packed ? launch_mode<D, kPacked>(p, num_sms, st) : launch_mode<D, kHeads>(p, num_sms, st);
 }
 
 }  // namespace

@@ -57,14 +57,14 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     const int at = turn && !p.interleaved ? 8 * c : 16 * c;
     const int next = turn && !p.interleaved ? p.rot / 2 : 8;
     const long long t = blockIdx.x;
-    const long long pos = __ldg(p.positions + t);
+    const long long pos = load_behind_wait(p.positions + t);
     if (pos < 0 || pos >= p.max_position) {      // a padding token, or one past the table
         if (pos >= 0 && threadIdx.x == 0) report(p.err, PKV_DEVERR_POSITION);
         return;
     }
     long long slot = -1;
     if (p.key_cache != nullptr) {
-        slot = __ldg(p.slot_mapping + t);
+        slot = load_behind_wait(p.slot_mapping + t);
         if (slot >= (long long)p.NB * p.bs) {
             if (threadIdx.x == 0) report(p.err, PKV_DEVERR_SLOT);
             slot = -1;

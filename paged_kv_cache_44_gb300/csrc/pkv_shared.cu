@@ -24,11 +24,12 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const __grid_constant
     constexpr int E = D / 32, B = kMergeChunk;
     pdl_trigger();
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.own_max = 0;      // for the next call
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= (long long)p.Tq * p.Hq) return;
     const int s = (int)(row / p.Hq);
-    const int begin = __ldg(p.begin + s), n = min(max(__ldg(p.lens + s), 0), x.max_ctx) - begin;
+    const int begin = load_behind_wait(p.begin + s), n = min(max(load_behind_wait(p.lens + s), 0), x.max_ctx) - begin;
     int pre = 0, own = num_partitions(n, x.P, x.Q, 0);
     if (begin == 0) {
         if (own <= 1) return;                    // the decode has written it
@@ -99,7 +100,7 @@ cudaError_t launch_d(const PromptParams& p, const DecodeParams& d, int num_sms, 
     if (!prefill_encode_kv_map(&kmap, p.k, d) || !prefill_encode_kv_map(&vmap, p.v, d)) return cudaErrorInvalidValue;
     const long long tiles = ((long long)p.max_q * p.g + kRows - 1) / kRows;
     const long long units = (long long)p.S * p.Hkv * ((tiles + 1) / 2) * ceil_div(ceil_div(p.max_k, kTok), p.P > 0 ? p.P : 1 << 24);
-    return launch_attend<D, true>(p, kmap, kmap, vmap, units, num_sms, st);
+    return launch_attend<D, kShared>(p, kmap, kmap, vmap, units, num_sms, st);
 }
 
 }  // namespace

@@ -67,7 +67,7 @@ __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long lon
     if constexpr (WIN) n -= window_span(n - p.window, p.sinks, p.bs).gap;
     int begin = 0;
     if constexpr (SUFFIX) {
-        begin = __ldg(p.begin + x.s);
+        begin = load_behind_wait(p.begin + x.s);
         n = max(n - begin, 0);
     }
     x.np = num_partitions(n, p.P, p.Q, p.hold);

@@ -128,6 +128,27 @@ def test_window(shape, window, sinks, part):
     check(out, q, k, v, ql, kl, True, window, sinks, shape[2] ** -0.5)
 
 
+@pytest.mark.parametrize("shape", SHAPES + [(40, 1, 64), (200, 1, 128)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (False, 0, 0), (True, 30, 3), (True, 400, 140)])
+@pytest.mark.parametrize("part", [0, 128, 256, -1])
+def test_few_queries_each(shape, causal, window, sinks, part):
+    """At most 64 queries a sequence: tiles of (query, head) rows, one tile's partitions in pairs."""
+    ql = [1, 5, 64, 0, 17, 33, 2, 64, 30, 9]
+    kl = [700, 5, 64, 40, 17, 1031, 0, 1500, 29, 4000]
+    q, k, v = inputs(ql, kl, *shape, seed=20)
+    out = call(q, k, v, ql, kl, causal, window, sinks, part=part)
+    check(out, q, k, v, ql, kl, causal, window, sinks, shape[2] ** -0.5)
+
+
+def test_few_queries_of_a_projection():
+    """Rows that hold Q, K and V, and rows whose length is no multiple of a head (then tiles of 128 queries)."""
+    ql = [40, 3, 64]
+    for width in (12 + 4, 12 + 4.5):
+        rows = torch.randn(sum(ql), int(width * 64), device="cuda").to(BF)
+        q, k, v = (rows[:, a * 64:b * 64].unflatten(1, (b - a, 64)) for a, b in ((0, 12), (12, 14), (14, 16)))
+        check(call(q, k, v, ql, ql), q, k, v, ql, ql, True, 0, 0, 64 ** -0.5)
+
+
 def test_a_window_over_everything_changes_nothing():
     ql = [400, 129]
     q, k, v = inputs(ql, ql, 12, 2, 128, seed=4)
@@ -241,6 +262,22 @@ def test_repeats_are_equal_and_workspaces_are_reused():
     check(call(q, k, v, ql, kl, workspace=small), q, k, v, ql, kl, True, 0, 0, 128 ** -0.5)
     with pytest.raises(pkv.PkvError):
         call(q, k, v, ql, kl, workspace=small, part=128)
+
+
+def test_starts_written_by_the_kernel_before():
+    ql, kl = [3, 100, 40], [5000, 900, 40]
+    q, k, v = inputs(ql, kl, 12, 2, 128, seed=16)
+    want = call(q, k, v, ql, kl)
+    qs, ks, ws = starts(ql), starts(kl), pkv.make_prompt_workspace(3, 143, 100, 5000, 12, 2, 128)
+    a, b = qs.clone(), ks.clone()
+    outs = [torch.zeros_like(want) for _ in range(8)]
+    torch.cuda.synchronize()
+    for o in outs:
+        qs.zero_(), ks.zero_()
+        qs.copy_(a), ks.copy_(b)
+        pkv.prompt_attention(o, q, k, v, qs, 100, 128 ** -0.5, key_start=ks, max_key_len=5000, workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
 
 
 def test_graph_streams_and_two_at_once():

@@ -194,6 +194,22 @@ def test_graph_and_stream():
         assert torch.equal(bits(got.cpu()), bits(want))
 
 
+def test_positions_written_by_the_kernel_before():
+    c = case(64, 12, 2, 128, 128, 16, torch.bfloat16, torch.bfloat16, False, True, seed=10)
+    pos, slots = c["pos"].clone(), c["slots"].clone()
+    outs = [torch.zeros(64, 12, 128, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    for o in outs:
+        c["pos"].zero_(), c["slots"].fill_(-1)
+        c["pos"].copy_(pos), c["slots"].copy_(slots)
+        call(c, o, None, False)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.cpu()[c["live"]], c["rq"][c["live"]])
+    for got, want in zip(c["pools"], c["want"]):
+        assert torch.equal(got.cpu(), want)
+
+
 def test_pool_past_32_bits():
     """Slots whose byte offsets need more than 32 bits."""
     Hkv, d, bs = 8, 128, 32

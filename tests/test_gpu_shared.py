@@ -220,6 +220,25 @@ def test_workspaces_graph_and_streams():
     assert torch.equal(others[0], out) and torch.equal(others[1], out)
 
 
+def test_calls_one_behind_the_other():
+    """Queued calls of one workspace, whose longest own parts differ, and lengths that the kernel before them writes."""
+    cases = [Case([(640, [641, 660]), (32, [40, 50])], 12, 2, 128, 16, seed=12), Case([(64, [3000, 900]), (128, [200, 4000])], 12, 2, 128, 16, seed=13)]
+    ws = torch.zeros(max(pkv.shared_workspace_size(4, 2, 12, 2, 128, 16, *c.bounds, 64) for c in cases), dtype=torch.uint8, device="cuda")
+    outs = [[torch.zeros_like(c.q) for _ in range(6)] for c in cases]
+    kept = [(c.n.clone(), c.starts.clone(), c.shared.clone()) for c in cases]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for c, o, (n, starts, shared) in zip(cases, outs, kept):
+            c.n.zero_(), c.starts.zero_(), c.shared.zero_()
+            c.n.copy_(n), c.starts.copy_(starts), c.shared.copy_(shared)
+            pkv.paged_attention_decode_shared(o[i], c.q, c.kc, c.vc, c.tables, c.n, c.starts, c.shared, *c.bounds, c.scale,
+                                              partition_size=64, workspace=ws)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        c.check(o[0])
+        assert all(torch.equal(x, o[0]) for x in o)
+
+
 def test_with_the_block_pool():
     """Tables from the host block manager: requests that start with one cached prompt."""
     bs, Hq, Hkv, d = 16, 8, 2, 64
