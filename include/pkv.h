@@ -786,6 +786,10 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void
  * sees its own length.  A block id outside [0, NB) is reported and its tokens
  * are absent, as in the decode.
  *
+ * sharing (a pkv_sharing): PKV_SHARE_AUTO reads the shared blocks once where
+ * that is estimated to be faster (by the bounds: sequences on their own would
+ * read 256 MB or more of them again) and otherwise decodes every sequence on
+ * its own, without a look at the groups; PKV_SHARE_ALWAYS in any case.
  * partition_size: as in the decode, for the shared tokens (rounded up to 128)
  * and the others alike.  `workspace` must hold
  * pkv_decode_shared_workspace_size(...) bytes, its first 256 zero before first
@@ -793,8 +797,10 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void
  * says).  Supported: bf16 query and cache; anything else returns
  * PKV_ERR_UNSUPPORTED.
  */
+typedef enum { PKV_SHARE_AUTO = 0, PKV_SHARE_ALWAYS = 1 } pkv_sharing;
 PKV_API size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, int bs, int max_context_len,
-                                                int max_shared_len, int max_group_size, int partition_size);
+                                                int max_shared_len, int max_group_size, int partition_size,
+                                                int sharing);
 PKV_API pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_dtype q_dtype,
                                                      const void* key_cache, const void* value_cache,
                                                      pkv_dtype cache_dtype, const int32_t* block_tables, int MB,
@@ -802,7 +808,8 @@ PKV_API pkv_status pkv_paged_attention_decode_shared(void* out, const void* quer
                                                      const int32_t* shared_lens, int S, int G, int max_context_len,
                                                      int max_shared_len, int max_group_size, int Hq, int Hkv, int d,
                                                      int bs, int NB, float scale, int partition_size, void* workspace,
-                                                     size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream);
+                                                     size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream,
+                                                     int sharing);
 
 /* ------------------------------------------------------------------------
  * The calls of the four sections above with their arguments in one array,

@@ -171,10 +171,10 @@ def _load() -> ctypes.CDLL:
     lib.pkv_prompt_attention.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, vp, vp] + [i32] * 8 + \
         [f32, i32, i32, i32, i32, vp, sz, vp, vp]
     lib.pkv_prompt_attention.restype = i32
-    lib.pkv_decode_shared_workspace_size.argtypes = [i32] * 10
+    lib.pkv_decode_shared_workspace_size.argtypes = [i32] * 11
     lib.pkv_decode_shared_workspace_size.restype = sz
     lib.pkv_paged_attention_decode_shared.argtypes = [vp, vp, i32, vp, vp, i32, vp, i32, vp, vp, vp] + [i32] * 10 + \
-        [f32, i32, vp, sz, vp, vp]
+        [f32, i32, vp, sz, vp, vp, i32]
     lib.pkv_paged_attention_decode_shared.restype = i32
     lib.pkv_invoke.argtypes = [i32, ctypes.c_char_p]
     lib.pkv_invoke.restype = i32
@@ -897,17 +897,22 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
 
 # ---- decode of sequences that share blocks
 
+SHARING = {"auto": 0, "always": 1}
+
+
 def shared_workspace_size(S: int, G: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, max_shared_len: int,
-                          max_group_size: int, partition_size: int = 0) -> int:
+                          max_group_size: int, partition_size: int = 0, sharing: str = "auto") -> int:
     return int(lib.pkv_decode_shared_workspace_size(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len,
-                                                    max_group_size, partition_size))
+                                                    max_group_size, partition_size, SHARING[sharing]))
 
 
 def make_shared_workspace(S: int, G: int, Hq: int, Hkv: int, d: int, bs: int, max_context_len: int, max_shared_len: int,
-                          max_group_size: int, partition_size: int = 0, device=None) -> torch.Tensor:
+                          max_group_size: int, partition_size: int = 0, sharing: str = "auto",
+                          device=None) -> torch.Tensor:
     """A workspace for paged_attention_decode_shared, its header zero (reused
     as make_window_workspace says)."""
-    n = shared_workspace_size(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size)
+    n = shared_workspace_size(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size,
+                              sharing)
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
     ws[:256] = 0
     return ws
@@ -918,12 +923,15 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
                                   group_start: torch.Tensor, shared_lens: torch.Tensor, max_context_len: int,
                                   max_shared_len: int, max_group_size: int, scale: float, partition_size: int = 0,
                                   workspace: Optional[torch.Tensor] = None, err_word: Optional[torch.Tensor] = None,
-                                  stream=None) -> torch.Tensor:
+                                  stream=None, sharing: str = "auto") -> torch.Tensor:
     """paged_attention_decode (bf16) of sequences in groups whose first blocks
     are the same: group i is the sequences group_start[i] .. group_start[i+1]
     (int32 [G+1]), and their first shared_lens[i] tokens (int32 [G], whole
     blocks) are read once, through the first one's table.  max_shared_len and
-    max_group_size (host) bound them."""
+    max_group_size (host) bound them.  sharing: "auto" (where little would be
+    read again, every sequence on its own) or "always"."""
+    if sharing not in SHARING:
+        raise ValueError(f"sharing must be one of {sorted(SHARING)}")
     S, Hq, d = shape = query.shape
     NB, bs, Hkv, d2 = pool = key_cache.shape
     q_dt, c_dt, G = query.dtype, key_cache.dtype, shared_lens.numel()
@@ -934,13 +942,14 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
         raise ValueError("group_start must be int32 [G + 1] and shared_lens int32 [G]")
     if workspace is None:
         workspace = _own_workspace(stream, make_shared_workspace, S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len,
-                                   max_group_size, partition_size, device=query.device)
+                                   max_group_size, partition_size, sharing, device=query.device)
     p_o, p_q, p_kc, p_vc, p_bt, p_cl, p_gs, p_sl, p_ws, p_err, p_st = _pointers(
         stream, out, query, key_cache, value_cache, block_tables, context_lens, group_start, shared_lens, workspace,
         err_word)
     _decode_shared(
         p_o, p_q, dtype_code(q_dt), p_kc, p_vc, dtype_code(c_dt), p_bt, MB, p_cl, p_gs, p_sl, S, G, max_context_len,
-        max_shared_len, max_group_size, Hq, Hkv, d, bs, NB, scale, partition_size, p_ws, workspace.nbytes, p_err, p_st)
+        max_shared_len, max_group_size, Hq, Hkv, d, bs, NB, scale, partition_size, p_ws, workspace.nbytes, p_err, p_st,
+        SHARING[sharing])
     return out
 
 

@@ -1112,8 +1112,17 @@ bool shared_shape_ok(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, 
 
 constexpr int kMaxOwnParts = 96;
 
-// Whether the shared tokens are worth a launch of their own.
-bool shares_enough(int G, int max_shared, int max_group, int bs) { return G > 0 && max_shared >= bs && max_group > 1; }
+// Whether the shared tokens get a launch of their own: where sequences on
+// their own would read them from 256 MB on again (by the bounds).  Two more
+// launches take 15-20 us, about what HBM and L2 take for that: 64 sequences
+// sharing 2,048 tokens of 4 heads of 128 (264 MB) 42 us and 45 on their own,
+// 128 of them 48 and 64; 256 sharing 512 (267 MB) 64.5 and 61.4; 100 of 256
+// sharing 1,024 (207 MB, read from L2 while HBM is the bound) 342 and 325.
+constexpr long long kShareBytes = 256LL << 20;
+bool shares(int G, int max_shared, int max_group, int Hkv, int d, int bs, int sharing) {
+    if (G < 1 || max_shared < bs || max_group < 1) return false;
+    return sharing == PKV_SHARE_ALWAYS || (long long)G * (max_group - 1) * max_shared * Hkv * d * 4 >= kShareBytes;
+}
 
 SharedPlan choose_shared(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, int max_shared, int max_group, int req,
                          size_t room) {
@@ -1142,10 +1151,12 @@ SharedPlan choose_shared(int S, int G, int Hq, int Hkv, int d, int bs, int max_c
 extern "C" {
 
 size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, int bs, int max_context_len,
-                                        int max_shared_len, int max_group_size, int partition_size) {
-    if (!shared_shape_ok(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size)) return 0;
+                                        int max_shared_len, int max_group_size, int partition_size, int sharing) {
+    if (!shared_shape_ok(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size) ||
+        sharing < PKV_SHARE_AUTO || sharing > PKV_SHARE_ALWAYS)
+        return 0;
     const size_t plain = make_plan(S, Hq, d, max_context_len, resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size)).bytes;
-    if (!shares_enough(G, max_shared_len, max_group_size, bs)) return plain;
+    if (!shares(G, max_shared_len, max_group_size, Hkv, d, bs, sharing)) return plain;
     return max(plain, choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size,
                                     SIZE_MAX).bytes);
 }
@@ -1156,7 +1167,8 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_d
                                              const int32_t* shared_lens, int S, int G, int max_context_len,
                                              int max_shared_len, int max_group_size, int Hq, int Hkv, int d, int bs,
                                              int NB, float scale, int partition_size, void* workspace,
-                                             size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream) {
+                                             size_t workspace_bytes, int32_t* err_word, pkv_stream_t stream, int sharing) {
+    if (sharing < PKV_SHARE_AUTO || sharing > PKV_SHARE_ALWAYS) return PKV_ERR_INVALID_ARG;
     if (G < 0 || max_shared_len < 0 || max_shared_len > max_context_len || max_group_size < 0) return PKV_ERR_INVALID_ARG;
     if (q_dtype != PKV_BF16 || cache_dtype != PKV_BF16 || max_group_size > 65535 || G > 65535) return PKV_ERR_UNSUPPORTED;
     const pkv_status chk = check_decode_args(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,
@@ -1167,12 +1179,12 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_d
     if ((reinterpret_cast<uintptr_t>(group_start) & 3u) || (reinterpret_cast<uintptr_t>(shared_lens) & 3u))
         return PKV_ERR_INVALID_ARG;
     const size_t room = workspace_room(workspace, workspace_bytes);
-    const bool shares = shares_enough(G, max_shared_len, max_group_size, bs);
+    const bool share = shares(G, max_shared_len, max_group_size, Hkv, d, bs, sharing);
     SharedPlan sp{};
-    if (shares)
+    if (share)
         sp = choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size, room);
-    if (!shares || (partition_size == 0 && sp.bytes > room)) {
-        // nothing to share, or no room to: every sequence on its own
+    if (!share || (partition_size == 0 && sp.bytes > room)) {
+        // not enough to share, or no room to: every sequence on its own
         int P = resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size);
         P = fit_partition(P, max_context_len, partition_size, room, [&](int n) { return make_plan(S, Hq, d, max_context_len, n).bytes; });
         return pkv_paged_attention_decode_ex(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,

@@ -66,7 +66,8 @@ class Case:
         out = torch.full_like(self.q, 7.0)
         err = torch.zeros(1, dtype=torch.int32, device="cuda")
         pkv.paged_attention_decode_shared(out, self.q, self.kc, self.vc, self.tables, self.n, self.starts, self.shared,
-                                          *self.bounds, self.scale, partition_size=part, err_word=err, **kw)
+                                          *self.bounds, self.scale, partition_size=part, err_word=err,
+                                          **{"sharing": "always", **kw})
         torch.cuda.synchronize()
         assert int(err) == err_code
         return out
@@ -120,6 +121,20 @@ def test_long_document():
     c.check(c.run())
 
 
+def test_the_choice():
+    """auto: the plain decode where little is shared, bit for bit, and the same answer where much is."""
+    c = Case([(304, [305, 344, 304, 400])], 12, 2, 128, 16, seed=14)
+    plain = torch.zeros_like(c.q)
+    pkv.paged_attention_decode(plain, c.q, c.kc, c.vc, c.tables, c.n, c.bounds[0], c.scale)
+    assert torch.equal(c.run(sharing="auto"), plain)
+    c = Case([(4096, [4096 + i for i in range(40)])], 4, 4, 128, 16, seed=15)         # 327 MB read again
+    plain = torch.zeros_like(c.q)
+    pkv.paged_attention_decode(plain, c.q, c.kc, c.vc, c.tables, c.n, c.bounds[0], c.scale)
+    out = c.run(sharing="auto")
+    assert torch.equal(out, c.run()) and not torch.equal(out, plain)
+    c.check(out)
+
+
 def test_nothing_shared():
     """Groups that share nothing, or have one member, and no groups at all."""
     for groups in ([(0, [300, 200])], [(208, [300])], [(15, [300, 20])]):
@@ -128,7 +143,7 @@ def test_nothing_shared():
     c = Case([(64, [100, 200, 300])], 12, 2, 128, 16, seed=6)
     out = torch.zeros_like(c.q)
     empty = torch.zeros(1, dtype=torch.int32, device="cuda")
-    pkv.paged_attention_decode_shared(out, c.q, c.kc, c.vc, c.tables, c.n, empty, empty[:0], 300, 0, 0, c.scale)
+    pkv.paged_attention_decode_shared(out, c.q, c.kc, c.vc, c.tables, c.n, empty, empty[:0], 300, 0, 0, c.scale, sharing="always")
     c.check(out)
 
 
@@ -174,7 +189,7 @@ def test_growing_logits():
 def test_workspaces_graph_and_streams():
     c = Case([(640, [700, 900, 650, 641]), (128, [300, 400])], 12, 2, 128, 16, seed=10)
     S, Hq, Hkv, d = c.shape
-    ws = pkv.make_shared_workspace(S, 2, Hq, Hkv, d, 16, *c.bounds)
+    ws = pkv.make_shared_workspace(S, 2, Hq, Hkv, d, 16, *c.bounds, sharing="always")
     want = c.run(workspace=ws)
     c.check(want)
     for _ in range(3):
@@ -188,7 +203,7 @@ def test_workspaces_graph_and_streams():
 
     def step(to=out, space=ws, **kw):
         pkv.paged_attention_decode_shared(to, c.q, c.kc, c.vc, c.tables, c.n, c.starts, c.shared, *c.bounds, c.scale,
-                                          workspace=space, **kw)
+                                          workspace=space, sharing="always", **kw)
 
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -223,7 +238,7 @@ def test_workspaces_graph_and_streams():
 def test_calls_one_behind_the_other():
     """Queued calls of one workspace, whose longest own parts differ, and lengths that the kernel before them writes."""
     cases = [Case([(640, [641, 660]), (32, [40, 50])], 12, 2, 128, 16, seed=12), Case([(64, [3000, 900]), (128, [200, 4000])], 12, 2, 128, 16, seed=13)]
-    ws = torch.zeros(max(pkv.shared_workspace_size(4, 2, 12, 2, 128, 16, *c.bounds, 64) for c in cases), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(max(pkv.shared_workspace_size(4, 2, 12, 2, 128, 16, *c.bounds, 64, "always") for c in cases), dtype=torch.uint8, device="cuda")
     outs = [[torch.zeros_like(c.q) for _ in range(6)] for c in cases]
     kept = [(c.n.clone(), c.starts.clone(), c.shared.clone()) for c in cases]
     torch.cuda.synchronize()
@@ -232,7 +247,7 @@ def test_calls_one_behind_the_other():
             c.n.zero_(), c.starts.zero_(), c.shared.zero_()
             c.n.copy_(n), c.starts.copy_(starts), c.shared.copy_(shared)
             pkv.paged_attention_decode_shared(o[i], c.q, c.kc, c.vc, c.tables, c.n, c.starts, c.shared, *c.bounds, c.scale,
-                                              partition_size=64, workspace=ws)
+                                              partition_size=64, workspace=ws, sharing="always")
     torch.cuda.synchronize()
     for c, o in zip(cases, outs):
         c.check(o[0])

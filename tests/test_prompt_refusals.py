@@ -84,3 +84,42 @@ def test_prompt_binding():
                      ((q, q, k, k, qs.long(), 4, 1.0), {}), ((q, q, k, k, qs, 4, 1.0), dict(key_start=qs[:1]))]:
         with pytest.raises(ValueError):
             pkv.prompt_attention(*args, workspace=q, **kw)
+
+
+def _shared(out=A, q=2 * A, qd=1, kc=3 * A, vc=4 * A, cd=1, tables=5 * A, MB=100, lens=6 * A, gs=7 * A, sl=8 * A, S=4, G=2,
+            mx=1000, ms=500, mg=3, Hq=8, Hkv=2, d=128, bs=16, NB=200, scale=0.1, part=0, ws=9 * A, wsb=1 << 40, sharing=1):
+    return pkv.lib.pkv_paged_attention_decode_shared(out, q, qd, kc, vc, cd, tables, MB, lens, gs, sl, S, G, mx, ms, mg, Hq,
+                                                     Hkv, d, bs, NB, scale, part, ws, wsb, None, None, sharing)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=-1), 1), (dict(S=0), 0), (dict(S=65536), 2), (dict(G=-1), 1), (dict(G=65536), 2), (dict(mx=1601), 1), (dict(ms=-1), 1),
+    (dict(ms=1001), 1), (dict(mg=-1), 1), (dict(mg=65536), 2), (dict(qd=0), 2), (dict(cd=0), 2), (dict(cd=2), 2), (dict(d=96), 2),
+    (dict(bs=8), 2), (dict(Hq=9), 1), (dict(NB=0), 1), (dict(scale=float("nan")), 1), (dict(part=-2), 1), (dict(part=24), 1),
+    (dict(out=None), 1), (dict(lens=None), 1), (dict(gs=None), 1), (dict(sl=None), 1), (dict(gs=7 * A + 2), 1),
+    (dict(sl=8 * A + 1), 1), (dict(kc=3 * A + 8), 1), (dict(sharing=2), 1), (dict(sharing=-1), 1), (dict(ws=None, wsb=0), 3),
+    (dict(part=64, wsb=1000), 3), (dict(ws=9 * A + 8), 1)])
+def test_shared(kw, status):
+    assert _shared(**kw) == status
+
+
+def test_shared_workspace():
+    f = pkv.shared_workspace_size
+    plain = pkv.decode_workspace_size(64, 64, 8, 128, 16, 33792)
+    assert f(64, 4, 64, 8, 128, 16, 33792, 0, 0) == plain                     # nothing to share
+    assert f(4, 1, 8, 2, 128, 16, 500, 304, 4) == pkv.decode_workspace_size(4, 8, 2, 128, 16, 500)
+    assert f(4, 1, 8, 2, 128, 16, 500, 304, 4, sharing="always") >= 256 + 4 * 8 * 2 * 130 * 4
+    assert f(64, 4, 64, 8, 128, 16, 33792, 32768, 16) > 64 * 64 * 2 * 130 * 4
+    assert f(64, 4, 64, 8, 128, 16, 1000, 1001, 16) == 0 and f(64, -1, 64, 8, 128, 16, 1000, 100, 16) == 0
+    assert f(64, 4, 64, 8, 96, 16, 1000, 100, 16) == 0 and f(64, 4, 64, 8, 128, 16, 1000, 100, 16, 10) == 0
+
+
+def test_shared_binding():
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    kc, i = torch.zeros(8, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 4, dtype=torch.int32)
+    n, gs = i[0, :2].contiguous(), i[0, :3].contiguous()
+    for args, kw in [((q, q, kc, kc[:4], i, n, gs, n, 10, 0, 0, 1.0), {}), ((q, q, kc, kc, i, n, gs, gs, 10, 0, 0, 1.0), {}),
+                     ((q, q, kc, kc, i, n, gs.long(), n, 10, 0, 0, 1.0), {}), ((q, q, kc, kc, i[:1], n, gs, n, 10, 0, 0, 1.0), {}),
+                     ((q.float(), q, kc, kc, i, n, gs, n, 10, 0, 0, 1.0), {}), ((q, q, kc, kc, i, n, gs, n, 10, 0, 0, 1.0), dict(sharing="no"))]:
+        with pytest.raises(ValueError):
+            pkv.paged_attention_decode_shared(*args, workspace=q, **kw)
