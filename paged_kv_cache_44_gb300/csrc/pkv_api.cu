@@ -1124,6 +1124,17 @@ bool shares(int G, int max_shared, int max_group, int Hkv, int d, int bs, int sh
     return sharing == PKV_SHARE_ALWAYS || (long long)G * (max_group - 1) * max_shared * Hkv * d * 4 >= kShareBytes;
 }
 
+// Sequences on their own, as the windowed decode with everything in its window:
+// it splits a small launch further and merges within it.  Eight sequences of
+// 305..344 tokens, 2 K/V heads, 12.3 us and 22.5 by the plain decode; two of
+// 1,088, 4 heads, 14.3 and 20.5; 64 of 129..384, 4 heads, 18.4 and 22.5; but 64
+// of 513..640, 4 heads, 24.6 and 22.5, and two of 32,832, 2 heads, 32.8 and 28.7.
+bool as_window(int S, int Hq, int Hkv, int d, int bs, int max_ctx, int req) {
+    const long long sets = (long long)S * Hkv * ((Hq / Hkv + kHeadSet - 1) / kHeadSet);
+    return req == 0 && max_ctx > 0 &&
+           (resolve_partition(S, Hq, Hkv, d, bs, max_ctx, 0) == 0 || (max_ctx <= 1280 && sets < 152));
+}
+
 SharedPlan choose_shared(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, int max_shared, int max_group, int req,
                          size_t room) {
     // what a sequence has of its own: taken to be what the longest one would have beside the longest shared part
@@ -1155,7 +1166,9 @@ size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, in
     if (!shared_shape_ok(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size) ||
         sharing < PKV_SHARE_AUTO || sharing > PKV_SHARE_ALWAYS)
         return 0;
-    const size_t plain = make_plan(S, Hq, d, max_context_len, resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size)).bytes;
+    const size_t plain = as_window(S, Hq, Hkv, d, bs, max_context_len, partition_size)
+                             ? pkv_decode_window_workspace_size(S, Hq, Hkv, d, bs, max_context_len, max_context_len, 0, 0)
+                             : pkv_decode_workspace_size(S, Hq, Hkv, d, bs, max_context_len, partition_size);
     if (!shares(G, max_shared_len, max_group_size, Hkv, d, bs, sharing)) return plain;
     return max(plain, choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size,
                                     SIZE_MAX).bytes);
@@ -1185,6 +1198,11 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_d
         sp = choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size, room);
     if (!share || (partition_size == 0 && sp.bytes > room)) {
         // not enough to share, or no room to: every sequence on its own
+        if (as_window(S, Hq, Hkv, d, bs, max_context_len, partition_size))
+            return pkv_paged_attention_decode_window(out, query, q_dtype, key_cache, value_cache, cache_dtype,
+                                                     block_tables, MB, context_lens, S, max_context_len, Hq, Hkv, d, bs,
+                                                     NB, scale, 1.f, 1.f, max_context_len, 0, 0, workspace,
+                                                     workspace_bytes, err_word, stream, PKV_DECODE_AUTO);
         int P = resolve_partition(S, Hq, Hkv, d, bs, max_context_len, partition_size);
         P = fit_partition(P, max_context_len, partition_size, room, [&](int n) { return make_plan(S, Hq, d, max_context_len, n).bytes; });
         return pkv_paged_attention_decode_ex(out, query, q_dtype, key_cache, value_cache, cache_dtype, block_tables, MB,

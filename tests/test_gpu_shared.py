@@ -122,11 +122,13 @@ def test_long_document():
 
 
 def test_the_choice():
-    """auto: the plain decode where little is shared, bit for bit, and the same answer where much is."""
-    c = Case([(304, [305, 344, 304, 400])], 12, 2, 128, 16, seed=14)
-    plain = torch.zeros_like(c.q)
-    pkv.paged_attention_decode(plain, c.q, c.kc, c.vc, c.tables, c.n, c.bounds[0], c.scale)
-    assert torch.equal(c.run(sharing="auto"), plain)
+    """auto: a decode without a look at the groups where little is shared, and the shared one where much is."""
+    for groups in ([(304, [305, 344, 304, 400])], [(2048, [2050, 3000])], [(304, [1000 + i for i in range(100)])]):
+        c = Case(groups, 12, 2, 128, 16, seed=14)
+        out = c.run(sharing="auto")
+        c.check(out)
+        c.starts.fill_(-1)
+        assert torch.equal(c.run(sharing="auto"), out)
     c = Case([(4096, [4096 + i for i in range(40)])], 4, 4, 128, 16, seed=15)         # 327 MB read again
     plain = torch.zeros_like(c.q)
     pkv.paged_attention_decode(plain, c.q, c.kc, c.vc, c.tables, c.n, c.bounds[0], c.scale)

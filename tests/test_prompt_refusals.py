@@ -107,7 +107,8 @@ def test_shared_workspace():
     f = pkv.shared_workspace_size
     plain = pkv.decode_workspace_size(64, 64, 8, 128, 16, 33792)
     assert f(64, 4, 64, 8, 128, 16, 33792, 0, 0) == plain                     # nothing to share
-    assert f(4, 1, 8, 2, 128, 16, 500, 304, 4) == pkv.decode_workspace_size(4, 8, 2, 128, 16, 500)
+    assert f(4, 1, 8, 2, 128, 16, 5000, 304, 4) == pkv.decode_workspace_size(4, 8, 2, 128, 16, 5000)
+    assert f(4, 1, 8, 2, 128, 16, 500, 304, 4) == pkv.decode_window_workspace_size(4, 8, 2, 128, 16, 500, 500)
     assert f(4, 1, 8, 2, 128, 16, 500, 304, 4, sharing="always") >= 256 + 4 * 8 * 2 * 130 * 4
     assert f(64, 4, 64, 8, 128, 16, 33792, 32768, 16) > 64 * 64 * 2 * 130 * 4
     assert f(64, 4, 64, 8, 128, 16, 1000, 1001, 16) == 0 and f(64, -1, 64, 8, 128, 16, 1000, 100, 16) == 0
