@@ -61,7 +61,7 @@ constexpr int kSoftWarps = 8, kThreads = 384;
 constexpr int kKWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 11;
 constexpr float kRescaleLog2 = 8.f;
 constexpr long long kWaitLimit = 4000000000LL;    // ~2 s: a barrier that never completes
-constexpr uint32_t kTmemCols = 512;               // O_0, O_1, S_0, S_1
+constexpr uint32_t kTmemCols = 512;               // O_0, O_1, S_0, S_1; P_t over the first half of S_t
 __host__ __device__ constexpr uint32_t tmem_o(int t) { return 128u * t; }
 __host__ __device__ constexpr uint32_t tmem_s(int t) { return 256u + 128u * t; }
 // Registers: launched with kThreads x kLaunchRegs; the softmax warps raise
@@ -801,38 +801,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 umma::fence_after_sync();
-                uint32_t sr[kTok / 32][32];
-#pragma unroll
-                for (int w = 0; w < kTok / 32; ++w) umma::tmem_ld32(s_col + 32 * w, sr[w]);
-                umma::tmem_wait_ld();
                 const int key = stage_key(j0 + j, e2.x, e2.y);
                 const uint32_t* there = masks + 4 * ((stages + order(pair, e2.w, t, j)) & 7);
-                bool whole = key + kTok - 1 <= min(first, kl - 1) &&
+                bool whole = !flip && key + kTok - 1 <= min(first, kl - 1) &&
                              (p.window == 0 || key + kTok <= p.sinks || key > far - p.window);
-                if constexpr (SHARED) {
-                    whole = whole && (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
-                }
-                if (flip) {
-#pragma unroll
-                    for (int w = 0; w < kTok / 32; ++w)
-#pragma unroll
-                        for (int b = 0; b < 32; ++b) sr[w][b] = __float_as_uint(__uint_as_float(sr[w][b]) * p.scale_log2);
-                }
+                if constexpr (SHARED) whole = whole && (there[0] & there[1] & there[2] & there[3]) == 0xffffffffu;
                 if (!whole) {
-                    // -inf where this row does not see the key
-#pragma unroll
+                    // -inf where this row does not see the key, in place: few stages need it, and their code, a
+                    // word of 32 keys at a time, stays out of the others' way
+#pragma unroll 1
                     for (int w = 0; w < kTok / 32; ++w) {
                         const int v0 = key + 32 * w;
                         uint32_t seen = bits_below(min(pos, kl - 1) + 1 - v0);
                         if constexpr (SHARED) seen &= there[w];
                         else if (p.window > 0) seen &= ~bits_between(v0, p.sinks, pos - p.window + 1);
-                        if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+                        if (!flip && __all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+                        uint32_t x[32];
+                        umma::tmem_ld32(s_col + 32 * w, x);
+                        umma::tmem_wait_ld();
 #pragma unroll
-                            for (int b = 0; b < 32; ++b)
-                                if (!((seen >> b) & 1u)) sr[w][b] = 0xff800000u;
+                        for (int b = 0; b < 32; ++b) {
+                            if (flip) x[b] = __float_as_uint(__uint_as_float(x[b]) * p.scale_log2);
+                            if (!((seen >> b) & 1u)) x[b] = 0xff800000u;
                         }
+                        umma::tmem_st32(s_col + 32 * w, x);
                     }
+                    umma::tmem_wait_st();
                 }
+                uint32_t sr[kTok / 32][32];
+#pragma unroll
+                for (int w = 0; w < kTok / 32; ++w) umma::tmem_ld32(s_col + 32 * w, sr[w]);
+                umma::tmem_wait_ld();
                 float mx8[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mx8[k] = __uint_as_float(sr[0][k]);
@@ -904,26 +903,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int np = e1.y, part = e1.z + (pair && t ? 1 : 0);
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-            for (int c0 = 0; c0 < D / 32; ++c0) {
+            // (a loop: unrolled it is 4 KB of code that a unit runs once, and 64 x 512 tokens take 178 us, not 159)
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t ov[32];
                 if (n > 0) {
-                    umma::tmem_ld32(o_col + 32 * c0, ov);
-                    umma::tmem_wait_ld();
-                }
-                if (n == 0) {
+                    umma::tmem_ld32(o_col + c0, ov);
+                } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) ov[k] = 0u;
                 }
-                if (!rv) continue;
-                const int col = 32 * c0;
-                if (!SHARED && np == 1) {
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + hrow * D + col;
-                    store_row32(dst, ov, f, (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0);
-                } else {
-                    store_part32(p.part_acc + (hrow * p.Pmax + part) * D + col, ov,
-                                 (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
+                umma::tmem_wait_ld();
+                if (rv) {
+                    if (!SHARED && np == 1) {
+                        store_row32(static_cast<__nv_bfloat16*>(p.out) + hrow * D + c0, ov, f,
+                                    (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0);
+                    } else {
+                        store_part32(p.part_acc + (hrow * p.Pmax + part) * D + c0, ov,
+                                     (reinterpret_cast<uintptr_t>(p.part_acc) & 31u) == 0);
+                    }
                 }
+                __syncwarp();
             }
             if (rv && (SHARED || np > 1)) {
                 const size_t u = hrow * p.Pmax + part;
