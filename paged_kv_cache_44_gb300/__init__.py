@@ -783,10 +783,15 @@ def evict_tokens(token_slots: torch.Tensor, scores: torch.Tensor, num_tokens: to
 
 # ---- a prompt's way into the cache
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements from one token of a [T, H, d] tensor to the next; the heads of a token are contiguous."""
-    T, H, d = t.shape
+def _row_stride(t: Optional[torch.Tensor], shape: tuple, dt: torch.dtype) -> int:
+    """Elements from one token to the next of a tensor that must be [T, H, d]
+    of dtype dt with the heads of a token contiguous; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype != dt:
+        raise ValueError("query, key, value and the outputs must agree in tokens, heads, d and dtype")
     s0, s1, s2 = t.stride()
+    T, H, d = shape
     if s2 != 1 or (s1 != d and H > 1):
         raise ValueError("the heads of a token must be contiguous")
     return s0 if T > 1 else H * d
@@ -805,42 +810,46 @@ def rotary_kv_write(query: Optional[torch.Tensor], key: Optional[torch.Tensor], 
     Inputs and outputs may be slices of wider rows (one projection's Q, K and
     V side by side); q_out may be query, and k_out key.  Without query and
     q_out only K and V are taken, without caches only Q and K rotated."""
-    any_in = query if query is not None else key
-    if any_in is None or any_in.dim() != 3:
+    any_in = key if query is None else query
+    if any_in is None or any_in.dim() != 3 or (key is not None and key.dim() != 3):
         raise ValueError("rotary_kv_write takes query and/or key of three dimensions")
-    (T, _, d), dt = any_in.shape, any_in.dtype
-    Hq, Hkv = 0 if query is None else query.shape[1], 0 if key is None else key.shape[1]
+    q_shape, dt = any_in.shape, any_in.dtype
+    T, Hq, d = q_shape
+    k_shape = q_shape if key is None else key.shape
+    Hkv = 0 if key is None else k_shape[1]
+    if query is None:
+        Hq = 0
+    cached = key_cache is not None
     if (query is None) != (q_out is None):
         raise ValueError("query and q_out go together")
-    if (key_cache is None) != (value_cache is None) or (key_cache is None) != (slot_mapping is None) or \
-            (key_cache is None) != (value is None):
+    if cached != (value_cache is not None) or cached != (slot_mapping is not None) or cached != (value is not None):
         raise ValueError("value, the two caches and slot_mapping go together")
-    if (key is None) != (k_out is None and key_cache is None):
+    if (key is None) != (k_out is None and not cached):
         raise ValueError("key needs k_out or the caches, and they need key")
-    for t, H in ((query, Hq), (q_out, Hq), (key, Hkv), (value, Hkv), (k_out, Hkv)):
-        if t is not None and (t.shape != (T, H, d) or t.dtype != dt):
-            raise ValueError("query, key, value and the outputs must agree in tokens, heads, d and dtype")
+    if k_shape[0] != T or k_shape[2] != d:
+        raise ValueError("query, key, value and the outputs must agree in tokens, heads, d and dtype")
+    s_q, s_qo = _row_stride(query, q_shape, dt), _row_stride(q_out, q_shape, dt)
+    s_k, s_v, s_ko = _row_stride(key, k_shape, dt), _row_stride(value, k_shape, dt), _row_stride(k_out, k_shape, dt)
     if positions.dtype != torch.int64 or positions.shape != (T,):
         raise ValueError("positions must be int64 [T]")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [max_position, rotary_dim]")
     NB, bs, c_code = 1, 1, BF16
-    if key_cache is not None:
-        NB, bs = key_cache.shape[:2]
-        if key_cache.shape != (NB, bs, Hkv, d) or value_cache.shape != key_cache.shape or \
-                value_cache.dtype != key_cache.dtype:
+    if cached:
+        pool, c_dt = key_cache.shape, key_cache.dtype
+        NB, bs = pool[0], pool[1]
+        if pool != (NB, bs, Hkv, d) or value_cache.shape != pool or value_cache.dtype != c_dt:
             raise ValueError("shape mismatch between tokens and caches")
         if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
             raise ValueError("slot_mapping must be int64 [T]")
-        c_code = dtype_code(key_cache.dtype)
-    strides = [0 if t is None else _row_stride(t) for t in (query, key, value, q_out, k_out)]
+        c_code = dtype_code(c_dt)
+    max_position, rot = cos_sin.shape
     p_q, p_k, p_v, p_qo, p_ko, p_pos, p_cs, p_kc, p_vc, p_sm, p_err, p_st = _pointers(
         stream, query, key, value, q_out, k_out, positions, cos_sin, key_cache, value_cache, slot_mapping, err_word,
         rows=5)
     _rotary_write(
-        p_q, p_k, p_v, dtype_code(dt), strides[0], strides[1], strides[2], p_pos, p_cs, cos_sin.shape[0],
-        cos_sin.shape[1], int(interleaved), p_qo, strides[3], p_ko, strides[4], p_kc, p_vc, c_code, p_sm, T, NB, bs,
-        Hq, Hkv, d, k_scale, v_scale, p_err, p_st)
+        p_q, p_k, p_v, dtype_code(dt), s_q, s_k, s_v, p_pos, p_cs, max_position, rot, int(interleaved), p_qo, s_qo,
+        p_ko, s_ko, p_kc, p_vc, c_code, p_sm, T, NB, bs, Hq, Hkv, d, k_scale, v_scale, p_err, p_st)
 
 
 def prompt_workspace_size(S: int, num_query_tokens: int, max_query_len: int, max_key_len: int, Hq: int, Hkv: int, d: int,
@@ -872,11 +881,11 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
     last query sits at its last key.  causal False: every key is seen; window
     > 0: the first num_sinks keys and the last `window` up to the query."""
     Tq, Hq, d = shape = query.shape
-    Tk, Hkv, d2 = key.shape
+    Tk, Hkv, d2 = k_shape = key.shape
     dt, S = query.dtype, query_start.numel() - 1
-    if d2 != d or out.shape != shape or value.shape != key.shape or \
-            not (out.dtype == dt == key.dtype == value.dtype):
+    if d2 != d or out.shape != shape or out.dtype != dt:
         raise ValueError("shape or dtype mismatch")
+    s_q, s_k, s_v = _row_stride(query, shape, dt), _row_stride(key, k_shape, dt), _row_stride(value, k_shape, dt)
     if key_start is None:
         key_start = query_start
     if max_key_len is None:
@@ -889,9 +898,8 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
     p_q, p_k, p_v, p_o, p_qs, p_ks, p_ws, p_err, p_st = _pointers(
         stream, query, key, value, out, query_start, key_start, workspace, err_word, rows=3)
     _prompt(
-        p_o, p_q, p_k, p_v, dtype_code(dt), _row_stride(query), _row_stride(key), _row_stride(value), p_qs, p_ks, S, Tq,
-        Tk, max_query_len, max_key_len, Hq, Hkv, d, scale, int(causal), window, num_sinks, partition_size, p_ws,
-        workspace.nbytes, p_err, p_st)
+        p_o, p_q, p_k, p_v, dtype_code(dt), s_q, s_k, s_v, p_qs, p_ks, S, Tq, Tk, max_query_len, max_key_len, Hq, Hkv,
+        d, scale, int(causal), window, num_sinks, partition_size, p_ws, workspace.nbytes, p_err, p_st)
     return out
 
 

@@ -87,14 +87,21 @@ constexpr uint32_t kPFull2 = 256;      // [2 tiles]: ... of the second half of t
 constexpr uint32_t kTmemSlot = 272, kAbort = 276, kRing = 288 /* [2][4] int4 */;
 constexpr uint32_t kMasks = kRing + 128 /* [8 stages][4 words] */, kCtlBytes = kMasks + 128;
 
-template <int D>
+// The rows of a tile: 128 queries of one head (kHeads: K and V of a head are
+// read for two tiles), or the (query, head) pairs of a K/V head in order, 128 at
+// a time (kPacked, kShared: few queries fill a tile between them).
+enum Mode { kHeads, kPacked, kShared };
+
+template <int D, int MODE>
 struct Cfg {
     static constexpr int kHalves = D / 64;                 // 128-byte halves of a row
     static constexpr int kItemBytes = kTok * 2 * D;        // a K, V or Q tile
-    static constexpr int kKItems = D == 128 ? 3 : 4, kVItems = D == 128 ? 2 : 4;
+    // kHeads: an item of K less, and room for 64 columns of each tile's output, which leaves by TMA
+    static constexpr int kKItems = D == 128 ? (MODE == kHeads ? 2 : 3) : 4, kVItems = D == 128 ? 2 : 4;
+    static constexpr int kOutBytes = MODE == kHeads ? kRows * 128 : 0;
     static constexpr int kVOff = kKItems * kItemBytes;
     static constexpr int kQOff = (kKItems + kVItems) * kItemBytes;
-    static constexpr int kTileBytes = kQOff + 2 * kItemBytes;
+    static constexpr int kOutOff = kQOff + 2 * kItemBytes, kTileBytes = kOutOff + 2 * kOutBytes;
     // the control block, up to the next 1,024 bytes (the dynamic shared memory starts on such a boundary;
     // the kernel checks it)
     static constexpr int kSmemBytes = ((int)kCtlBytes + 1023) / 1024 * 1024 + kTileBytes;
@@ -116,6 +123,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
+// a box of shared memory into global memory, a bulk group of its own
+__device__ __forceinline__ void tensor_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(src)
+        : "memory");
+}
+
 // true in one thread of the (converged) warp, always the same one
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -133,11 +149,6 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
 }
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// The rows of a tile: 128 queries of one head (kHeads: K and V of a head are
-// read for two tiles), or the (query, head) pairs of a K/V head in order, 128 at
-// a time (kPacked, kShared: few queries fill a tile between them).
-enum Mode { kHeads, kPacked, kShared };
 
 // A sequence's rows; false when a bound is broken (it is skipped then).
 // kShared: a group of sequences, its members q0 .. q0 + ql, whose first kl
@@ -279,8 +290,9 @@ __device__ __forceinline__ void load_blocks(const PromptParams& p, const CUtenso
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap qmap,
-                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<D>;
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap omap) {
+    using C = Cfg<D, MODE>;
     constexpr bool SHARED = MODE == kShared, PACKED = MODE != kHeads;
     constexpr int NK = C::kKItems, NV = C::kVItems;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -903,7 +915,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int np = e1.y, part = e1.z + (pair && t ? 1 : 0);
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-            // (a loop: unrolled it is 4 KB of code that a unit runs once, and 64 x 512 tokens take 178 us, not 159)
+            // Whole warps of rows leave by TMA, 64 columns at a time through shared memory: stored by the threads,
+            // a row each, 32 lines per instruction, 64 x 512 tokens take XXX us (both directions 204).  (Loops: unrolled
+            // they are 4 KB of code that a unit runs once; 64 x 512 tokens 178 us, not 159.)
+            const bool whole_rows = MODE == kHeads && np == 1 && block * kRows + (warp & 3) * 32 + 31 < ql;
+            if (whole_rows) {
+                const uint32_t out = base + C::kOutOff + t * C::kOutBytes + (warp & 3) * 4096;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t ov[32];
+                    if (n > 0) {
+                        umma::tmem_ld32(o_col + c0, ov);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] = 0u;
+                    }
+                    if (c0 % 64 == 0) {
+                        // what was stored from here before has been read
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
+                    umma::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<false>(__uint_as_float(ov[8 * k + 2 * e]) * f, __uint_as_float(ov[8 * k + 2 * e + 1]) * f);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(out + lane * 128 +
+                                                                               (((c0 / 8 + k) & 7) ^ (lane & 7)) * 16),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    if (c0 % 64 == 32) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tensor_store_2d(&omap, out, (e1.x * p.g + head) * D + c0 - 32, e0.x + block * kRows + (warp & 3) * 32);
+                    }
+                }
+            } else
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t ov[32];
@@ -932,6 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma::fence_before_sync();
         }
+        // the output stored from shared memory is in place before the block leaves
+        if (MODE == kHeads && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     umma::fence_before_sync();
@@ -944,8 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int MODE>
 cudaError_t launch_attend(const PromptParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                          long long units, int num_sms, cudaStream_t st) {
-    using C = Cfg<D>;
+                          const CUtensorMap& omap, long long units, int num_sms, cudaStream_t st) {
+    using C = Cfg<D, MODE>;
     auto kern = attend_kernel<D, MODE>;
     // the register shares must fit in what the block is launched with
     // (setmaxnreg waits forever otherwise): checked once, on the binary
@@ -963,7 +1016,7 @@ cudaError_t launch_attend(const PromptParams& p, const CUtensorMap& qmap, const 
     cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), C::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int grid = (int)(units < num_sms ? (units > 0 ? units : 1) : num_sms);
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, st, p, qmap, kmap, vmap);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, st, p, qmap, kmap, vmap, omap);
 }
 
 }  // namespace

@@ -41,16 +41,20 @@ __global__ void __launch_bounds__(256) prompt_merge_kernel(const __grid_constant
 
 template <int D, int MODE>
 cudaError_t launch_mode(const PromptParams& p, int num_sms, cudaStream_t st) {
-    CUtensorMap qmap, kmap, vmap;
+    CUtensorMap qmap, kmap, vmap, omap;
     // (no keys at all: nothing is loaded through the maps of K and V)
     if (!encode_rows_map(&kmap, p.Tk > 0 ? p.k : p.q, p.Tk, p.Hkv * D, p.k_stride, kTok) ||
         !encode_rows_map(&vmap, p.Tk > 0 ? p.v : p.q, p.Tk, p.Hkv * D, p.v_stride, kTok))
         return cudaErrorInvalidValue;
-    if (MODE == kPacked) qmap = kmap;
-    else if (!encode_rows_map(&qmap, p.q, p.Tq, p.Hq * D, p.q_stride, kRows)) return cudaErrorInvalidValue;
+    if (MODE == kPacked) {
+        qmap = omap = kmap;                      // (not used)
+    } else if (!encode_rows_map(&qmap, p.q, p.Tq, p.Hq * D, p.q_stride, kRows) ||
+               !encode_rows_map(&omap, p.out, p.Tq, p.Hq * D, (long long)p.Hq * D, 32)) {
+        return cudaErrorInvalidValue;
+    }
     const long long per_head = MODE == kPacked ? (ceil_div(p.max_q * p.g, kRows) + 1) / 2
                                                : (long long)ceil_div(p.max_q, p.group * kRows) * ((p.g * p.group + 1) / 2);
-    const cudaError_t e = launch_attend<D, MODE>(p, qmap, kmap, vmap, (long long)p.S * p.Hkv * per_head * p.Pmax, num_sms, st);
+    const cudaError_t e = launch_attend<D, MODE>(p, qmap, kmap, vmap, omap, (long long)p.S * p.Hkv * per_head * p.Pmax, num_sms, st);
     if (e != cudaSuccess || p.Pmax <= 1) return e;
     const long long rows = (long long)p.Tq * p.Hq;
     return launch_pdl(prompt_merge_kernel<D, MODE>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, p);

@@ -100,7 +100,7 @@ cudaError_t launch_d(const PromptParams& p, const DecodeParams& d, int num_sms, 
     if (!prefill_encode_kv_map(&kmap, p.k, d) || !prefill_encode_kv_map(&vmap, p.v, d)) return cudaErrorInvalidValue;
     const long long tiles = ((long long)p.max_q * p.g + kRows - 1) / kRows;
     const long long units = (long long)p.S * p.Hkv * ((tiles + 1) / 2) * ceil_div(ceil_div(p.max_k, kTok), p.P > 0 ? p.P : 1 << 24);
-    return launch_attend<D, kShared>(p, kmap, kmap, vmap, units, num_sms, st);
+    return launch_attend<D, kShared>(p, kmap, kmap, vmap, kmap, units, num_sms, st);
 }
 
 }  // namespace
