@@ -955,7 +955,7 @@ bool prompt_shape_ok(int S, int Tq, int max_q, int max_k, int Hq, int Hkv, int d
 constexpr int kPackedQueries = 64;
 bool prompt_packed(int max_q, int64_t q_stride, int d) { return max_q <= kPackedQueries && q_stride % d == 0; }
 
-// Stages per partition (0: no split).  Units that fill the SMs are not split.
+// Stages per partition (0: no split).
 int resolve_prompt_partition(int S, int Tq, int max_q, int Hq, int Hkv, int d, int stages, int req, size_t room) {
     if (req != 0) return req > 0 ? req / kPromptStage : 0;
     const int g = Hq / Hkv, group = prompt_group(g);
@@ -967,10 +967,15 @@ int resolve_prompt_partition(int S, int Tq, int max_q, int Hq, int Hkv, int d, i
         units = (long long)S * Hkv * ((tiles + 1) / 2);
         if (tiles == 1) units = (units + 1) / 2;           // paired partitions
     }
-    if (units == 0 || units >= 152) return 0;
+    if (units == 0 || units > 76) return 0;
     const long long parts = 152 / units;
     int P = (int)((stages + parts - 1) / parts);
     if (P < 4) P = 4;
+    // A stage takes 1.65 us; a split launch 7 more, and 1 KB written and read per row and partition (at 4 TB/s).  1,024
+    // queries, 12 / 2 heads, 20.0 us (causal) and 21.3 in one partition, 25.2 and 30.0 in two; 2,048 of them 33.4 and
+    // 35.6, in two 39 and 61; but 5 and 9 queries over 16,384 and 32,768 keys 329 and 26.4.
+    const long long np = (stages + P - 1) / P;
+    if ((stages - P) * 165LL < 700 + (long long)Tq * Hq * np / 40) return 0;
     while (P < stages && plan_prompt(Tq, Hq, d, stages, P).bytes > room) P += P / 8 > 1 ? P / 8 : 1;
     return P < stages ? P : 0;
 }
