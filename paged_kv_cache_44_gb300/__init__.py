@@ -24,6 +24,13 @@ block manager (:class:`BlockPool`), and what bounds a cache's size:
   :func:`paged_attention_decode_kv4` -- a cache in 4 bits;
 * :func:`token_attention_decode_scored`, :func:`evict_tokens` -- attention
   weights accumulated per token, and the tokens with the least dropped.
+
+A prompt's way into the cache, and the decode of sequences that share blocks:
+
+* :func:`rotary_kv_write` -- rotary embedding of Q and K with the cache write;
+* :func:`prompt_attention` -- attention over whole packed prompts;
+* :func:`paged_attention_decode_shared` -- groups of sequences whose first
+  blocks are the same read them once.
 """
 from __future__ import annotations
 
@@ -886,10 +893,10 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
     if d2 != d or out.shape != shape or out.dtype != dt:
         raise ValueError("shape or dtype mismatch")
     s_q, s_k, s_v = _row_stride(query, shape, dt), _row_stride(key, k_shape, dt), _row_stride(value, k_shape, dt)
+    if (key_start is None) != (max_key_len is None):
+        raise ValueError("key_start and max_key_len go together")
     if key_start is None:
-        key_start = query_start
-    if max_key_len is None:
-        max_key_len = max_query_len
+        key_start, max_key_len = query_start, max_query_len
     if query_start.dtype != torch.int32 or key_start.dtype != torch.int32 or key_start.numel() != S + 1 or S < 0:
         raise ValueError("query_start and key_start must be int32 [S + 1]")
     if workspace is None:

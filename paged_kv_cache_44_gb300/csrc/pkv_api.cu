@@ -1008,7 +1008,8 @@ pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, c
         return PKV_ERR_INVALID_ARG;
     if (Hq % Hkv != 0) return PKV_ERR_INVALID_ARG;
     if (dtype != PKV_BF16 || !(d == 64 || d == 128) || S > 65535) return PKV_ERR_UNSUPPORTED;
-    if ((long long)Hq * d > (1 << 24)) return PKV_ERR_UNSUPPORTED;
+    if ((long long)Hq * d > (1 << 24) || num_query_tokens > (1 << 30) || num_key_tokens > (1 << 30))
+        return PKV_ERR_UNSUPPORTED;
     if (!isfinite(scale) || window < 0 || num_sinks < 0 || (window > 0 && !causal)) return PKV_ERR_INVALID_ARG;
     if (partition_size < -1 || (partition_size > 0 && partition_size % kPromptStage != 0)) return PKV_ERR_INVALID_ARG;
     if (S == 0 || num_query_tokens == 0) return PKV_OK;
@@ -1022,7 +1023,8 @@ pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, c
     for (const Rows& r : {Rows{query, q_stride, Hq, num_query_tokens}, Rows{key, k_stride, Hkv, num_key_tokens},
                           Rows{value, v_stride, Hkv, num_key_tokens}}) {
         if (r.n == 0) continue;
-        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride >= (1LL << 38) || r.stride % 8 != 0)
+        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride >= (1LL << 38) || r.stride % 8 != 0 ||
+            r.stride > (1LL << 46) / r.n)
             return PKV_ERR_INVALID_ARG;
         if (overlap(out, r.at, out_bytes, (size_t)((r.n - 1) * r.stride + (int64_t)r.heads * d) * 2)) return PKV_ERR_INVALID_ARG;
     }
@@ -1289,11 +1291,13 @@ pkv_status pkv_rotary_kv_write(const void* query, const void* key, const void* v
         int64_t stride;
         int heads;
     };
+    const int64_t far = 1LL << 46;                   // (sums of sizes below stay in 64 bits)
+    if (cached && ((int64_t)NB * bs > far / d || (int64_t)NB * bs * d > far / Hkv)) return PKV_ERR_INVALID_ARG;
     const Rows rows[5] = {{query, q_stride, Hq}, {key, k_stride, Hkv}, {value, v_stride, Hkv},
                           {q_out, q_out_stride, Hq}, {k_out, k_out_stride, Hkv}};
     for (const Rows& r : rows) {
         if (r.at == nullptr) continue;
-        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride > (1LL << 40) || r.stride * eb % 16 != 0)
+        if (!aligned16(r.at) || r.stride < (int64_t)r.heads * d || r.stride > far / T || r.stride * eb % 16 != 0)
             return PKV_ERR_INVALID_ARG;
     }
     // an output lies on its own input, row for row, or on nothing that is read or written here

@@ -25,7 +25,7 @@ def _rotary(q=A, k=2 * A, v=3 * A, dt=1, qs=1024, ks=256, vs=256, pos=4 * A, cs=
     (dict(cdt=2, k_scale=0.0), 1), (dict(cdt=2, v_scale=float("nan")), 1), (dict(kc=8 * A + 2), 1),
     # outputs over something else that is read or written
     (dict(qo=2 * A), 1), (dict(qo=A + 16), 1), (dict(qo=A, qos=2048), 1), (dict(ko=3 * A), 1), (dict(ko=6 * A + 256), 1),
-    (dict(qo=8 * A + 4096), 1), (dict(kc=9 * A), 1), (dict(qs=1536, q=A, k=A + 2048, ks=1536, qo=A + 1024, qos=1536), 1)])
+    (dict(T=1 << 20, qs=1 << 30), 1), (dict(NB=1 << 30, bs=1 << 10), 1), (dict(qo=8 * A + 4096), 1), (dict(kc=9 * A), 1), (dict(qs=1536, q=A, k=A + 2048, ks=1536, qo=A + 1024, qos=1536), 1)])
 def test_rotary(kw, status):
     assert _rotary(**kw) == status
 
@@ -60,7 +60,8 @@ def _prompt(out=A, q=2 * A, k=3 * A, v=4 * A, dt=1, qs=1024, ks=256, vs=256, q_s
     (dict(part=100), 1), (dict(out=None), 1), (dict(q=None), 1), (dict(k=None), 1), (dict(q_start=None), 1),
     (dict(k_start=None), 1), (dict(q=2 * A + 8), 1), (dict(qs=1020), 1), (dict(qs=1028), 1), (dict(ks=255), 1),
     (dict(vs=1 << 38), 1), (dict(out=A + 4), 1), (dict(q_start=5 * A + 2), 1), (dict(out=2 * A), 1), (dict(out=3 * A - 16), 1),
-    (dict(out=4 * A + 2048), 1), (dict(part=128, mk=1000, ws=None, wsb=0), 3), (dict(part=128, mk=1000, wsb=1000), 3),
+    (dict(out=4 * A + 2048), 1), (dict(Tq=(1 << 30) + 1), 2), (dict(Tk=(1 << 30) + 1), 2),
+    (dict(vs=1 << 37, Tk=1 << 10), 1), (dict(part=128, mk=1000, ws=None, wsb=0), 3), (dict(part=128, mk=1000, wsb=1000), 3),
     (dict(part=128, mk=1000, ws=7 * A + 8), 1)])
 def test_prompt(kw, status):
     assert _prompt(**kw) == status
@@ -81,7 +82,8 @@ def test_prompt_binding():
     q, k = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
     qs = torch.tensor([0, 4], dtype=torch.int32)
     for args, kw in [((q, q, k, k.float(), qs, 4, 1.0), {}), ((q, q, k, k[:3], qs, 4, 1.0), {}), ((q[:2], q, k, k, qs, 4, 1.0), {}),
-                     ((q, q, k, k, qs.long(), 4, 1.0), {}), ((q, q, k, k, qs, 4, 1.0), dict(key_start=qs[:1]))]:
+                     ((q, q, k, k, qs.long(), 4, 1.0), {}), ((q, q, k, k, qs, 4, 1.0), dict(key_start=qs[:1], max_key_len=4)), ((q, q, k, k, qs, 4, 1.0), dict(key_start=qs)),
+                     ((q, q, k, k, qs, 4, 1.0), dict(max_key_len=4))]:
         with pytest.raises(ValueError):
             pkv.prompt_attention(*args, workspace=q, **kw)
 
