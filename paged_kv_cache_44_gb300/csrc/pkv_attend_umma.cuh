@@ -21,11 +21,12 @@
 //               lane): P = 2^(x - m) in bf16 goes over the first half of S's
 //               columns
 //   warp 8      claims units, K tiles by TMA into a ring
-//   warp 9      one thread issues the products:
+//   warps 9, 10 issue a tile's products each (one warp for both, waiting for the two
+//               tiles in a fixed order: one prompt of 32,768 tokens 4,893 us, not 4,718;
+//               one of 1 token 0.2 us less), and gather its rows where it is packed:
 //                 S_t = Q_t . K_j^T       M 128, N 128, K d
 //                 O_t (+)= P_t . V_j      M 128, N d, K 128 (P_t in TMEM)
-//   warp 10     Q tiles by TMA
-//   warp 11     V tiles by TMA; zeroes the rows of a sequence's last tile that
+//   warp 11     V tiles, and Q tiles of one head, by TMA; zeroes the rows of a sequence's last tile that
 //               are other sequences' (0 times what they hold may be NaN)
 // A row's reference maximum m moves only when a stage's maximum exceeds it by
 // more than 2^8; O is then rescaled in TMEM.  Every exponent stays <= 2^8 and O
@@ -58,8 +59,10 @@ using namespace tc;
 constexpr int kTok = kPromptStage;    // key tokens per stage
 constexpr int kRows = kPromptStage;   // queries per tile
 constexpr int kSoftWarps = 8, kThreads = 384;
-constexpr int kKWarp = 8, kMmaWarp = 9, kQWarp = 10, kVWarp = 11;
+constexpr int kKWarp = 8, kMmaWarp = 9 /* and 10: a tile each */, kVWarp = 11;
+constexpr int kTurnStages = 16, kTurnTail = 8;
 constexpr float kRescaleLog2 = 8.f;
+constexpr long long kTurnLimit = 16384;           // cycles: some five stages
 constexpr long long kWaitLimit = 4000000000LL;    // ~2 s: a barrier that never completes
 constexpr uint32_t kTmemCols = 512;               // O_0, O_1, S_0, S_1; P_t over the first half of S_t
 __host__ __device__ constexpr uint32_t tmem_o(int t) { return 128u * t; }
@@ -84,7 +87,7 @@ constexpr uint32_t kUEmpty = 224;      // [2]
 constexpr uint32_t kTail = 240;        // the V tile whose rows are to be zeroed has landed
 constexpr uint32_t kFin = 248;
 constexpr uint32_t kPFull2 = 256;      // [2 tiles]: ... of the second half of the keys
-constexpr uint32_t kTmemSlot = 272, kAbort = 276, kRing = 288 /* [2][4] int4 */;
+constexpr uint32_t kTmemSlot = 272, kAbort = 276, kTurn = 280 /* [2 tiles] */, kRing = 288 /* [2][4] int4 */;
 constexpr uint32_t kMasks = kRing + 128 /* [8 stages][4 words] */, kCtlBytes = kMasks + 128;
 
 // The rows of a tile: 128 queries of one head (kHeads: K and V of a head are
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + kAbort);
     int4* ring = reinterpret_cast<int4*>(smem_raw + kRing);              // [2 units][4]
+    volatile uint32_t* turns = reinterpret_cast<volatile uint32_t*>(smem_raw + kTurn);   // stages of each tile that had their turn
     uint32_t* masks = reinterpret_cast<uint32_t*>(smem_raw + kMasks);    // SHARED: tokens there are, stage g in slot g % 8
     auto ktile = [&](uint32_t j) { return base + (j % NK) * C::kItemBytes; };
     auto vtile = [&](uint32_t j) { return base + C::kVOff + (j % NV) * C::kItemBytes; };
@@ -317,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kKFull, i), 1);
-            mbar_init(bar(kKEmpty, i), 1);
+            mbar_init(bar(kKEmpty, i), 2);
             mbar_init(bar(kVFull, i), 1);
-            mbar_init(bar(kVEmpty, i), 1);
+            mbar_init(bar(kVEmpty, i), 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(kSFull, t), 1);
@@ -332,8 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kUEmpty, t), kSoftWarps + 3);
         }
         mbar_init(bar(kTail, 0), 1);
-        mbar_init(bar(kFin, 0), 1);
+        mbar_init(bar(kFin, 0), 2);
         *abort_flag = 0;
+        turns[0] = turns[1] = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) umma::tmem_alloc(ctl + kTmemSlot, kTmemCols);
@@ -368,6 +373,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         own = __reduce_max_sync(0xffffffffu, own);
         if (lane == 0 && own > 0) atomicMax(p.own_max, own);
     }
+    // Tiles take turns so that one's softmax runs beside the other's products,
+    // not beside its softmax.  Only their pace depends on it: a tile that has
+    // waited for as long as several stages goes on.  Tile t's stage j follows
+    // the other's stage j (t 1) or j - 1 (t 0), `before` stages of the other in
+    // the units before and `here` in this one.
+    //
+    // In turn go the products (by_products), or in long lists of 128-wide heads
+    // the softmaxes, but for the last kTurnTail stages.  TFLOP/s with turns of
+    // the softmaxes, of the products, without: d 128, 16,384 tokens both ways
+    // 1,781, 1,574, 1,725; d 64, 4 x 4,096 tokens causal 878, 1,011, 941 (both
+    // ways 783, 920, 881).  1,000 tokens alone (8 stages): turns of the products
+    // 18.5 us, without 20.8.  kTurnStages 10, 16, 32: 8 x 6,000 tokens with a
+    // window of 1,024 at 1,084, 1,136, 1,124, 16,384 at 1,754, 1,763, 1,680.
+    auto by_products = [](int c0, int c1) { return D == 64 || min(c0, c1) < kTurnStages; };
+    auto my_turn = [&](int t, int j, uint32_t before, int here) {
+        const uint32_t need = before + min(t == 0 ? j : j + 1, here);
+        const long long t0 = clock64();
+        while ((int)(turns[t ^ 1] - need) < 0 && clock64() - t0 < kTurnLimit) {
+        }
+        __syncwarp();
+    };
     // the first key of stage j of a unit's list
     auto stage_key = [](int j, int sinks, int low) { return (j < sinks ? j : j - sinks + low) * kTok; };
     // Stages of a unit whose tiles take c0 and c1 of them: the same ones, or
@@ -380,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return PACKED && pair ? (m < 2 * c1 ? m / 2 + (m & 1) * p.P : m - c1) : m;
     };
     // A parity wait is exact while the barrier is within one phase of the
-    // awaited one; every wait below is by construction.  K_j and V_j sit in
+    // awaited one; every wait below is by construction (a slot is filled again
+    // once both tiles' products have gone past it).  K_j and V_j sit in
     // slots j % NK, j % NV (j counted over the block's stages); the per-tile
     // barriers count the stages that tile took part in.
 
@@ -491,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if constexpr (SHARED) {
                     // which of the stage's tokens there are: a block whose id is out of the pool is absent
+                    // (stage g - 8's were read: both tiles' products have gone past stage g - NK, NK < 8)
                     const int pb = ids.stage(p, pair && j < 2 * c1 ? j & 1 : 0);
                     const uint32_t there = __ballot_sync(0xffffffffu, pb >= 0);
                     if (pb == -2) report(p.err, PKV_DEVERR_BLOCK_ID);
@@ -529,19 +557,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kVWarp) {
-        // ------------------------------------------------------------ V tiles
+        // ------------------------------------------------------ Q and V tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        uint32_t g = 0, un = 0, tails = 0;
+        uint32_t g = 0, un = 0, tails = 0, qu[2] = {0u, 0u};
         bool ok = true, bad = false;
         for (;;) {
             const int slot = un & 1;
             ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
             if (__any_sync(0xffffffffu, !ok)) break;
-            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2];
-            const bool pair = PACKED && ring[4 * slot + 3].w > 0;
+            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2], e3 = ring[4 * slot + 3];
+            const bool pair = PACKED && e3.w > 0;
             __syncwarp();
             if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
             if (e1.x < 0) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (PACKED || (t == 0 ? e2.z : e2.w) == 0) continue;       // no keys, or no tile
+                if (qu[t] >= 1) ok = wait(bar(kQEmpty, t), (qu[t] - 1) & 1, true);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    bad = true;
+                    break;
+                }
+                if (lane == 0) {
+                    // rows past the sequence's last are other sequences' or zeros: their results are not stored
+                    mbar_arrive_expect_tx(bar(kQFull, t), C::kItemBytes);
+                    const int head = e1.x * p.g + (t == 0 ? e3.y : e3.w), row = e0.x + (t == 0 ? e3.x : e3.z) * kRows;
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tensor_load_2d(qbuf(t) + h * (kRows * 128), &qmap, head * D + h * 64, row, bar(kQFull, t));
+                }
+                __syncwarp();
+                ++qu[t];
+            }
+            if (bad) break;
             const int n = count(pair, e2.z, e2.w);
             BlockIds ids;
             if constexpr (SHARED) ids.start(p, e0.x, e0.w / p.bs, e1.w, pair ? p.P : 0);
@@ -596,55 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t k = 1; k <= (uint32_t)NV && k <= g; ++k)
             wait(bar(kVFull, (g - k) % NV), ((g - k) / NV) & 1, false);
-    } else if (warp == kQWarp) {
-        // ------------------------------------------------------------ Q tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        uint32_t un = 0, qu[2] = {0u, 0u};
-        bool ok = true, bad = false;
-        for (;;) {
-            const int slot = un & 1;
-            ok = wait(bar(kUFull, slot), (un >> 1) & 1, true);
-            if (__any_sync(0xffffffffu, !ok)) break;
-            const int4 e0 = ring[4 * slot], e1 = ring[4 * slot + 1], e2 = ring[4 * slot + 2], e3 = ring[4 * slot + 3];
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
-            if (e1.x < 0) break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if ((t == 0 ? e2.z : e2.w) == 0) continue;       // no keys, or no tile
-                if (qu[t] >= 1) ok = wait(bar(kQEmpty, t), (qu[t] - 1) & 1, true);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    bad = true;
-                    break;
-                }
-                if constexpr (PACKED) {
-                    DecodeParams q{};
-                    q.q = p.q;
-                    q.Hq = (int)(p.q_stride / D);                // (heads from one token to the next)
-                    q.g = p.g;
-                    const int r0 = (t == 0 ? e3.x : e3.z) * kRows;
-                    load_q_rows<D, kRows>(q, e0.x, e1.x, r0, 0, kRows, e0.z * p.g - r0, qbuf(t));
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) umma::mbar_arrive(bar(kQFull, t));
-                } else if (lane == 0) {
-                    // rows past the sequence's last are other sequences' or zeros: their results are not stored
-                    mbar_arrive_expect_tx(bar(kQFull, t), C::kItemBytes);
-                    const int head = e1.x * p.g + (t == 0 ? e3.y : e3.w), row = e0.x + (t == 0 ? e3.x : e3.z) * kRows;
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tensor_load_2d(qbuf(t) + h * (kRows * 128), &qmap, head * D + h * 64, row, bar(kQFull, t));
-                }
-                __syncwarp();
-                ++qu[t];
-            }
-            if (bad) break;
-            ++un;
-        }
         for (int t = 0; t < 2; ++t)
             if (qu[t] > 0) wait(bar(kQFull, t), (qu[t] - 1) & 1, false);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ----------------------------------------------------------- products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // The whole warp walks the loop and one elected thread issues: the
@@ -657,11 +659,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // descriptors of the first K step of slot 0; a slot or K step on adds to the address, in 16 bytes
         const uint64_t q_desc = umma::desc_sw128(qbuf(0), 16, 1024), k_desc = umma::desc_sw128(base, 16, 1024);
         const uint64_t v_desc = umma::desc_sw128(base + C::kVOff, kTok * 128, 1024);
-        uint32_t g = 0, un = 0, gt[2] = {0u, 0u}, qu[2] = {0u, 0u};
+        const int t = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+        uint32_t g = 0, un = 0, gt = 0, qu = 0, before = 0;
         bool ok = true;
         // waits of the whole warp
         auto all = [&](uint32_t b, uint32_t parity) -> bool { return !__any_sync(0xffffffffu, !wait(b, parity, true)); };
-        auto issue_s = [&](int t, uint32_t gs, bool last) {
+        // a slot, once what was issued before has read it
+        auto release = [&](uint32_t b) {
+            if (elect_one()) umma::commit(b);
+            __syncwarp();
+        };
+        // The other tile's stages, before stage `to`: each is waited for and released like the tile's own, so
+        // that no slot is filled twice between two waits (of one parity), nor while this tile counts on it
+        uint32_t ks = 0, vs = 0;                             // the next K and V stages of the block
+        auto skip_k = [&](uint32_t to) -> bool {
+            for (; ks != to; ++ks) {
+                if (!all(bar(kKFull, ks % NK), (ks / NK) & 1)) return false;
+                if (lane == 0) umma::mbar_arrive(bar(kKEmpty, ks % NK));
+            }
+            return true;
+        };
+        auto skip_v = [&](uint32_t to) -> bool {
+            for (; vs != to; ++vs) {
+                if (!all(bar(kVFull, vs % NV), (vs / NV) & 1)) return false;
+                if (lane == 0) umma::mbar_arrive(bar(kVEmpty, vs % NV));
+            }
+            return true;
+        };
+        auto issue_s = [&](uint32_t gs, bool last) {
             const uint64_t kd = k_desc + (gs % NK) * (C::kItemBytes / 16), qd = q_desc + t * (C::kItemBytes / 16);
             umma::fence_after_sync();
             if (elect_one()) {
@@ -671,12 +696,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma::mma_bf16(tm + tmem_s(t), qd + off, kd + off, idS, kk > 0);
                 }
                 umma::commit(bar(kSFull, t));
-                if (last) umma::commit(bar(kQEmpty, t));
+                if (last && !PACKED) umma::commit(bar(kQEmpty, t));
             }
             __syncwarp();
+            release(bar(kKEmpty, gs % NK));
+            ks = gs + 1;
         };
         // half of a stage's keys
-        auto issue_pv = [&](int t, uint32_t gs, int half, bool first) {
+        auto issue_pv = [&](uint32_t gs, int half, bool first) {
             const uint64_t vd = v_desc + (gs % NV) * (C::kItemBytes / 16) + half * (kTok / 2 * 128 / 16);
             umma::fence_after_sync();
             if (elect_one()) {
@@ -688,71 +715,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        auto release = [&](uint32_t b) {                  // a slot, once what was issued before has read it
-            if (elect_one()) umma::commit(b);
-            __syncwarp();
-        };
         for (;;) {
             const int slot = un & 1;
             if (!all(bar(kUFull, slot), (un >> 1) & 1)) break;
             const int kvh = __shfl_sync(0xffffffffu, ring[4 * slot + 1].x, 0);
-            const int c[2] = {__shfl_sync(0xffffffffu, ring[4 * slot + 2].z, 0),
-                              __shfl_sync(0xffffffffu, ring[4 * slot + 2].w, 0)};
-            const int n = max(c[0], c[1]);
+            const int c0 = __shfl_sync(0xffffffffu, ring[4 * slot + 2].z, 0), c1 = __shfl_sync(0xffffffffu, ring[4 * slot + 2].w, 0);
             const bool pair = PACKED && __shfl_sync(0xffffffffu, ring[4 * slot + 3].w, 0) > 0;
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            if (lane == 0 && (!PACKED || kvh < 0)) umma::mbar_arrive(bar(kUEmpty, slot));
             if (kvh < 0) break;
-            auto at = [&](int t, int j) { return g + order(pair, c[1], t, j); };
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (c[t] == 0 || !ok) continue;
-                const uint32_t s0 = at(t, 0);
-                ok = all(bar(kKFull, s0 % NK), (s0 / NK) & 1) && all(bar(kQFull, t), qu[t] & 1);
-                // the tile's last P . V has read the buffer
-                if (ok && gt[t] > 0) ok = all(bar(kPVDone, t), (gt[t] - 1) & 1);
+            const int c = t ? c1 : c0;
+            const bool in_turn = by_products(c0, c1);
+            const uint32_t end = g + count(pair, c0, c1);
+            if (c > 0) {
+                const uint32_t s0 = g + order(pair, c1, t, 0);
+                // the tile's last P . V has read S's buffer (and its last S was before that)
+                if (gt > 0) ok = all(bar(kPVDone, t), (gt - 1) & 1);
                 if (!ok) break;
-                issue_s(t, s0, c[t] == 1);
-                if (pair) release(bar(kKEmpty, s0 % NK));
-            }
-            if (!ok) break;
-            if (n > 0 && !pair) release(bar(kKEmpty, g % NK));
-            for (int j = 0; j < n && ok; ++j) {
-                bool next_k = false;
-                if (!pair) ok = all(bar(kVFull, (g + j) % NV), ((g + j) / NV) & 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (j >= c[t] || !ok) continue;
-                    const uint32_t s0 = at(t, j);
-                    if (pair) ok = all(bar(kVFull, s0 % NV), (s0 / NV) & 1);
-                    ok = ok && all(bar(kPFull, t), gt[t] & 1);
-                    if (!ok) break;
-                    issue_pv(t, s0, 0, j == 0);
-                    ok = all(bar(kPFull2, t), gt[t] & 1);
-                    if (!ok) break;
-                    issue_pv(t, s0, 1, false);
-                    if (pair) release(bar(kVEmpty, s0 % NV));
-                    if (j + 1 < c[t]) {
-                        // the next S_t overwrites P_t: only after P_t . V_j is done
-                        const uint32_t s1 = at(t, j + 1);
-                        if (!next_k || pair) ok = all(bar(kKFull, s1 % NK), (s1 / NK) & 1);
-                        next_k = true;
-                        ok = ok && all(bar(kPVDone, t), gt[t] & 1);
-                        if (!ok) break;
-                        issue_s(t, s1, j + 2 == c[t]);
-                        if (pair) release(bar(kKEmpty, s1 % NK));
-                    }
-                    ++gt[t];
+                if constexpr (PACKED) {
+                    // rows of (query, head) pairs are gathered: by this warp, which waits for them anyway
+                    DecodeParams q{};
+                    q.q = p.q;
+                    q.Hq = (int)(p.q_stride / D);                // (heads from one token to the next)
+                    q.g = p.g;
+                    const int4 e0 = ring[4 * slot], e3 = ring[4 * slot + 3];
+                    const int r0 = (t == 0 ? e3.x : e3.z) * kRows;
+                    load_q_rows<D, kRows>(q, e0.x, kvh, r0, 0, kRows, e0.z * p.g - r0, qbuf(t));
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async();
+                    __syncwarp();
+                } else {
+                    ok = all(bar(kQFull, t), qu & 1);
                 }
+                ok = ok && skip_k(s0) && all(bar(kKFull, s0 % NK), (s0 / NK) & 1);
                 if (!ok) break;
-                if (!pair) {
-                    release(bar(kVEmpty, (g + j) % NV));
-                    if (j + 1 < n) release(bar(kKEmpty, (g + j + 1) % NK));
-                }
+                issue_s(s0, c == 1);
             }
-            g += count(pair, c[0], c[1]);
+            if constexpr (PACKED) {
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(bar(kUEmpty, slot));
+            }
+            for (int j = 0; j < c; ++j, ++gt) {
+                const uint32_t s0 = g + order(pair, c1, t, j);
+                ok = skip_v(s0) && all(bar(kVFull, s0 % NV), (s0 / NV) & 1) && all(bar(kPFull, t), gt & 1);
+                if (!ok) break;
+                if (in_turn) my_turn(t, j, before, t ? c0 : c1);
+                issue_pv(s0, 0, j == 0);
+                ok = all(bar(kPFull2, t), gt & 1);
+                if (!ok) break;
+                issue_pv(s0, 1, false);
+                release(bar(kVEmpty, s0 % NV));
+                vs = s0 + 1;
+                if (j + 1 < c) {
+                    // the next S_t overwrites P_t: only after P_t . V_j is done
+                    const uint32_t s1 = g + order(pair, c1, t, j + 1);
+                    ok = skip_k(s1) && all(bar(kKFull, s1 % NK), (s1 / NK) & 1) && all(bar(kPVDone, t), gt & 1);
+                    if (!ok) break;
+                    issue_s(s1, j + 2 == c);
+                }
+                if (in_turn && lane == 0) turns[t] = gt + 1;
+            }
+            while (ok && ks != end) ok = skip_k(ks + 1) && skip_v(ks);
             if (!ok) break;
-            for (int t = 0; t < 2; ++t) qu[t] += c[t] > 0;
+            before += t ? c0 : c1;
+            g = end;
+            qu += c > 0;
             ++un;
         }
         // every product issued here completes before the block releases TMEM
@@ -767,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + lane_base + tmem_s(t);
         const uint32_t o_col = tmem + lane_base + tmem_o(t);
-        uint32_t gt = 0, un = 0, gs = 0;
+        uint32_t gt = 0, un = 0, gs = 0, before = 0;
         bool ok = true, bad = false;
         for (;;) {
             const int slot = un & 1;
@@ -782,7 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool pair = PACKED && e3.w > 0;
             const uint32_t stages = gs;                          // the unit's first in the block's count (SHARED's masks)
             gs += count(pair, e2.z, e2.w);
+            const int here = t == 0 ? e2.w : e2.z;               // the other tile's stages
+            const uint32_t before_here = before;
+            before += here;
             if (head < 0) continue;                              // the unit has one tile
+            const bool in_turn = by_products(n, here);
             const int block = t == 0 ? e3.x : e3.z;
             const int ql = e0.z, kl = e0.w;
             int qi = block * kRows + i, hh = head;               // this row's query and head of the K/V head's
@@ -814,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 umma::fence_after_sync();
+                if (!in_turn && n - j >= kTurnTail) my_turn(t, j, before_here, here);
                 const int key = stage_key(j0 + j, e2.x, e2.y);
                 const uint32_t* there = masks + 4 * ((stages + order(pair, e2.w, t, j)) & 7);
                 bool whole = !flip && key + kTok - 1 <= min(first, kl - 1) &&
@@ -900,6 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) umma::mbar_arrive(bar(w == 1 ? kPFull : kPFull2, t));
                     }
                 }
+                if (!in_turn && (tid & 127) == 0) turns[t] = gt + 1;
                 float ls[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) umma::f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
