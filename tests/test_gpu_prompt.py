@@ -250,6 +250,25 @@ def test_many_sequences():
         check(call(q, k, v, ql, ql, part=part), q, k, v, ql, ql, True, 0, 0, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("shape", [(6, 2, 64), (9, 3, 128), (2, 2, 128), (40, 2, 64)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "both"])
+def test_units_of_one_tile_between_units_of_two(shape, causal):
+    # odd numbers of tiles over keys of every length, several units per SM: a tile sits out whole units, and begins
+    # its next one while the other tile is still at the one it sat out
+    Hq, Hkv, d = shape
+    gen = torch.Generator().manual_seed(17)
+    ql = [int(torch.randint(1, 129 if i % 3 else 400, (1,), generator=gen)) for i in range(180)]
+    kl = [a + int(torch.randint(0, 1500 if i % 2 else 130, (1,), generator=gen)) for i, a in enumerate(ql)]
+    if Hq == 40:
+        ql = [1 + n % 9 for n in ql]                     # packed: tiles of (query, head) pairs, partitions in pairs
+    q, k, v = inputs(ql, kl, Hq, Hkv, d, seed=18)
+    part = 256 if Hq == 40 else 0
+    out = call(q, k, v, ql, kl, causal, part=part)
+    check(out, q, k, v, ql, kl, causal, 0, 0, d ** -0.5)
+    for _ in range(20):
+        assert torch.equal(call(q, k, v, ql, kl, causal, part=part), out)
+
+
 def test_repeats_are_equal_and_workspaces_are_reused():
     ql, kl = [3, 100], [5000, 900]
     q, k, v = inputs(ql, kl, 12, 2, 128, seed=13)
