@@ -957,44 +957,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int np = e1.y, part = e1.z + (pair && t ? 1 : 0);
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-            // Whole warps of rows leave by TMA, 64 columns at a time through shared memory: stored by the threads,
-            // a row each, 32 lines per instruction, 64 x 512 tokens take 204 us in both directions, not 189.  (Loops: unrolled
-            // they are 4 KB of code that a unit runs once; 64 x 512 tokens 178 us, not 159.)
+            // Whole warps of rows leave by TMA, 64 columns at a time through shared memory: stored by the threads, a row
+            // each, 32 lines per instruction, 64 x 512 tokens take 204 us in both directions, not 189; 32 columns at a time
+            // they run at 1,308 TFLOP/s, not 1,360.  (Loops: unrolled they are 4 KB of code that a unit runs once; 64 x 512
+            // tokens 178 us, not 159.)
             const bool whole_rows = MODE == kHeads && np == 1 && block * kRows + (warp & 3) * 32 + 31 < ql;
             if (whole_rows) {
+                const uint32_t keep = n > 0 ? 0xffffffffu : 0u;      // (O_t holds anything where there were no keys)
                 const uint32_t out = base + C::kOutOff + t * C::kOutBytes + (warp & 3) * 4096;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t ov[32];
-                    if (n > 0) {
-                        umma::tmem_ld32(o_col + c0, ov);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) ov[k] = 0u;
-                    }
-                    if (c0 % 64 == 0) {
-                        // what was stored from here before has been read
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        __syncwarp();
-                    }
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t oa[32], ob[32];
+                    umma::tmem_ld32(o_col + c0, oa);
+                    umma::tmem_ld32(o_col + c0 + 32, ob);
+                    // what was stored from here before has been read
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
                     umma::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<false>(__uint_as_float(ov[8 * k + 2 * e]) * f, __uint_as_float(ov[8 * k + 2 * e + 1]) * f);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(out + lane * 128 +
-                                                                               (((c0 / 8 + k) & 7) ^ (lane & 7)) * 16),
+                        for (int e = 0; e < 4; ++e) {
+                            const int q = 8 * (k & 3) + 2 * e;
+                            w[e] = keep & pack2<false>(__uint_as_float(k < 4 ? oa[q] : ob[q]) * f,
+                                                       __uint_as_float(k < 4 ? oa[q + 1] : ob[q + 1]) * f);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(out + lane * 128 + (k ^ (lane & 7)) * 16),
                                      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                                      : "memory");
                     }
-                    if (c0 % 64 == 32) {
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0)
-                            tensor_store_2d(&omap, out, (e1.x * p.g + head) * D + c0 - 32, e0.x + block * kRows + (warp & 3) * 32);
-                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        tensor_store_2d(&omap, out, (e1.x * p.g + head) * D + c0, e0.x + block * kRows + (warp & 3) * 32);
                 }
             } else
 #pragma unroll 1
