@@ -22,7 +22,7 @@
 //               columns
 //   warp 8      claims units, K tiles by TMA into a ring
 //   warps 9, 10 issue a tile's products each (one warp for both, waiting for the two
-//               tiles in a fixed order: one prompt of 32,768 tokens 4,893 us, not 4,718;
+//               tiles in a fixed order: one prompt of 32,768 tokens 4,893 us, not 4,705;
 //               one of 1 token 0.2 us less), and gather its rows where it is packed:
 //                 S_t = Q_t . K_j^T       M 128, N 128, K d
 //                 O_t (+)= P_t . V_j      M 128, N d, K 128 (P_t in TMEM)
