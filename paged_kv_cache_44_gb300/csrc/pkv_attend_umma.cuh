@@ -957,13 +957,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int np = e1.y, part = e1.z + (pair && t ? 1 : 0);
             const size_t row = (size_t)(e0.x + qi), hrow = row * p.Hq + e1.x * p.g + hh;
             const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+            // A row that sees no key here is zeros: its weights are, but 0 times a V value that is not finite is not (and
+            // O_t holds anything where there were no keys).
+            const bool unseen = l == 0.f;
             // Whole warps of rows leave by TMA, 64 columns at a time through shared memory: stored by the threads, a row
             // each, 32 lines per instruction, 64 x 512 tokens take 204 us in both directions, not 189; 32 columns at a time
             // they run at 1,308 TFLOP/s, not 1,360.  (Loops: unrolled they are 4 KB of code that a unit runs once; 64 x 512
             // tokens 178 us, not 159.)
             const bool whole_rows = MODE == kHeads && np == 1 && block * kRows + (warp & 3) * 32 + 31 < ql;
             if (whole_rows) {
-                const uint32_t keep = n > 0 ? 0xffffffffu : 0u;      // (O_t holds anything where there were no keys)
+                const uint32_t keep = unseen ? 0u : 0xffffffffu;
                 const uint32_t out = base + C::kOutOff + t * C::kOutBytes + (warp & 3) * 4096;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 64) {
@@ -996,13 +999,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t ov[32];
-                if (n > 0) {
-                    umma::tmem_ld32(o_col + c0, ov);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) ov[k] = 0u;
-                }
+                umma::tmem_ld32(o_col + c0, ov);
                 umma::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) ov[k] = unseen ? 0u : ov[k];
                 if (rv) {
                     if (!SHARED && np == 1) {
                         store_row32(static_cast<__nv_bfloat16*>(p.out) + hrow * D + c0, ov, f,
