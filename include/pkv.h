@@ -784,8 +784,9 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void
  * shares a block; a group that breaks a bound is reported
  * (PKV_DEVERR_QUERY_LEN) and decoded without sharing.  Groups that overlap
  * give unspecified results.  A sequence shorter than its group's shared tokens
- * sees its own length.  A block id outside [0, NB) is reported and its tokens
- * are absent, as in the decode.
+ * is decoded on its own, and shared tokens that no sequence sees may hold
+ * anything, NaN included.  A block id outside [0, NB) is reported and its
+ * tokens are absent, as in the decode.
  *
  * sharing (a pkv_sharing): PKV_SHARE_AUTO reads the shared blocks once where
  * that is estimated to be faster (by the bounds: sequences on their own would

@@ -366,9 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // where each sequence's own part begins, and the longest one, for the kernels behind this one
         int own = 0;
         for (int s = blockIdx.x * kThreads + tid; s < p.Tq; s += gridDim.x * kThreads) {
-            const int begin = shared_tokens(p, s);
+            // A member that ends inside the shared tokens is decoded on its own (what its rows give here is not used):
+            // tokens it does not see would weigh 0, but may hold what is not finite, or have never been written.
+            const int n = min(load_behind_wait(p.lens + s), p.max_ctx), whole = shared_tokens(p, s);
+            const int begin = n < whole ? 0 : whole;
             p.begin[s] = begin;
-            own = max(own, min(load_behind_wait(p.lens + s), p.max_ctx) - begin);
+            own = max(own, n - begin);
         }
         own = __reduce_max_sync(0xffffffffu, own);
         if (lane == 0 && own > 0) atomicMax(p.own_max, own);
@@ -828,11 +831,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 first = p.causal ? kl - ql + block * kRows / p.g : kl - 1;
                 pos = p.causal ? kl - ql + qi : kl - 1;
                 far = p.causal ? kl - ql + (block * kRows + kRows - 1) / p.g : kl - 1;
-            }
-            if constexpr (SHARED) {
-                // a member that ends inside the shared blocks sees its own tokens only
-                pos = rv ? min(__ldg(p.lens + e0.x + qi), kl) - 1 : kl - 1;
-                first = (int)__reduce_min_sync(0xffffffffu, (unsigned)max(pos + 1, 0)) - 1;
             }
             const int j0 = e1.w + (pair && t ? p.P : 0);         // the tile's first stage
             const bool flip = !(p.scale_log2 > 0.f);

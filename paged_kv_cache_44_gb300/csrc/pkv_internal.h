@@ -139,7 +139,7 @@ struct PromptParams {
     // of the Tq, whose first key_start[i] tokens lie in the blocks of the first one's table
     const int32_t* tables;    // [Tq][MB]
     const int32_t* lens;      // [Tq]
-    int32_t* begin;           // [Tq]: written: the tokens a sequence shares
+    int32_t* begin;           // [Tq]: written: the tokens it takes from its group (0: all on its own)
     int* own_max;             // raised to the most tokens a sequence has of its own (0 between calls)
     int MB, bs, NB, max_ctx;
 };
