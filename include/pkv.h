@@ -745,7 +745,8 @@ PKV_API pkv_status pkv_rotary_kv_write(const void* query, const void* key, const
  * [0, Tk), is skipped and reported (PKV_DEVERR_QUERY_LEN).  A V value that is
  * not finite may reach queries of the same sequence that see other keys but
  * not this one, by way of queries that do see it (their weight 0 times it); K
- * values do not, and a query that sees no key is zeros in any case.
+ * values do not, and a query that sees no key is zeros in any case.  Keys that
+ * no query of their sequence sees (behind every window) may hold anything.
  *
  * Few rows over many keys are split: partition_size 0 = library choice, -1 =
  * never, > 0 = that many keys (a multiple of 128); then `workspace` must hold

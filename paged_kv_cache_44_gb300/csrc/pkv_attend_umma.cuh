@@ -26,8 +26,8 @@
 //               one of 1 token 0.2 us less), and gather its rows where it is packed:
 //                 S_t = Q_t . K_j^T       M 128, N 128, K d
 //                 O_t (+)= P_t . V_j      M 128, N d, K 128 (P_t in TMEM)
-//   warp 11     V tiles, and Q tiles of one head, by TMA; zeroes the rows of a sequence's last tile that
-//               are other sequences' (0 times what they hold may be NaN)
+//   warp 11     V tiles, and Q tiles of one head, by TMA; zeroes rows that no query of the sequence sees
+//               (other sequences' in its last tile, those before every window: 0 times what they hold may be NaN)
 // A row's reference maximum m moves only when a stage's maximum exceeds it by
 // more than 2^8; O is then rescaled in TMEM.  Every exponent stays <= 2^8 and O
 // / l is the same softmax whatever m was.  P is rounded to bf16 (by 2^-8 of a
@@ -594,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (bad) break;
             const int n = count(pair, e2.z, e2.w);
+            // keys between the sinks and the first query's window: no query of the sequence sees them
+            const int hidden0 = p.sinks, hidden1 = !SHARED && p.window > 0 ? e0.w - e0.z - p.window + 1 : 0;
             BlockIds ids;
             if constexpr (SHARED) ids.start(p, e0.x, e0.w / p.bs, e1.w, pair ? p.P : 0);
             for (int j = 0; j < n; ++j, ++g) {
@@ -603,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const int key = stage_key(e1.w + turn(pair, e2.w, j), e2.x, e2.y);
-                // rows of the tile, in eighths (SHARED: a block or half of one) or counted, that hold something
+                // rows of the tile, in eighths (SHARED: a block or half of one) or counted, that hold something, and whether
+                // some of them are unseen
                 const int here = e0.w - key;
                 uint32_t there = 0xffu;
                 int pb = 0;
@@ -611,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pb = ids.stage(p, pair && j < 2 * e2.w ? j & 1 : 0);
                     there = __ballot_sync(0xffffffffu, pb >= 0);
                 }
-                const bool part = SHARED ? there != (p.bs == 16 ? 0xffu : 0xfu) : here < kTok;
+                const bool unseen = hidden0 < hidden1 && key < hidden1 && key + kTok > hidden0;
+                const bool part = SHARED ? there != (p.bs == 16 ? 0xffu : 0xfu) : here < kTok || unseen;
                 const uint32_t full = bar(kVFull, g % NV), landed = part ? bar(kTail, 0) : full;
                 if constexpr (SHARED) {
                     load_blocks<D>(p, &vmap, vtile(g), e1.x, pb, there, landed);
@@ -630,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t vb = vtile(g);
-                    for (int i = (SHARED ? 0 : here * 8) + lane; i < kTok * 8; i += 32) {
+                    for (int i = (SHARED || unseen ? 0 : here * 8) + lane; i < kTok * 8; i += 32) {
                         if (SHARED && ((there >> (i / 8 / p.bs)) & 1u)) continue;
+                        if (!SHARED && i < here * 8 && (key + i / 8 < hidden0 || key + i / 8 >= hidden1)) continue;
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h)
                             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + h * (kTok * 128) + i * 16), "r"(0u)

@@ -5,7 +5,7 @@ result, and rows that see nothing beside rows that do."""
 import pytest
 import torch
 
-from tests.test_gpu_prompt import call, inputs
+from tests.test_gpu_prompt import call, check, inputs
 from tests.test_gpu_shared import Case
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,23 @@ def test_prompt_rows_that_see_nothing(ql, kl, shape, part):
             assert (out[at:at + a - b] == 0).all()
             assert not torch.isfinite(out[at + a - b:at + a]).any()
             at += a
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 64), (12, 2, 128), (28, 4, 128), (3, 3, 64)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 3), (128, 128), (257, 130), (1000, 0)])
+@pytest.mark.parametrize("part", [0, 128, -1])
+@pytest.mark.parametrize("few", [True, False], ids=["few", "many"])
+def test_prompt_keys_behind_every_window(shape, window, sinks, part, few):
+    """Keys between the sinks and the first query's window: no query of the sequence sees them."""
+    ql, kl = ([5, 64, 1, 9], [2000, 700, 130, 9]) if few else ([5, 130, 300, 257], [2000, 1031, 777, 257])
+    q, k, v = inputs(ql, kl, *shape, seed=25)
+    clean = call(q, k, v, ql, kl, True, window, sinks, part=part)
+    check(clean, q, k, v, ql, kl, True, window, sinks, shape[2] ** -0.5)
+    for bad in BAD:
+        k2, v2, at = k.clone(), v.clone(), 0
+        for a, b in zip(ql, kl):
+            lo, hi = sinks, b - a - window + 1
+            if hi > lo:
+                k2[at + lo:at + hi], v2[at + lo:at + hi] = bad, bad
+            at += b
+        assert torch.equal(call(q, k2, v2, ql, kl, True, window, sinks, part=part), clean)
