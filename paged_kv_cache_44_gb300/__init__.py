@@ -899,6 +899,7 @@ def prompt_attention(out: torch.Tensor, query: torch.Tensor, key: torch.Tensor, 
         key_start, max_key_len = query_start, max_query_len
     if query_start.dtype != torch.int32 or key_start.dtype != torch.int32 or key_start.numel() != S + 1 or S < 0:
         raise ValueError("query_start and key_start must be int32 [S + 1]")
+    max_key_len = min(max_key_len, Tk)           # (a loose bound; partition_size > 0 lays its partitions out by it)
     if workspace is None:
         workspace = _own_workspace(stream, make_prompt_workspace, S, Tq, max_query_len, max_key_len, Hq, Hkv, d, window,
                                    num_sinks, partition_size, device=query.device)

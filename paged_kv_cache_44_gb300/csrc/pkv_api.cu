@@ -932,18 +932,15 @@ namespace {
 // Key stages of the longest tile of a prompt: those of the sinks and of what
 // the windows of one group of query blocks span.
 int prompt_stages(int max_k, int g, int window, int sinks) {
-    const int all = (max_k + kPromptStage - 1) / kPromptStage;
+    const int all = (int)((max_k - 1LL + kPromptStage) / kPromptStage);      // (a bound may be as large as an int)
     if (window <= 0) return all;
     const long long span = (long long)window - 1 + prompt_group(g) * kPromptStage + kPromptStage - 1;
-    const long long n = (span + kPromptStage - 1) / kPromptStage + (sinks + kPromptStage - 1) / kPromptStage;
+    const long long n = (span + kPromptStage - 1) / kPromptStage + (sinks - 1LL + kPromptStage) / kPromptStage;
     return n < all ? (int)n : all;
 }
 
-PrefillPlan plan_prompt(int Tq, int Hq, int d, int stages, int P) {
-    PrefillPlan pl = plan_prefill(Tq, Hq, d, stages * kPromptStage, P * kPromptStage);
-    pl.P = P;
-    return pl;
-}
+// (stages and P in stages, not tokens)
+PrefillPlan plan_prompt(int Tq, int Hq, int d, int stages, int P) { return plan_prefill(Tq, Hq, d, stages, P); }
 
 bool prompt_shape_ok(int S, int Tq, int max_q, int max_k, int Hq, int Hkv, int d, int req) {
     return S >= 0 && S <= 65535 && Tq >= 0 && max_q >= 0 && max_k >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
@@ -992,6 +989,7 @@ size_t pkv_prompt_workspace_size(int S, int num_query_tokens, int max_query_len,
     if (!prompt_shape_ok(S, num_query_tokens, max_query_len, max_key_len, Hq, Hkv, d, partition_size) || window < 0 ||
         num_sinks < 0)
         return 0;
+    max_query_len = min(max_query_len, num_query_tokens);
     clamp_window(max_key_len, window, num_sinks);
     const int stages = prompt_stages(max_key_len, Hq / Hkv, window, num_sinks);
     const int P = resolve_prompt_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, stages, partition_size, SIZE_MAX);
@@ -1030,6 +1028,10 @@ pkv_status pkv_prompt_attention(void* out, const void* query, const void* key, c
     }
     if (!aligned16(out) || (reinterpret_cast<uintptr_t>(query_start) & 3u) || (reinterpret_cast<uintptr_t>(key_start) & 3u))
         return PKV_ERR_INVALID_ARG;
+    // bounds may be loose: no sequence has more queries or keys than there are (but partitions that the caller asks
+    // for take the workspace that it was told for its bound)
+    max_query_len = min(max_query_len, num_query_tokens);
+    if (partition_size == 0) max_key_len = min(max_key_len, num_key_tokens);
     clamp_window(max_key_len, window, num_sinks);
     const int stages = prompt_stages(max_key_len, Hq / Hkv, window, num_sinks);
     const int P = resolve_prompt_partition(S, num_query_tokens, max_query_len, Hq, Hkv, d, stages, partition_size,
@@ -1073,7 +1075,7 @@ struct SharedPlan {
 };
 SharedPlan plan_shared(int S, int Hq, int d, int max_ctx, int max_shared, int pre, int P) {
     SharedPlan sp{};
-    const int stages = (max_shared + kPromptStage - 1) / kPromptStage;
+    const int stages = (int)((max_shared - 1LL + kPromptStage) / kPromptStage);
     sp.pre = pre;
     sp.first_own = pre > 0 ? (stages + pre - 1) / pre : 1;
     sp.own = make_plan(S, Hq, d, max_ctx, P);
@@ -1090,10 +1092,10 @@ SharedPlan plan_shared(int S, int Hq, int d, int max_ctx, int max_shared, int pr
 // Stages per partition of the shared tokens: the number of equal partitions
 // with the least rounds of units, a unit's fixed cost counted as 3 stages.
 int resolve_shared_prefix(int G, int max_group, int g, int Hkv, int max_shared, int req) {
-    const int stages = (max_shared + kPromptStage - 1) / kPromptStage;
+    const int stages = (int)((max_shared - 1LL + kPromptStage) / kPromptStage);
     if (req == -1) return 0;
     if (req > 0) {
-        const int p = (req + kPromptStage - 1) / kPromptStage;
+        const int p = (int)((req - 1LL + kPromptStage) / kPromptStage);
         return p < stages ? p : 0;
     }
     // a group of one tile pairs its partitions: two of them are a unit
