@@ -790,9 +790,12 @@ PKV_API pkv_status pkv_prompt_attention(void* out, const void* query, const void
  * tokens are absent, as in the decode.
  *
  * sharing (a pkv_sharing): PKV_SHARE_AUTO reads the shared blocks once where
- * that is estimated to be faster (by the bounds: sequences on their own would
- * read 256 MB or more of them again) and otherwise decodes every sequence on
- * its own, without a look at the groups; PKV_SHARE_ALWAYS in any case.
+ * that is estimated to be faster, and otherwise decodes every sequence on its
+ * own, without a look at the groups; PKV_SHARE_ALWAYS in any case.  The estimate
+ * is by the bounds: sequences on their own would read 256 MB or more again if
+ * there were G groups of max_group_size (at most S sequences) that share
+ * max_shared_len.  So a group that shares nothing counts too: sequences before
+ * the first group and behind the last are better in none.
  * partition_size: as in the decode, for the shared tokens (rounded up to 128)
  * and the others alike.  `workspace` must hold
  * pkv_decode_shared_workspace_size(...) bytes, its first 256 zero before first

@@ -1122,15 +1122,20 @@ bool shared_shape_ok(int S, int G, int Hq, int Hkv, int d, int bs, int max_ctx, 
 constexpr int kMaxOwnParts = 96;
 
 // Whether the shared tokens get a launch of their own: where sequences on
-// their own would read them from 256 MB on again (by the bounds).  Two more
+// their own would read them from 256 MB on again.  By the bounds, which is all
+// that the host has: G groups of max_group members, but no more members than
+// sequences.  A group that shares nothing counts as the others do.  Two more
 // launches take 15-20 us, about what HBM and L2 take for that: 64 sequences
 // sharing 2,048 tokens of 4 heads of 128 (264 MB) 42 us and 45 on their own,
 // 128 of them 48 and 64; 256 sharing 512 (267 MB) 64.5 and 61.4; 100 of 256
-// sharing 1,024 (207 MB, read from L2 while HBM is the bound) 342 and 325.
+// sharing 1,024 (207 MB, read from L2 while HBM is the bound) 353 and 332 (by
+// the bounds 207 MB where they are the only group, 415 with the others as a
+// second one).
 constexpr long long kShareBytes = 256LL << 20;
-bool shares(int G, int max_shared, int max_group, int Hkv, int d, int bs, int sharing) {
+bool shares(int S, int G, int max_shared, int max_group, int Hkv, int d, int bs, int sharing) {
     if (G < 1 || max_shared < bs || max_group < 1) return false;
-    return sharing == PKV_SHARE_ALWAYS || (long long)G * (max_group - 1) * max_shared * Hkv * d * 4 >= kShareBytes;
+    const long long again = min((long long)G * (max_group - 1), (long long)S - 1);
+    return sharing == PKV_SHARE_ALWAYS || again * max_shared * Hkv * d * 4 >= kShareBytes;
 }
 
 // Sequences on their own, as the windowed decode with everything in its window:
@@ -1178,7 +1183,7 @@ size_t pkv_decode_shared_workspace_size(int S, int G, int Hq, int Hkv, int d, in
     const size_t plain = as_window(S, Hq, Hkv, d, bs, max_context_len, partition_size)
                              ? pkv_decode_window_workspace_size(S, Hq, Hkv, d, bs, max_context_len, max_context_len, 0, 0)
                              : pkv_decode_workspace_size(S, Hq, Hkv, d, bs, max_context_len, partition_size);
-    if (!shares(G, max_shared_len, max_group_size, Hkv, d, bs, sharing)) return plain;
+    if (!shares(S, G, max_shared_len, max_group_size, Hkv, d, bs, sharing)) return plain;
     return max(plain, choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size,
                                     SIZE_MAX).bytes);
 }
@@ -1201,7 +1206,7 @@ pkv_status pkv_paged_attention_decode_shared(void* out, const void* query, pkv_d
     if ((reinterpret_cast<uintptr_t>(group_start) & 3u) || (reinterpret_cast<uintptr_t>(shared_lens) & 3u))
         return PKV_ERR_INVALID_ARG;
     const size_t room = workspace_room(workspace, workspace_bytes);
-    const bool share = shares(G, max_shared_len, max_group_size, Hkv, d, bs, sharing);
+    const bool share = shares(S, G, max_shared_len, max_group_size, Hkv, d, bs, sharing);
     SharedPlan sp{};
     if (share)
         sp = choose_shared(S, G, Hq, Hkv, d, bs, max_context_len, max_shared_len, max_group_size, partition_size, room);
