@@ -28,7 +28,8 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 // Loads that stay behind pdl_wait().  __ldg promises data that nothing writes
 // while the kernel runs, so the compiler may move it up, past the wait too,
 // where the address does not depend on an earlier load: a length or a start that
-// the previous kernel of the stream writes would then be read too early.
+// the previous kernel of the stream writes would then be read too early.  (What
+// stands behind a branch on such a word, tables and rows, stays where it is.)
 __device__ __forceinline__ int32_t load_behind_wait(const int32_t* p) {
     int32_t v;
     asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");

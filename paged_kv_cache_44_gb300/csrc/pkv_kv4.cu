@@ -147,7 +147,7 @@ __device__ __forceinline__ bool octet_of(const Kv4Params& p, Octet& o) {
     o.i0 = 8LL * blockIdx.x;
     o.slot = -1;
     if (lane < 8 && o.i0 + lane < p.T) {
-        o.slot = __ldg(p.slots + o.i0 + lane);
+        o.slot = load_behind_wait(p.slots + o.i0 + lane);
         if (o.slot >= (long long)p.NB * p.bs) {
             if (row == 0) report(p.err, PKV_DEVERR_SLOT);
             o.slot = -1;

@@ -424,10 +424,11 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(DecodeParams p, cons
     int lo = 0, hi = p.S;                      // largest s with query_start[s] <= tq
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (query_start[mid] <= tq) lo = mid; else hi = mid;
+        if (load_behind_wait(query_start + mid) <= tq) lo = mid; else hi = mid;
     }
     const int s = lo;
-    const int n = p.context_lens[s], q0 = query_start[s], ql = query_start[s + 1] - q0;
+    const int n = load_behind_wait(p.context_lens + s), q0 = load_behind_wait(query_start + s);
+    const int ql = load_behind_wait(query_start + s + 1) - q0;
     if (n < 0 || n > p.max_ctx || ql < 0 || ql > n || ql > max_q || q0 < 0 || q0 + ql > T || tq >= q0 + ql)
         return;                                // the sequence the main kernel skipped
     const int kvh = h / p.g, row = (tq - q0) * p.g + (h - kvh * p.g);

@@ -56,9 +56,9 @@ __device__ __forceinline__ bool qtile_of(const DecodeParams& p, const int32_t* q
     const int r2 = (int)(rem - (unsigned long long)x.s * p.Hkv * rt_max);
     x.kvh = r2 / rt_max;
     x.rt = r2 - x.kvh * rt_max;
-    const int n = __ldg(p.context_lens + x.s);
-    x.q0 = __ldg(query_start + x.s);
-    x.ql = __ldg(query_start + x.s + 1) - x.q0;
+    const int n = load_behind_wait(p.context_lens + x.s);
+    x.q0 = load_behind_wait(query_start + x.s);
+    x.ql = load_behind_wait(query_start + x.s + 1) - x.q0;
     if (n < 0 || n > p.max_ctx || x.ql < 0 || x.ql > n || x.ql > max_q || x.q0 < 0 || x.q0 + x.ql > T) {
         if (x.part == 0 && r2 == 0) report(p.err, PKV_DEVERR_QUERY_LEN);
         return false;

@@ -59,7 +59,7 @@ __device__ __forceinline__ bool unit_of(const DecodeParams& p, unsigned long lon
     const int set = r2 - x.kvh * nsets;
     x.h0 = x.kvh * p.g + set * kHeadsPerUnit;
     x.nh = min(kHeadsPerUnit, p.g - set * kHeadsPerUnit);
-    int n = SUFFIX ? load_behind_wait(p.context_lens + x.s) : __ldg(p.context_lens + x.s);
+    int n = load_behind_wait(p.context_lens + x.s);
     if (n < 0 || n > p.max_ctx) {
         if (!in_a && idx == 0 && r2 == 0) report(p.err, PKV_DEVERR_CONTEXT_LEN);
         n = n < 0 ? 0 : p.max_ctx;
