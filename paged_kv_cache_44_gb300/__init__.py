@@ -943,9 +943,10 @@ def paged_attention_decode_shared(out: torch.Tensor, query: torch.Tensor, key_ca
     """paged_attention_decode (bf16) of sequences in groups whose first blocks
     are the same: group i is the sequences group_start[i] .. group_start[i+1]
     (int32 [G+1]), and their first shared_lens[i] tokens (int32 [G], whole
-    blocks) are read once, through the first one's table.  max_shared_len and
-    max_group_size (host) bound them.  sharing: "auto" (where little would be
-    read again, every sequence on its own) or "always"."""
+    blocks) are read once, through the first one's table; a member shorter than
+    them is decoded on its own.  max_shared_len and max_group_size (host) bound
+    them.  sharing: "auto" (where, by the bounds, little would be read again,
+    every sequence on its own) or "always"."""
     if sharing not in SHARING:
         raise ValueError(f"sharing must be one of {sorted(SHARING)}")
     S, Hq, d = shape = query.shape

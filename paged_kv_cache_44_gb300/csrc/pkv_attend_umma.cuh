@@ -29,9 +29,10 @@
 //   warp 11     V tiles, and Q tiles of one head, by TMA; zeroes rows that no query of the sequence sees
 //               (other sequences' in its last tile, those before every window: 0 times what they hold may be NaN)
 // A row's reference maximum m moves only when a stage's maximum exceeds it by
-// more than 2^8; O is then rescaled in TMEM.  Every exponent stays <= 2^8 and O
-// / l is the same softmax whatever m was.  P is rounded to bf16 (by 2^-8 of a
-// weight at most): the tensor cores take 16-bit operands; sums stay in fp32.
+// more than 8 (log2 units); O is then rescaled in TMEM.  Every weight stays <=
+// 2^8 and O / l is the same softmax whatever m was.  P is rounded to bf16 (by
+// 2^-8 of a weight at most): the tensor cores take 16-bit operands; sums stay in
+// fp32.
 //
 // Units are numbered longest first: query blocks from the last to the first
 // over all sequences, so the end of a launch is made of short ones.  A block

@@ -27,8 +27,8 @@
 //               bf16 over the first half of S_j's columns, running sum; at
 //               the end O / l, or the partition's (m, l, O).
 // The reference maximum m of a row changes only when a stage's maximum
-// exceeds it by more than 2^8; O and l are then rescaled (O in TMEM, after
-// the previous product has completed).  Every exponent stays <= 2^8, and the
+// exceeds it by more than 8 (log2 units); O and l are then rescaled (O in TMEM,
+// after the previous product has completed).  Every weight stays <= 2^8, and the
 // final O / l is the same softmax whatever reference was used.
 #include <cuda.h>
 #include <cuda_bf16.h>

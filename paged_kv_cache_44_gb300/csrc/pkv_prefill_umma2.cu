@@ -34,9 +34,9 @@
 //               (m, l, O).  Two groups keep two softmax warps on every SM
 //               sub-partition, so one fills the other's waits.
 // The reference maximum m of a row changes only when a stage's maximum
-// exceeds it by more than 2^8; O and l are then rescaled (O in TMEM: the
-// previous product has completed, since S of this stage was issued after
-// it).  Every exponent stays <= 2^8, and the final O / l is the same softmax
+// exceeds it by more than 8 (log2 units); O and l are then rescaled (O in TMEM:
+// the previous product has completed, since S of this stage was issued after
+// it).  Every weight stays <= 2^8, and the final O / l is the same softmax
 // whatever reference was used.
 #include <cuda.h>
 #include <cuda_bf16.h>
